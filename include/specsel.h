@@ -275,6 +275,144 @@ spec_status spec_shortlist_topk(const uint16_t *hidden, int64_t cols, int64_t d,
                                 const void *spack, int64_t rows, const int32_t *id_map, int32_t k,
                                 uint16_t *logits, uint16_t *out_vals, int32_t *out_ids);
 
+/* ---- Paged key/value cache of the target (and drafter) -------------------
+ *
+ * The verify pass ("A drafter inside the artifact", Ignis DFlash2 page, "How
+ * it works", first paragraph) scores every lane's anchor and drafts in one
+ * pass over that lane's cached keys and values; attention keeps every
+ * column's keys.  These entry points hold that cache in pages and serve any
+ * chunk of new tokens per lane: one (decoding), an anchor and its drafts
+ * (verifying), or a piece of a prompt.  The pages give no layout; the one
+ * below is this library's.
+ *
+ * A step is spec_paged_plan (pages, block tables, positions and slots from the
+ * lengths), spec_paged_store (the new keys and values into their slots) and
+ * spec_paged_attention.  Lengths stay in device memory: nothing waits for the
+ * host, and the three calls can be captured in a CUDA graph (the batch's
+ * buffers have fixed sizes; tokens past the step's total are left alone). */
+#define SPEC_BF16 0
+#define SPEC_F16 1
+#define SPEC_PAGED_MAX_LANES 4096
+
+/* Keys and values of one layer: element (page, token, head, i) of k lies at
+ * k + page*k_strides[0] + token*k_strides[1] + head*k_strides[2] + i (strides in
+ * elements; any order of the first three dimensions), and so for v.  Base
+ * addresses are 16-byte aligned and strides non-negative multiples of 8
+ * elements below 2^39.  A slot is page * page_size + token. */
+typedef struct {
+    void *k, *v;            /* device, 16-bit elements of type dtype */
+    int64_t k_strides[3], v_strides[3];
+    int64_t pages;          /* 1 .. 2^31-1 */
+    int32_t page_size;      /* tokens a page, >= 1 (attention: a power of two >= 8) */
+    int32_t heads;          /* key/value heads, >= 1 */
+    int32_t head_dim;       /* a multiple of 8, at most 256 (attention: 64, 128 or 256) */
+    int32_t dtype;          /* SPEC_BF16 or SPEC_F16 */
+} spec_paged_cache;
+
+/* One step's lanes.  The plan reads the first group and writes the second;
+ * attention reads block_table, cu_new and seq_lens only (the rest may be NULL
+ * there).  All device memory of the caller, int32 unless noted. */
+typedef struct {
+    const int32_t *context_lens;   /* [lanes] tokens already cached (negative: 0) */
+    const int32_t *new_lens;       /* [lanes] new tokens of this step, 0 allowed (negative: 0) */
+    const int32_t *held;           /* [lanes] pages the lane's table row holds already */
+    int32_t *block_table;          /* [lanes][max_pages] page of each page_size tokens; rows are contiguous */
+    int32_t *cu_new;               /* [lanes+1] where each lane's new tokens start; the last is their total */
+    int32_t *seq_lens;             /* [lanes] context + new */
+    int32_t *held_out;             /* [lanes] pages held after the step */
+    int32_t *positions;            /* [tokens] position of each new token in its lane; 0 past the total */
+    int64_t *slots;                /* int64 [tokens] slot of each new token; -1 without a page and past the total */
+    int32_t *info;                 /* [4] new tokens; cursor after the step; pages that were wanting;
+                                      lanes whose tokens exceed max_pages pages */
+    int64_t lanes;                 /* 0 .. SPEC_PAGED_MAX_LANES */
+    int64_t max_pages;             /* entries of a table row, 1 .. 2^31-1 */
+    int64_t tokens;                /* size of positions and slots, >= 0 */
+    int32_t page_size;
+} spec_paged_batch;
+
+/* Plan a step: cu_new, seq_lens, positions; the pages each lane lacks for
+ * seq_lens tokens, taken from free_pages[cursor ..] in lane order and appended to
+ * its table row; the slot of every new token.
+ *   free_pages int32 [num_free] (may be NULL when num_free == 0); cursor: device
+ *              int32 [1], the pages of the list used up before (NULL: 0).
+ * When the list runs out, lanes take what is left in order, and tokens without
+ * a page get slot -1; nothing is read or written out of range, and info tells.
+ * Outputs must not alias inputs (keep two held and info buffers and swap them
+ * from step to step); block_table is updated in place, only at entries the
+ * step adds, so repeating a call repeats its results.
+ * One launch.  lanes == 0 still writes cu_new[0], the padding and info. */
+spec_status spec_paged_plan(const spec_paged_batch *batch, const int32_t *free_pages, int64_t num_free,
+                            const int32_t *cursor);
+
+/* Store new keys and values: token t's k and v (element (t, head, i) at
+ * k + t*k_token_stride + head*k_head_stride + i; 16-byte aligned, strides
+ * non-negative multiples of 8 elements) go to slot slots[t] of the cache.
+ * Tokens whose slot lies outside [0, pages*page_size) are skipped.  Two tokens
+ * must not share a slot. */
+spec_status spec_paged_store(const void *k, const void *v, int64_t tokens, int64_t k_token_stride,
+                             int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                             const int64_t *slots, const spec_paged_cache *cache);
+
+/* Attention of every lane's new tokens over its cached keys and values, causal:
+ * new token i of a lane (position p = seq_len - new + i) attends keys
+ * max(0, p - window + 1) .. p (window 0: all keys up to p), which must be in
+ * the cache already (spec_paged_store).  Query head h reads key/value head
+ * h / (heads_q / cache->heads).
+ *   out[t][h] = sum_j w_j v_j,  w = softmax(scale * q.k_j),
+ *   lse[t][h] = log sum_j exp(scale * q.k_j).
+ *   q         cache->dtype, element (t, h, i) at q + t*q_token_stride + h*q_head_stride + i
+ *             (16-byte aligned, strides non-negative multiples of 8), t < tokens;
+ *   batch     block_table, cu_new, seq_lens, lanes, max_pages, page_size; row t of q belongs
+ *             to the lane with cu_new[lane] <= t < cu_new[lane+1];
+ *   scale     positive and finite, usually 1 / sqrt(head_dim);
+ *   max_new   the longest chunk to expect: a hint for the choice of tiles, results do not
+ *             depend on it;
+ *   out       cache->dtype, contiguous [tokens][heads_q][head_dim], 16-byte aligned;
+ *   lse       fp32 [tokens][heads_q], or NULL;
+ *   workspace device, 16-byte aligned, spec_paged_attention_workspace() bytes, zeroed once before
+ *             its first use; calls that may overlap on the GPU need one each.
+ * Rows of q past cu_new[lanes] are left alone.  A row with no key in reach (a
+ * seq_len below the chunk) gets out = 0 and lse = -inf.  What the cache holds
+ * past a lane's last position or before its window, NaN included, does not
+ * matter; values at positions inside seq_len must be finite.  Table entries outside
+ * [0, pages) read as zero keys and values.
+ * The scores and their sums are fp32; the weights w enter the second product
+ * rounded to dtype, unnormalised; out is rounded once. */
+spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
+                                 int64_t q_head_stride, const spec_paged_cache *cache, const spec_paged_batch *batch,
+                                 float scale, int64_t window, int64_t max_new, void *out, float *lse,
+                                 void *workspace, int64_t workspace_bytes);
+
+/* Bytes of workspace spec_paged_attention needs on the current device, for any
+ * sizes; a negative status on failure. */
+int64_t spec_paged_attention_workspace(void);
+
+/* Penalties, biases and grammar masks on logits, before they are verified or
+ * sampled: logits bf16 [lanes][cols][V] (any 2-byte alignment) -> out, the same layout.
+ * Column j of a lane predicts the token after the lane's history and its first
+ * j drafts.  For each token t, in fp32, rounded once to bf16:
+ *   seen in the prompt, the output or drafts[0..j-1]:  x = x > 0 ? x / r : x * r;
+ *   n = its count in the output and drafts[0..j-1]:    x -= f * n + p * (n > 0);
+ *   the lane's biases for t are added;
+ *   t masked out by the column's grammar:              x = -inf.
+ *   history      int32 [lanes][history_stride]: the first prompt_lens[l] ids are the prompt,
+ *                those up to history_lens[l] the output (lengths are cut to the stride);
+ *                NULL (with both lengths): no history;
+ *   drafts       int32 [lanes][cols-1], or NULL: no drafts counted;
+ *   penalties    fp32 [lanes][3]: r > 0 (1: none), f, p; or NULL: none;
+ *   bias_ids, bias_vals   int32, fp32 [lanes][max_bias], the first bias_lens[l] in use; or all NULL;
+ *                equal ids of a lane add up (in no fixed order);
+ *   mask         uint32 [mask_count][(V+31)/32]: bit t%32 of word t/32 set: t is allowed; mask_rows int32
+ *                [lanes*cols]: the column's row of mask, outside [0, mask_count): no mask; or both NULL.
+ * Ids outside [0, V) are ignored.  out may be logits itself (in place), and
+ * must not overlap it otherwise.  1 <= cols <= SPEC_MAX_GAMMA + 1. */
+spec_status spec_logits_process(const uint16_t *logits, int64_t lanes, int32_t cols, int64_t V,
+                                const int32_t *history, int64_t history_stride, const int32_t *prompt_lens,
+                                const int32_t *history_lens, const int32_t *drafts, const float *penalties,
+                                const int32_t *bias_ids, const float *bias_vals, int64_t max_bias,
+                                const int32_t *bias_lens, const uint32_t *mask, int64_t mask_count,
+                                const int32_t *mask_rows, uint16_t *out);
+
 /* Which streaming kernel runs a round.  All compute the same results (every
  * output is the unique exact answer); they differ only in speed:
  *   SPEC_KERNEL_GROUPMAX -- two phases in one launch.  The stream keeps only

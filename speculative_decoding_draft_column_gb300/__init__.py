@@ -31,6 +31,9 @@ __all__ = [
     "spec_set_stream", "spec_get_stream", "spec_reserve", "spec_release", "spec_last_error",
     "spec_launch_count", "spec_device_status", "topk", "topk_mapped", "verify", "round_step", "EXPORTS",
     "spec_shortlist_pack", "spec_shortlist_logits", "spec_shortlist_topk",
+    "SPEC_BF16", "SPEC_F16", "SPEC_PAGED_MAX_LANES", "PagedCache", "PagedBatch", "spec_paged_plan", "spec_paged_store",
+    "spec_paged_attention", "spec_paged_attention_workspace", "new_attention_workspace", "spec_logits_process",
+    "paged_attention", "process_logits",
 ]
 
 SPEC_OK, SPEC_ERR_ARG, SPEC_ERR_ALLOC, SPEC_ERR_CUDA = 0, -1, -2, -3
@@ -71,6 +74,11 @@ _SIGS = {
     "spec_shortlist_pack": [_p, _p, _i64, _i64, _p, _p],
     "spec_shortlist_logits": [_p, _i64, _i64, _p, _p, _i64, _p],
     "spec_shortlist_topk": [_p, _i64, _i64, _p, _p, _i64, _p, _i32, _p, _p, _p],
+    "spec_paged_plan": [_p, _p, _i64, _p],
+    "spec_paged_store": [_p, _p, _i64, _i64, _i64, _i64, _i64, _p, _p],
+    "spec_paged_attention": [_p, _i64, _i32, _i64, _i64, _p, _p, ctypes.c_float, _i64, _i64, _p, _p, _p, _i64],
+    "spec_paged_attention_workspace": [],
+    "spec_logits_process": [_p, _i64, _i32, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _i64, _p, _p, _i64, _p, _p],
 }
 EXPORTS = tuple(_SIGS)
 for _name, _args in _SIGS.items():
@@ -80,6 +88,7 @@ for _name, _args in _SIGS.items():
 lib.spec_get_stream.restype = ctypes.c_void_p
 lib.spec_last_error.restype = ctypes.c_char_p
 lib.spec_launch_count.restype = ctypes.c_int64
+lib.spec_paged_attention_workspace.restype = ctypes.c_int64
 
 
 class SpecError(RuntimeError):
@@ -418,3 +427,10 @@ def round_step(draft_logits, k: int, target_logits, drafts):
     com = torch.empty((lanes, gamma + 1), dtype=torch.int32, device=dev)
     spec_round(draft_logits, cols, V, k, vals, ids, target_logits, drafts, lanes, gamma, acc, com)
     return vals, ids, acc, com
+
+
+# the paged cache and the logits rules (they use the checks above)
+from .paged import (  # noqa: E402
+    SPEC_BF16, SPEC_F16, SPEC_PAGED_MAX_LANES, PagedBatch, PagedCache, new_attention_workspace, paged_attention,
+    process_logits, spec_logits_process, spec_paged_attention, spec_paged_attention_workspace, spec_paged_plan,
+    spec_paged_store)

@@ -8,7 +8,7 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SRC = os.path.join(CSRC, "specsel.cu")
+SRCS = [os.path.join(CSRC, f) for f in ("specsel.cu", "paged.cu")]
 HDR = os.path.join(ROOT, "include", "specsel.h")
 LIB = os.path.join(PKG, "libspecsel.so")
 
@@ -26,9 +26,9 @@ def nvcc() -> str:
     return p
 
 
-def command(out: str = LIB, src: str = SRC, extra: tuple[str, ...] = ()) -> list[str]:
-    return [nvcc(), "-O3", "-std=c++17", ARCH, "-lineinfo", "-Xcompiler", "-fPIC", "-shared",
-            "-cudart", "shared", "-I", os.path.join(ROOT, "include"), "-I", CSRC, *extra, "-o", out, src]
+def command(out: str, srcs: list[str], extra: tuple[str, ...] = ()) -> list[str]:
+    return [nvcc(), "-O3", "-std=c++17", ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
+            "-cudart", "shared", "-I", os.path.join(ROOT, "include"), "-I", CSRC, *extra, "-o", out, *srcs]
 
 
 def stale(out: str = LIB) -> bool:
@@ -40,9 +40,16 @@ def stale(out: str = LIB) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile the sources in parallel, then link."""
     if force or stale():
-        cmd = command()
+        objs = [os.path.splitext(src)[0] + ".o" for src in SRCS]
+        cmds = [command(o, [src], ("-c",)) for src, o in zip(SRCS, objs)]
         if verbose:
-            print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
+            print("\n".join(" ".join(c) for c in cmds), flush=True)
+        procs = [subprocess.Popen(c) for c in cmds]
+        codes = [p.wait() for p in procs]
+        for cmd, rc in zip(cmds, codes):
+            if rc != 0:
+                raise subprocess.CalledProcessError(rc, cmd)
+        subprocess.run(command(LIB, objs, ("-shared",)), check=True)
     return LIB

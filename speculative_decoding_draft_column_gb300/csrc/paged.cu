@@ -1,0 +1,276 @@
+// libspecsel: the paged key/value cache (plan of a step, store, attention of a
+// chunk of new tokens) and the rules applied to logits -- argument checks,
+// launches and the C ABI.
+
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <mutex>
+
+#include "specsel.h"
+#include "common.cuh"
+#include "paged.cuh"
+#include "attention.cuh"
+#include "logits_rules.cuh"
+#include "host.h"
+
+using host::cuda_fail;
+using host::fail;
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+struct Device {
+    bool init = false;
+    int sms = 0;
+};
+
+std::mutex g_paged_mu;
+Device g_devices[kMaxDevices];
+
+spec_status device(Device **out)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (dev < 0 || dev >= kMaxDevices) return fail(SPEC_ERR_CUDA, "device ordinal %d unsupported", dev);
+    Device &d = g_devices[dev];
+    std::lock_guard<std::mutex> lock(g_paged_mu);
+    if (!d.init) {
+        e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+        e = cudaFuncSetAttribute(paged::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 2 * (SPEC_PAGED_MAX_LANES + 1) * 8);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+        d.init = true;
+    }
+    *out = &d;
+    return SPEC_OK;
+}
+
+bool misaligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+constexpr int64_t kMaxStride = 1ll << 39;
+
+bool bad_stride(int64_t s) { return s < 0 || s >= kMaxStride || s % 8 != 0; }
+
+template <typename K, typename A>
+spec_status launch(K kernel, dim3 grid, unsigned block, size_t smem, const A &a)
+{
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = host::stream();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+    if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
+    host::count_launch();
+    return SPEC_OK;
+}
+
+spec_status check_cache(const spec_paged_cache *c)
+{
+    if (!c || !c->k || !c->v) return fail(SPEC_ERR_ARG, "cache: null pointer");
+    if (c->dtype != SPEC_BF16 && c->dtype != SPEC_F16) return fail(SPEC_ERR_ARG, "cache: unknown dtype %d", c->dtype);
+    if (misaligned(c->k, 16) || misaligned(c->v, 16))
+        return fail(SPEC_ERR_ARG, "cache: keys and values must be 16-byte aligned");
+    if (c->pages < 1 || c->pages > INT32_MAX) return fail(SPEC_ERR_ARG, "cache: pages = %lld", (long long)c->pages);
+    if (c->page_size < 1) return fail(SPEC_ERR_ARG, "cache: page_size = %d < 1", c->page_size);
+    if (c->heads < 1) return fail(SPEC_ERR_ARG, "cache: heads = %d < 1", c->heads);
+    if (c->head_dim < 8 || c->head_dim > 256 || c->head_dim % 8 != 0)
+        return fail(SPEC_ERR_ARG, "cache: head_dim = %d, need a multiple of 8 up to 256", c->head_dim);
+    for (int i = 0; i < 3; ++i)
+        if (bad_stride(c->k_strides[i]) || bad_stride(c->v_strides[i]))
+            return fail(SPEC_ERR_ARG, "cache: strides must be non-negative multiples of 8 elements below 2^39");
+    return SPEC_OK;
+}
+
+spec_status check_batch(const spec_paged_batch *b)
+{
+    if (!b) return fail(SPEC_ERR_ARG, "batch: null pointer");
+    if (b->lanes < 0 || b->lanes > SPEC_PAGED_MAX_LANES)
+        return fail(SPEC_ERR_ARG, "batch: lanes = %lld outside [0, %d]", (long long)b->lanes, SPEC_PAGED_MAX_LANES);
+    if (b->max_pages < 1 || b->max_pages > INT32_MAX)
+        return fail(SPEC_ERR_ARG, "batch: max_pages = %lld", (long long)b->max_pages);
+    if (b->page_size < 1) return fail(SPEC_ERR_ARG, "batch: page_size = %d < 1", b->page_size);
+    return SPEC_OK;
+}
+
+}  // namespace
+
+namespace host {
+
+cudaError_t take_paged_timeouts(unsigned int *flags)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(flags, g_wait_timeouts, sizeof *flags);
+    if (e != cudaSuccess || *flags == 0) return e;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof zero);
+}
+
+}  // namespace host
+
+extern "C" {
+
+spec_status spec_paged_plan(const spec_paged_batch *batch, const int32_t *free_pages, int64_t num_free,
+                            const int32_t *cursor)
+{
+    host::clear_error();
+    spec_status st = check_batch(batch);
+    if (st != SPEC_OK) return st;
+    const spec_paged_batch &b = *batch;
+    if (b.tokens < 0) return fail(SPEC_ERR_ARG, "batch: tokens = %lld < 0", (long long)b.tokens);
+    if (num_free < 0 || num_free > INT32_MAX) return fail(SPEC_ERR_ARG, "num_free = %lld", (long long)num_free);
+    if (!b.cu_new || !b.info ||
+        (b.lanes > 0 && (!b.context_lens || !b.new_lens || !b.held || !b.block_table || !b.seq_lens || !b.held_out)) ||
+        (b.tokens > 0 && (!b.positions || !b.slots)) || (num_free > 0 && !free_pages))
+        return fail(SPEC_ERR_ARG, "null pointer");
+    const void *words[] = {b.context_lens, b.new_lens, b.held,      b.block_table, b.cu_new,   b.seq_lens,
+                           b.held_out,     b.info,     b.positions, free_pages,    cursor};
+    for (const void *p : words)
+        if (misaligned(p, 4)) return fail(SPEC_ERR_ARG, "misaligned pointer (int32 arrays need 4 bytes)");
+    if (misaligned(b.slots, 8)) return fail(SPEC_ERR_ARG, "misaligned pointer (slots need 8 bytes)");
+    if (b.lanes > 0 && (b.held == b.held_out || b.context_lens == b.seq_lens))
+        return fail(SPEC_ERR_ARG, "outputs must not alias inputs (held_out and held, seq_lens and context_lens)");
+    Device *d = nullptr;
+    st = device(&d);
+    if (st != SPEC_OK) return st;
+    paged::PlanArgs a = {b, free_pages, num_free, cursor};
+    int64_t grid = (b.tokens + paged::kPlanThreads - 1) / paged::kPlanThreads;
+    const int64_t by_lanes = (b.lanes + paged::kPlanWarps - 1) / paged::kPlanWarps;
+    if (grid < by_lanes) grid = by_lanes;
+    if (grid < 1) grid = 1;
+    if (grid > d->sms) grid = d->sms;
+    return launch(paged::plan_kernel, dim3((unsigned)grid), paged::kPlanThreads, 2 * (size_t)(b.lanes + 1) * 8, a);
+}
+
+spec_status spec_paged_store(const void *k, const void *v, int64_t tokens, int64_t k_token_stride,
+                             int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                             const int64_t *slots, const spec_paged_cache *cache)
+{
+    host::clear_error();
+    spec_status st = check_cache(cache);
+    if (st != SPEC_OK) return st;
+    if (tokens < 0 || tokens > INT32_MAX) return fail(SPEC_ERR_ARG, "tokens = %lld", (long long)tokens);
+    if (tokens == 0) return SPEC_OK;
+    if (!k || !v || !slots) return fail(SPEC_ERR_ARG, "null pointer");
+    if (misaligned(k, 16) || misaligned(v, 16) || misaligned(slots, 8))
+        return fail(SPEC_ERR_ARG, "misaligned pointer (keys and values need 16 bytes, slots 8)");
+    if (bad_stride(k_token_stride) || bad_stride(k_head_stride) || bad_stride(v_token_stride) ||
+        bad_stride(v_head_stride))
+        return fail(SPEC_ERR_ARG, "strides must be non-negative multiples of 8 elements below 2^39");
+    Device *d = nullptr;
+    st = device(&d);
+    if (st != SPEC_OK) return st;
+    paged::StoreArgs a = {static_cast<const uint16_t *>(k), static_cast<const uint16_t *>(v), tokens,
+                          k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots, *cache};
+    const int64_t nv = tokens * cache->heads * (cache->head_dim / 8);
+    int64_t grid = (nv + paged::kStoreThreads - 1) / paged::kStoreThreads;
+    if (grid > 8 * d->sms) grid = 8 * d->sms;
+    return launch(paged::store_kernel, dim3((unsigned)grid), paged::kStoreThreads, 0, a);
+}
+
+int64_t spec_paged_attention_workspace(void) { return 256; }
+
+spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
+                                 int64_t q_head_stride, const spec_paged_cache *cache, const spec_paged_batch *batch,
+                                 float scale, int64_t window, int64_t max_new, void *out, float *lse,
+                                 void *workspace, int64_t workspace_bytes)
+{
+    host::clear_error();
+    spec_status st = check_cache(cache);
+    if (st == SPEC_OK) st = check_batch(batch);
+    if (st != SPEC_OK) return st;
+    const spec_paged_cache &c = *cache;
+    const spec_paged_batch &b = *batch;
+    if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256)
+        return fail(SPEC_ERR_ARG, "head_dim = %d: attention takes 64, 128 or 256", c.head_dim);
+    if (c.page_size < 8 || (c.page_size & (c.page_size - 1)) != 0)
+        return fail(SPEC_ERR_ARG, "page_size = %d: attention takes powers of two from 8", c.page_size);
+    if (b.page_size != c.page_size)
+        return fail(SPEC_ERR_ARG, "page_size of batch (%d) and cache (%d) differ", b.page_size, c.page_size);
+    if (tokens < 0 || tokens > INT32_MAX) return fail(SPEC_ERR_ARG, "tokens = %lld", (long long)tokens);
+    if (heads_q < 1 || heads_q % c.heads != 0)
+        return fail(SPEC_ERR_ARG, "heads_q = %d: need a positive multiple of the cache's %d heads", heads_q, c.heads);
+    if ((int64_t)tokens * heads_q > INT32_MAX) return fail(SPEC_ERR_ARG, "tokens * heads_q exceeds 2^31-1");
+    if (!(scale > 0.f) || !isfinite(scale)) return fail(SPEC_ERR_ARG, "scale = %g: must be positive and finite", scale);
+    if (window < 0) return fail(SPEC_ERR_ARG, "window = %lld < 0", (long long)window);
+    if (max_new < 0) return fail(SPEC_ERR_ARG, "max_new = %lld < 0", (long long)max_new);
+    if (bad_stride(q_token_stride) || bad_stride(q_head_stride))
+        return fail(SPEC_ERR_ARG, "strides must be non-negative multiples of 8 elements below 2^39");
+    if (tokens == 0 || b.lanes == 0) return SPEC_OK;
+    if (!q || !out || !b.block_table || !b.cu_new || !b.seq_lens || !workspace) return fail(SPEC_ERR_ARG, "null pointer");
+    if (misaligned(q, 16) || misaligned(out, 16) || misaligned(workspace, 16) || misaligned(lse, 4) ||
+        misaligned(b.block_table, 4) || misaligned(b.cu_new, 4) || misaligned(b.seq_lens, 4))
+        return fail(SPEC_ERR_ARG, "misaligned pointer (q, out and workspace need 16 bytes, int32 and lse 4)");
+    const int64_t need = spec_paged_attention_workspace();
+    if (need < 0) return (spec_status)need;
+    if (workspace_bytes < need)
+        return fail(SPEC_ERR_ARG, "workspace: %lld bytes, the call needs %lld", (long long)workspace_bytes,
+                    (long long)need);
+    Device *d = nullptr;
+    st = device(&d);
+    if (st != SPEC_OK) return st;
+    attn::Args a;
+    memset(&a, 0, sizeof a);
+    a.q = static_cast<const uint16_t *>(q);
+    a.tokens = tokens; a.qs_t = q_token_stride; a.qs_h = q_head_stride;
+    a.heads_q = heads_q; a.group = heads_q / c.heads; a.c = c;
+    a.block_table = b.block_table; a.cu_new = b.cu_new; a.seq_lens = b.seq_lens;
+    a.lanes = (int32_t)b.lanes; a.max_pages = b.max_pages;
+    a.scale = scale; a.window = window;
+    a.out = static_cast<uint16_t *>(out); a.lse = lse;
+    int64_t grid = (tokens * heads_q + 3) / 4;
+    if (grid > 16 * d->sms) grid = 16 * d->sms;
+    if (c.dtype == SPEC_F16) return launch(attn::simple_kernel<true>, dim3((unsigned)grid), 128, 0, a);
+    return launch(attn::simple_kernel<false>, dim3((unsigned)grid), 128, 0, a);
+}
+
+spec_status spec_logits_process(const uint16_t *logits, int64_t lanes, int32_t cols, int64_t V,
+                                const int32_t *history, int64_t history_stride, const int32_t *prompt_lens,
+                                const int32_t *history_lens, const int32_t *drafts, const float *penalties,
+                                const int32_t *bias_ids, const float *bias_vals, int64_t max_bias,
+                                const int32_t *bias_lens, const uint32_t *mask, int64_t mask_count,
+                                const int32_t *mask_rows, uint16_t *out)
+{
+    host::clear_error();
+    if (lanes < 0 || lanes > 65535) return fail(SPEC_ERR_ARG, "lanes = %lld outside [0, 65535]", (long long)lanes);
+    if (cols < 1 || cols > SPEC_MAX_GAMMA + 1)
+        return fail(SPEC_ERR_ARG, "cols = %d outside [1, %d]", cols, SPEC_MAX_GAMMA + 1);
+    if (V < 1 || V > INT32_MAX) return fail(SPEC_ERR_ARG, "V = %lld outside [1, 2^31-1]", (long long)V);
+    if (history_stride < 0 || max_bias < 0 || mask_count < 0)
+        return fail(SPEC_ERR_ARG, "history_stride, max_bias and mask_count must not be negative");
+    if (lanes == 0) return SPEC_OK;
+    if (!logits || !out) return fail(SPEC_ERR_ARG, "null pointer");
+    if (!!history != !!prompt_lens || !!history != !!history_lens)
+        return fail(SPEC_ERR_ARG, "history, prompt_lens and history_lens go together");
+    if (!!bias_ids != !!bias_vals || !!bias_ids != !!bias_lens)
+        return fail(SPEC_ERR_ARG, "bias_ids, bias_vals and bias_lens go together");
+    if (!!mask != !!mask_rows) return fail(SPEC_ERR_ARG, "mask and mask_rows go together");
+    if (misaligned(logits, 2) || misaligned(out, 2)) return fail(SPEC_ERR_ARG, "misaligned pointer (logits need 2 bytes)");
+    const void *words[] = {history, prompt_lens, history_lens, drafts, penalties, bias_ids, bias_vals, bias_lens, mask, mask_rows};
+    for (const void *p : words)
+        if (misaligned(p, 4)) return fail(SPEC_ERR_ARG, "misaligned pointer (32-bit arrays need 4 bytes)");
+    const int64_t bytes = lanes * cols * V * 2;   // below 2^16 * 2^4 * 2^31 * 2
+    const char *x = reinterpret_cast<const char *>(logits), *y = reinterpret_cast<const char *>(out);
+    if (x != y && x < y + bytes && y < x + bytes)
+        return fail(SPEC_ERR_ARG, "out overlaps logits without being them");
+    Device *d = nullptr;
+    spec_status st = device(&d);
+    if (st != SPEC_OK) return st;
+    rules::Args a = {logits, out, lanes, V, cols, history, history_stride, prompt_lens, history_lens, drafts,
+                     penalties, bias_ids, bias_vals, max_bias, bias_lens, mask, mask_count, mask_rows};
+    const unsigned slices = (unsigned)((V + 7 + rules::kSlice - 1) / rules::kSlice);
+    return launch(rules::process_kernel, dim3(slices, (unsigned)lanes), rules::kThreads, 0, a);
+}
+
+}  // extern "C"

@@ -32,6 +32,7 @@
 #include "round_warp.cuh"
 #include "round_gm.cuh"
 #include "head_q4.cuh"
+#include "host.h"
 
 namespace {
 
@@ -1095,7 +1096,10 @@ spec_status spec_device_status(void)
     unsigned int flags = 0, zero = 0;
     e = cudaMemcpyFromSymbol(&flags, g_wait_timeouts, sizeof flags);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyFromSymbol");
-    if (flags == 0) return SPEC_OK;
+    unsigned int paged = 0;
+    e = host::take_paged_timeouts(&paged);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyFromSymbol");
+    if ((flags | paged) == 0) return SPEC_OK;
     e = cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof zero);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyToSymbol");
     return fail(SPEC_ERR_CUDA, "a kernel gave up a bounded wait on its copy pipeline; its results are invalid");
@@ -1206,3 +1210,27 @@ extern "C" spec_status spec_round_noalloc(const uint16_t *draft_logits, int64_t 
     t_last_kernel = plan_kernel(plan);
     return SPEC_OK;
 }
+
+// ---------------------------------------------------------------------------
+// the shared host state, for the other translation units
+// ---------------------------------------------------------------------------
+
+namespace host {
+
+cudaStream_t stream() { return t_stream; }
+void clear_error() { t_err.clear(); }
+void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+spec_status cuda_fail(cudaError_t e, const char *what) { return ::cuda_fail(e, what); }
+
+spec_status fail(spec_status st, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    t_err = buf;
+    return st;
+}
+
+}  // namespace host
