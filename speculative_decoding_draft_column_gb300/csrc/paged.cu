@@ -23,10 +23,46 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
 struct Device {
     bool init = false;
     int sms = 0;
+    EncodeTiled encode = nullptr;
+    int attn_smem[5][2];   // dynamic shared memory of the attention kernels, [shape][fp16]
 };
+
+template <int D, int QT>
+constexpr int shape_index() { return D == 64 ? QT - 1 : D == 128 ? QT + 1 : 4; }
+
+// Give an attention kernel all the shared memory a CTA can have (one CTA an SM,
+// so that TMEM is never contended), and check what the kernel relies on: its
+// static shared memory stays below the first 1,024-byte boundary.
+template <int D, int QT, bool F16>
+spec_status prepare_attention(Device &d, int smem_max)
+{
+    using S = attn::Shape<D, QT>;
+    auto kernel = attn::attention_kernel<D, QT, F16>;
+    cudaFuncAttributes at;
+    cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes");
+    const int dynamic = smem_max - (int)at.sharedSizeBytes;
+    if (at.sharedSizeBytes > 1024 || 1024 + S::kPayload > smem_max)
+        return fail(SPEC_ERR_CUDA, "attention: %d bytes of shared memory are not enough", smem_max);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dynamic);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    d.attn_smem[shape_index<D, QT>()][F16] = dynamic;
+    return SPEC_OK;
+}
+
+template <int D, int QT>
+spec_status prepare_attention(Device &d, int smem_max)
+{
+    const spec_status st = prepare_attention<D, QT, false>(d, smem_max);
+    return st == SPEC_OK ? prepare_attention<D, QT, true>(d, smem_max) : st;
+}
 
 std::mutex g_paged_mu;
 Device g_devices[kMaxDevices];
@@ -45,6 +81,21 @@ spec_status device(Device **out)
         e = cudaFuncSetAttribute(paged::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  2 * (SPEC_PAGED_MAX_LANES + 1) * 8);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+        int smem_max = 0;
+        e = cudaDeviceGetAttribute(&smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+        spec_status st = prepare_attention<64, 1>(d, smem_max);
+        if (st == SPEC_OK) st = prepare_attention<64, 2>(d, smem_max);
+        if (st == SPEC_OK) st = prepare_attention<128, 1>(d, smem_max);
+        if (st == SPEC_OK) st = prepare_attention<128, 2>(d, smem_max);
+        if (st == SPEC_OK) st = prepare_attention<256, 1>(d, smem_max);
+        if (st != SPEC_OK) return st;
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+        e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaGetDriverEntryPointByVersion");
+        if (!fn || found != cudaDriverEntryPointSuccess) return fail(SPEC_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+        d.encode = reinterpret_cast<EncodeTiled>(fn);
         d.init = true;
     }
     *out = &d;
@@ -102,6 +153,41 @@ spec_status check_batch(const spec_paged_batch *b)
     if (b->max_pages < 1 || b->max_pages > INT32_MAX)
         return fail(SPEC_ERR_ARG, "batch: max_pages = %lld", (long long)b->max_pages);
     if (b->page_size < 1) return fail(SPEC_ERR_ARG, "batch: page_size = %d < 1", b->page_size);
+    return SPEC_OK;
+}
+
+constexpr int64_t max2(int64_t a, int64_t b) { return a > b ? a : b; }
+constexpr int64_t kPartFloats = max2(attn::Shape<128, 2>::kPartFloats, attn::Shape<256, 1>::kPartFloats);
+
+int attention_grid(const Device &d) { return d.sms < attn::kMaxSms ? d.sms : attn::kMaxSms; }
+
+template <int D, int QT>
+spec_status launch_attention(const Device &d, const attn::Args &a, bool f16)
+{
+    using S = attn::Shape<D, QT>;
+    static_assert(S::kPartFloats <= kPartFloats, "");
+    const dim3 grid((unsigned)attention_grid(d));
+    const size_t smem = (size_t)d.attn_smem[shape_index<D, QT>()][f16];
+    return f16 ? launch(attn::attention_kernel<D, QT, true>, grid, S::kThreads, smem, a)
+               : launch(attn::attention_kernel<D, QT, false>, grid, S::kThreads, smem, a);
+}
+
+// The cache as TMA sees it: [page][head][block of 64][token][64], boxes of one
+// page's tokens (at most a tile's) by 64 elements -- all blocks at once where
+// the box has a whole tile's rows, so that its blocks land a tile apart.
+spec_status page_map(const Device &d, const spec_paged_cache &c, void *base, const int64_t *strides, CUtensorMap *map)
+{
+    const int tile = c.head_dim == 256 ? attn::Shape<256, 1>::BK : attn::Shape<128, 1>::BK;
+    const cuuint32_t rows = (cuuint32_t)(c.page_size < tile ? c.page_size : tile);
+    const cuuint64_t dims[5] = {64, (cuuint64_t)c.page_size, (cuuint64_t)c.head_dim / 64, (cuuint64_t)c.heads,
+                                (cuuint64_t)c.pages};
+    const cuuint64_t st[4] = {(cuuint64_t)strides[1] * 2, 128, (cuuint64_t)strides[2] * 2, (cuuint64_t)strides[0] * 2};
+    const cuuint32_t box[5] = {64, rows, (int)rows == tile ? (cuuint32_t)c.head_dim / 64 : 1u, 1, 1};
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    const CUresult r = d.encode(map, c.dtype == SPEC_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                5, base, dims, st, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(SPEC_ERR_ARG, "cache: its layout has no tensor map (driver error %d)", (int)r);
     return SPEC_OK;
 }
 
@@ -179,7 +265,14 @@ spec_status spec_paged_store(const void *k, const void *v, int64_t tokens, int64
     return launch(paged::store_kernel, dim3((unsigned)grid), paged::kStoreThreads, 0, a);
 }
 
-int64_t spec_paged_attention_workspace(void) { return 256; }
+int64_t spec_paged_attention_workspace(void)
+{
+    host::clear_error();
+    Device *d = nullptr;
+    const spec_status st = device(&d);
+    if (st != SPEC_OK) return st;
+    return (int64_t)attn::kMaxSms * 4 + (int64_t)attention_grid(*d) * 2 * kPartFloats * 4;
+}
 
 spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
                                  int64_t q_head_stride, const spec_paged_cache *cache, const spec_paged_batch *batch,
@@ -222,17 +315,25 @@ spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q,
     if (st != SPEC_OK) return st;
     attn::Args a;
     memset(&a, 0, sizeof a);
+    st = page_map(*d, c, c.k, c.k_strides, &a.kmap);
+    if (st == SPEC_OK) st = page_map(*d, c, c.v, c.v_strides, &a.vmap);
+    if (st != SPEC_OK) return st;
     a.q = static_cast<const uint16_t *>(q);
     a.tokens = tokens; a.qs_t = q_token_stride; a.qs_h = q_head_stride;
-    a.heads_q = heads_q; a.group = heads_q / c.heads; a.c = c;
+    a.heads_q = heads_q; a.heads_kv = c.heads; a.group = heads_q / c.heads;
+    while ((1 << a.log_page) < c.page_size) ++a.log_page;
     a.block_table = b.block_table; a.cu_new = b.cu_new; a.seq_lens = b.seq_lens;
     a.lanes = (int32_t)b.lanes; a.max_pages = b.max_pages;
-    a.scale = scale; a.window = window;
+    a.c = scale * attn::kLog2e; a.window = window;
     a.out = static_cast<uint16_t *>(out); a.lse = lse;
-    int64_t grid = (tokens * heads_q + 3) / 4;
-    if (grid > 16 * d->sms) grid = 16 * d->sms;
-    if (c.dtype == SPEC_F16) return launch(attn::simple_kernel<true>, dim3((unsigned)grid), 128, 0, a);
-    return launch(attn::simple_kernel<false>, dim3((unsigned)grid), 128, 0, a);
+    a.tickets = static_cast<unsigned int *>(workspace);
+    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + attn::kMaxSms * 4);
+    const int64_t chunk = max_new > 0 ? max_new : (tokens + b.lanes - 1) / b.lanes;
+    const bool two = chunk * a.group > 128;   // more rows than one tile: two tiles share every K/V tile
+    const bool f16 = c.dtype == SPEC_F16;
+    if (c.head_dim == 256) return launch_attention<256, 1>(*d, a, f16);
+    if (c.head_dim == 128) return two ? launch_attention<128, 2>(*d, a, f16) : launch_attention<128, 1>(*d, a, f16);
+    return two ? launch_attention<64, 2>(*d, a, f16) : launch_attention<64, 1>(*d, a, f16);
 }
 
 spec_status spec_logits_process(const uint16_t *logits, int64_t lanes, int32_t cols, int64_t V,

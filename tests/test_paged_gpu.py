@@ -267,6 +267,24 @@ def test_long_split_context_and_workspace_reuse(sd):
         assert torch.equal(out.view(torch.int16), out2.view(torch.int16)) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_many_tiles_per_cta(sd, dim):
+    """Runs of many tiles: several items, and several tiles of an item, in every CTA."""
+    rng = np.random.default_rng(dim)
+    c = _case([3] * 24, rng.integers(0, 2_200, 24).tolist(), 4, 2, dim, 32, "bf16", seed=1)
+    out, lse = _attend(sd, c, max_new=3)
+    _check(c, out, lse)
+    c = _case([2], [70_000], 1, 1, dim, 64, "f16", seed=2)
+    out, lse = _attend(sd, c, max_new=2)
+    _check(c, out, lse)
+    c = _case([700, 1], [900, 1_100], 2, 4, dim, 16, "bf16", seed=3)
+    out, lse = _attend(sd, c, max_new=700)
+    _check(c, out, lse)
+    c = _case([300], [4_000], 2, 3, dim, 128, "f16", seed=4, sharp=6.0)
+    out, lse = _attend(sd, c, max_new=300)
+    _check(c, out, lse)
+
+
 def test_many_lanes(sd):
     rng = np.random.default_rng(3)
     new, ctx = rng.integers(0, 3, 700).tolist(), rng.integers(0, 40, 700).tolist()
