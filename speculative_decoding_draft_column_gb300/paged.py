@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import SPEC_ERR_ARG, SpecError, _check, _dev, _n, _use_torch_stream, lib
+from . import SPEC_ERR_ARG, SpecError, _check, _n, lib
 
 SPEC_BF16, SPEC_F16 = 0, 1
 SPEC_PAGED_MAX_LANES = 4096
@@ -42,29 +42,74 @@ def _dtype_code(x, name):
     _bad(f"{name}: dtype {x.dtype}, need bfloat16 or float16")
 
 
-def _typed(x, dtype, count, name):
-    """Pointer of a contiguous CUDA tensor of `dtype` with at least `count` elements."""
-    if x.dtype != dtype:
+def _load_torch():
+    import torch
+    global _torch, _raw_stream
+    _torch = lambda: torch  # noqa: E731 - no import statement on the way of each call
+    # the current stream's handle; the Stream object costs ten times as much
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    return torch
+
+
+def _torch():
+    return _load_torch()
+
+
+def _raw_stream(dev):
+    _load_torch()
+    return _raw_stream(dev)
+
+
+def _set_stream(dev):
+    lib.spec_set_stream(_raw_stream(dev))
+
+
+def _array(x, dtype, count, dev, name):
+    """Pointer of a contiguous CUDA tensor of `dtype` on device `dev` with at
+    least `count` elements; these calls take no raw pointers."""
+    if not hasattr(x, "get_device"):
+        _bad(f"{name}: need a CUDA tensor")
+    if x.get_device() != dev:
+        _bad(f"{name}: on {x.device}, need cuda:{dev}")
+    if x.dtype is not dtype:
         _bad(f"{name}: dtype {x.dtype}, need {dtype}")
-    return _dev(x, count, x.element_size(), name)
+    if not x.is_contiguous():
+        _bad(f"{name}: tensor must be contiguous")
+    if x.numel() < count:
+        _bad(f"{name}: {x.numel()} elements, the call needs {count}")
+    return x.data_ptr()
 
 
-def _strided(x, shape, cache, name):
-    """Check a [tokens, heads, head_dim] tensor whose rows are contiguous."""
-    if not x.is_cuda or x.device.index != cache.device:
-        _bad(f"{name}: on {x.device}, the cache is on cuda:{cache.device}")
-    if x.dtype != cache.torch_dtype:
+def _rows(x, shape, cache, name):
+    """Strides of a [tokens, heads, head_dim] tensor of the cache's type and
+    device whose rows are contiguous."""
+    if not hasattr(x, "get_device") or x.get_device() != cache.device:
+        _bad(f"{name}: need a CUDA tensor on cuda:{cache.device}, where the cache is")
+    if x.dtype is not cache.torch_dtype:
         _bad(f"{name}: dtype {x.dtype}, the cache's is {cache.torch_dtype}")
-    if x.dim() != 3 or (shape is not None and tuple(x.shape) != shape) or x.shape[2] != cache.head_dim:
-        _bad(f"{name}: shape {tuple(x.shape)}, need {shape or ('tokens', 'heads', cache.head_dim)}")
-    if x.stride(2) != 1 and x.numel():
+    have = x.shape
+    if len(have) != 3 or have[2] != cache.head_dim or (shape is not None and have != shape):
+        _bad(f"{name}: shape {tuple(have)}, need {shape or ('tokens', 'heads', cache.head_dim)}")
+    strides = x.stride()
+    if strides[2] != 1 and x.numel():
         _bad(f"{name}: the last dimension must be contiguous")
+    return strides
+
+
+def _rows_of(x, lanes, name):
+    """Length of the rows of a [lanes, length] tensor."""
+    shape = x.shape
+    if len(shape) != 2 or shape[0] < lanes:
+        _bad(f"{name}: need [lanes, length], got {tuple(shape)}")
+    return shape[1]
 
 
 def _on_current_device(index, name):
-    import torch
-    if index != torch.cuda.current_device():
-        _bad(f"{name}: on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
+    cur = _torch().cuda.current_device()
+    if index != cur:
+        _bad(f"{name}: on cuda:{index}, the current device is cuda:{cur}")
+    return cur
 
 
 class PagedCache:
@@ -106,12 +151,14 @@ class PagedBatch:
         lanes, max_pages = block_table.shape
         self.lanes, self.max_pages, self.page_size = lanes, max_pages, page_size
         self.block_table, self.cu_new, self.seq_lens = block_table, cu_new, seq_lens
-        i32 = torch.int32
-        s = _BatchStruct(block_table=_typed(block_table, i32, lanes * max_pages, "block_table"),
-                         cu_new=_typed(cu_new, i32, lanes + 1, "cu_new"),
-                         seq_lens=_typed(seq_lens, i32, lanes, "seq_lens"),
+        i32, dev = torch.int32, block_table.get_device()
+        if dev < 0:
+            _bad("block_table: need a CUDA tensor")
+        s = _BatchStruct(block_table=_array(block_table, i32, lanes * max_pages, dev, "block_table"),
+                         cu_new=_array(cu_new, i32, lanes + 1, dev, "cu_new"),
+                         seq_lens=_array(seq_lens, i32, lanes, dev, "seq_lens"),
                          lanes=lanes, max_pages=max_pages, page_size=page_size)
-        self.device = block_table.device.index
+        self.device = dev
         rest = (context_lens, new_lens, held, held_out, positions, slots, info)
         self.plannable = all(x is not None for x in rest)
         if not self.plannable and any(x is not None for x in rest):
@@ -122,8 +169,8 @@ class PagedBatch:
             tokens = positions.numel()
             for name, count in (("context_lens", lanes), ("new_lens", lanes), ("held", lanes), ("held_out", lanes),
                                 ("positions", tokens), ("info", 4)):
-                setattr(s, name, _typed(getattr(self, name), i32, count, name))
-            s.slots = _typed(slots, torch.int64, tokens, "slots")
+                setattr(s, name, _array(getattr(self, name), i32, count, dev, name))
+            s.slots = _array(slots, torch.int64, tokens, dev, "slots")
             s.tokens = tokens
         self._c = s
         self._ref = ctypes.byref(s)
@@ -141,29 +188,30 @@ class PagedBatch:
 def spec_paged_plan(batch, free_pages, cursor=None):
     """Plan a step into the batch's buffers; ``free_pages`` int32, ``cursor``
     int32 [1] (the pages of the list used before) or None."""
-    import torch
     if not batch.plannable:
         _bad("batch: made without the plan's buffers")
-    _on_current_device(batch.device, "batch")
+    i32 = _torch().int32
+    dev = _on_current_device(batch.device, "batch")
     n = free_pages.numel()
-    f = _typed(free_pages, torch.int32, n, "free_pages")
-    c = None if cursor is None else _typed(cursor, torch.int32, 1, "cursor")
-    _use_torch_stream()
-    _check(lib.spec_paged_plan(batch._ref, f, n, c))
+    f = _array(free_pages, i32, n, dev, "free_pages")
+    c = None if cursor is None else _array(cursor, i32, 1, dev, "cursor")
+    _set_stream(dev)
+    st = lib.spec_paged_plan(batch._ref, f, n, c)
+    if st:
+        _check(st)
 
 
 def spec_paged_store(k, v, slots, cache):
     """Store k, v [tokens, heads, head_dim] at slots int64 [tokens] of the cache."""
-    import torch
     tokens = k.shape[0]
     shape = (tokens, cache.heads, cache.head_dim)
-    _strided(k, shape, cache, "k")
-    _strided(v, shape, cache, "v")
-    _on_current_device(cache.device, "cache")
-    sl = _typed(slots, torch.int64, tokens, "slots")
-    _use_torch_stream()
-    _check(lib.spec_paged_store(k.data_ptr(), v.data_ptr(), tokens, k.stride(0), k.stride(1), v.stride(0),
-                                v.stride(1), sl, cache._ref))
+    ks, vs = _rows(k, shape, cache, "k"), _rows(v, shape, cache, "v")
+    dev = _on_current_device(cache.device, "cache")
+    sl = _array(slots, _torch().int64, tokens, dev, "slots")
+    _set_stream(dev)
+    st = lib.spec_paged_store(k.data_ptr(), v.data_ptr(), tokens, ks[0], ks[1], vs[0], vs[1], sl, cache._ref)
+    if st:
+        _check(st)
 
 
 def spec_paged_attention_workspace() -> int:
@@ -184,21 +232,22 @@ def new_attention_workspace(device="cuda"):
 def spec_paged_attention(q, cache, batch, scale, out, lse, workspace, window=0, max_new=0):
     """Attention of the batch's new tokens: q [tokens, heads_q, head_dim] into
     out (same shape, contiguous) and lse fp32 [tokens, heads_q] (or None)."""
-    import torch
-    _strided(q, None, cache, "q")
-    _on_current_device(cache.device, "cache")
-    if batch.device != cache.device:
+    shape = q.shape
+    qs = _rows(q, None, cache, "q")
+    dev = _on_current_device(cache.device, "cache")
+    if batch.device != dev:
         _bad("batch and cache are on different devices")
-    tokens, heads_q, _ = q.shape
-    if out.dtype != cache.torch_dtype or out.shape != q.shape:
-        _bad(f"out: {out.dtype} {tuple(out.shape)}, need {cache.torch_dtype} {tuple(q.shape)}")
-    o = _dev(out, q.numel(), 2, "out")
-    ls = None if lse is None else _typed(lse, torch.float32, tokens * heads_q, "lse")
-    ws = _dev(workspace, 0, 1, "workspace")
-    _use_torch_stream()
-    _check(lib.spec_paged_attention(q.data_ptr(), tokens, heads_q, q.stride(0), q.stride(1), cache._ref, batch._ref,
-                                    scale, window, max_new, o, ls, ws,
-                                    workspace.numel() * workspace.element_size()))
+    tokens, heads_q, dim = shape
+    if out.shape != shape:
+        _bad(f"out: shape {tuple(out.shape)}, need {tuple(shape)}")
+    o = _array(out, cache.torch_dtype, tokens * heads_q * dim, dev, "out")
+    ls = None if lse is None else _array(lse, _torch().float32, tokens * heads_q, dev, "lse")
+    ws = _array(workspace, workspace.dtype, 0, dev, "workspace")
+    _set_stream(dev)
+    st = lib.spec_paged_attention(q.data_ptr(), tokens, heads_q, qs[0], qs[1], cache._ref, batch._ref, scale, window,
+                                  max_new, o, ls, ws, workspace.numel() * workspace.element_size())
+    if st:
+        _check(st)
 
 
 def spec_logits_process(logits, lanes, cols, V, out, *, history=None, prompt_lens=None, history_lens=None,
@@ -206,47 +255,48 @@ def spec_logits_process(logits, lanes, cols, V, out, *, history=None, prompt_len
                         mask_rows=None):
     """Penalties, biases and grammar masks on bf16 logits [lanes*cols, V] into
     ``out`` (which may be ``logits``); every rule's tensors may be left out."""
-    import torch
-    i32 = torch.int32
-    ln, cs, n = _n(lanes), _n(cols), _n(lanes) * _n(cols) * _n(V)
+    t = _torch()
+    i32, f32 = t.int32, t.float32
+    ln, cs, vs = _n(lanes), _n(cols), _n(V)
+    n = ln * cs * vs
     for x, name in ((logits, "logits"), (out, "out")):
-        if x is not None and x.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        if x is not None and x.dtype is not t.bfloat16 and x.dtype not in (t.int16, t.uint16):
             _bad(f"{name}: dtype {x.dtype} is not bf16 bits")
-    lg, o = _dev(logits, n, 2, "logits"), _dev(out, n, 2, "out")
+    dev = t.cuda.current_device()
+    lg = None if logits is None else _array(logits, logits.dtype, n, dev, "logits")
+    o = None if out is None else _array(out, out.dtype, n, dev, "out")
     hs = nb = rows = 0
     h = pl = hl = d = pen = bi = bv = bl = m = mr = None
     if history is not None:
-        if history.dim() != 2 or history.shape[0] < ln:
-            _bad("history: need [lanes, length]")
-        hs = history.shape[1]
-        h = _typed(history, i32, ln * hs, "history")
+        hs = _rows_of(history, ln, "history")
+        h = _array(history, i32, ln * hs, dev, "history")
     if prompt_lens is not None:
-        pl = _typed(prompt_lens, i32, ln, "prompt_lens")
+        pl = _array(prompt_lens, i32, ln, dev, "prompt_lens")
     if history_lens is not None:
-        hl = _typed(history_lens, i32, ln, "history_lens")
+        hl = _array(history_lens, i32, ln, dev, "history_lens")
     if drafts is not None:
-        d = _typed(drafts, i32, ln * (cs - 1), "drafts")
+        d = _array(drafts, i32, ln * (cs - 1), dev, "drafts")
     if penalties is not None:
-        pen = _typed(penalties, torch.float32, 3 * ln, "penalties")
+        pen = _array(penalties, f32, 3 * ln, dev, "penalties")
     if bias_ids is not None:
-        if bias_ids.dim() != 2 or bias_ids.shape[0] < ln:
-            _bad("bias_ids: need [lanes, biases]")
-        nb = bias_ids.shape[1]
-        bi = _typed(bias_ids, i32, ln * nb, "bias_ids")
+        nb = _rows_of(bias_ids, ln, "bias_ids")
+        bi = _array(bias_ids, i32, ln * nb, dev, "bias_ids")
     if bias_vals is not None:
-        bv = _typed(bias_vals, torch.float32, ln * nb, "bias_vals")
+        bv = _array(bias_vals, f32, ln * nb, dev, "bias_vals")
     if bias_lens is not None:
-        bl = _typed(bias_lens, i32, ln, "bias_lens")
+        bl = _array(bias_lens, i32, ln, dev, "bias_lens")
     if mask is not None:
-        words = (_n(V) + 31) // 32
+        words = (vs + 31) // 32
+        rows = mask.shape[0]
         if mask.dim() != 2 or mask.shape[1] != words or mask.element_size() != 4:
             _bad(f"mask: need 32-bit words [rows, {words}]")
-        rows = mask.shape[0]
-        m = _dev(mask, rows * words, 4, "mask")
+        m = _array(mask, mask.dtype, rows * words, dev, "mask")
     if mask_rows is not None:
-        mr = _typed(mask_rows, i32, ln * cs, "mask_rows")
-    _use_torch_stream()
-    _check(lib.spec_logits_process(lg, lanes, cols, V, h, hs, pl, hl, d, pen, bi, bv, nb, bl, m, rows, mr, o))
+        mr = _array(mask_rows, i32, ln * cs, dev, "mask_rows")
+    _set_stream(dev)
+    st = lib.spec_logits_process(lg, lanes, cols, V, h, hs, pl, hl, d, pen, bi, bv, nb, bl, m, rows, mr, o)
+    if st:
+        _check(st)
 
 
 # ---- allocating conveniences ------------------------------------------------
