@@ -14,6 +14,10 @@ constexpr int kThreads = 512;
 constexpr int kSlice = 8 * kThreads;     // tokens of a slice: one 16-byte vector a thread and column
 constexpr int kWindow = kSlice + 8;      // a column's vectors may start up to 7 elements before the slice
 constexpr int kBatch = 4;                // columns whose loads are in flight together
+// Counts and biases lie by token mod 8: element i of every thread's vector is
+// read by consecutive threads from consecutive words.
+constexpr int kPitch = kWindow / 8;
+__device__ __forceinline__ int place(int e) { return (e & 7) * kPitch + (e >> 3); }
 constexpr uint32_t kSeen = 0x80000000u;  // the token is in the prompt; the other bits count the output
 
 struct Args {
@@ -42,6 +46,14 @@ __device__ __forceinline__ uint16_t to_bf16(float f)
     uint16_t h;
     asm("{\n\t.reg .b16 r;\n\tcvt.rn.bf16.f32 r, %1;\n\tmov.b16 %0, r;\n\t}" : "=h"(h) : "f"(f));
     return h;
+}
+
+// bytes of the sign bits that the selector's nibbles (8 + byte) name
+__device__ __forceinline__ uint32_t copies(uint32_t v, uint32_t selector)
+{
+    uint32_t d;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(d) : "r"(v), "r"(selector));
+    return d;
 }
 
 __device__ __forceinline__ int64_t clamp_len(int32_t n, int64_t most) { return n < 0 ? 0 : n > most ? most : n; }
@@ -94,8 +106,8 @@ __global__ void __launch_bounds__(kThreads, 3) process_kernel(const __grid_const
             for (int u = 0; u < kAhead; ++u) {
                 const int e = entry(id[u]);
                 if (e >= 0) {
-                    if (i0 + u * kThreads < prompt) atomicOr(&count[e], kSeen);
-                    else atomicAdd(&count[e], 1u);
+                    if (i0 + u * kThreads < prompt) atomicOr(&count[place(e)], kSeen);
+                    else atomicAdd(&count[place(e)], 1u);
                     touch(e);
                 }
             }
@@ -106,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 3) process_kernel(const __grid_const
         for (int64_t i = tid; i < nb; i += kThreads) {
             const int e = entry(__ldg(a.bias_ids + lane * a.max_bias + i));
             if (e >= 0) {
-                atomicAdd(&bias[e], __ldg(a.bias_vals + lane * a.max_bias + i));
+                atomicAdd(&bias[place(e)], __ldg(a.bias_vals + lane * a.max_bias + i));
                 touch(e);
             }
         }
@@ -120,20 +132,26 @@ __global__ void __launch_bounds__(kThreads, 3) process_kernel(const __grid_const
     const float over_r = 1.f / r;   // one divide a lane; x * (1 / r) is within 1.5 fp32 units of x / r
     __syncthreads();
 
-    auto rule = [&](uint32_t raw, int e) -> uint32_t {
-        const uint32_t c = count[e];
-        float x = bf16_as_float(raw);
-        if (c) {
-            x = __fmul_rn(x, x > 0.f ? over_r : r);
-            const uint32_t n = c & ~kSeen;
-            x = __fsub_rn(x, __fadd_rn(__fmul_rn(f, (float)n), n ? p : 0.f));
-        }
-        return to_bf16(__fadd_rn(x, bias[e]));
+    auto rule = [&](uint32_t raw, int at) -> uint32_t {   // at: the token's place
+        const uint32_t c = count[at], n = c & ~kSeen;
+        const float x = bf16_as_float(raw);
+        const float y = __fmul_rn(x, c == 0u ? 1.f : x > 0.f ? over_r : r);
+        const float z = __fsub_rn(y, __fadd_rn(__fmul_rn(f, (float)n), n ? p : 0.f));
+        return to_bf16(__fadd_rn(z, bias[at]));
     };
     const int64_t words = (a.V + 31) / 32;
     const bool same_phase = ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
     const int base_mis = (int)((reinterpret_cast<uintptr_t>(a.logits) & 15) / 2);
     const int64_t col0 = lane * a.cols;
+
+    // A vector starts at token t0 + rel of its column; rel = 8 * tid - mis, where
+    // mis (the same for the whole CTA) is the column's phase.
+    const uint16_t *in0 = a.logits + col0 * a.V + t0;
+    uint16_t *out0 = a.out + col0 * a.V + t0;
+    const uint32_t *mask0 = a.mask ? a.mask + (t0 >> 5) : nullptr;
+    const int mis0 = (int)((base_mis + col0 * a.V + t0) & 7), v7 = (int)(a.V & 7);
+    const int64_t left = a.V - t0;                  // tokens from t0 to the column's end
+    const int end = left > kSlice ? kSlice + 8 : (int)left, begin = t0 > 0 ? -8 : 0;   // tokens [begin, end) are the column's
 
     // kInner: no vector of the slice reaches over an end of its column, in
     // whatever phase, and input and output vectors line up
@@ -142,71 +160,93 @@ __global__ void __launch_bounds__(kThreads, 3) process_kernel(const __grid_const
         for (int j0 = 0; j0 < a.cols; j0 += kBatch) {
             uint4 x[kBatch];
             uint32_t allowed[kBatch];
-            int mis[kBatch];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 allowed[u] = 0xFFu;
-                mis[u] = (int)((base_mis + (col0 + j0 + u) * a.V + t0) & 7);
-                const int row = j0 + u < a.cols ? mask_row[j0 + u] : -1;
+                const int j = j0 + u, row = j < a.cols ? mask_row[j] : -1;
                 if (row < 0) continue;
-                const int64_t t = t0 + 8 * tid - mis[u], w = t >> 5;   // floor, also below 0
-                const uint32_t *m = reinterpret_cast<const uint32_t *>(a.mask) + row * words + w;
+                const int rel = 8 * tid - ((mis0 + j * v7) & 7), w = rel >> 5;   // w: floor, also below 0
+                const uint32_t *m = mask0 + row * words + w;
                 uint32_t lo = 0u, hi = 0u;
-                if (kInner || (w >= 0 && w < words)) lo = __ldg(m);
-                if ((t & 31) > 24 && (kInner || (w + 1 >= 0 && w + 1 < words))) hi = __ldg(m + 1);
-                allowed[u] = __funnelshift_r(lo, hi, (uint32_t)(t & 31)) & 0xFFu;
+                if (kInner || (rel < end && (t0 > 0 || w >= 0))) lo = __ldg(m);
+                if ((rel & 31) > 24 && (kInner || 32 * (w + 1) < end)) hi = __ldg(m + 1);
+                allowed[u] = __funnelshift_r(lo, hi, (uint32_t)(rel & 31)) & 0xFFu;
             }
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 x[u] = make_uint4(0, 0, 0, 0);
-                if (j0 + u >= a.cols || allowed[u] == 0u) continue;
-                const int64_t t = t0 + 8 * tid - mis[u];
-                const uint16_t *src = a.logits + (col0 + j0 + u) * a.V + t;
-                if (kInner || (t >= 0 && t + 8 <= a.V)) x[u] = __ldcs(reinterpret_cast<const uint4 *>(src));
-                else if (t + 8 > 0 && t < a.V) x[u] = load_edge(src, 0, 0, -t, a.V - t);
+                const int j = j0 + u;
+                if (j >= a.cols || allowed[u] == 0u) continue;
+                const int rel = 8 * tid - ((mis0 + j * v7) & 7);
+                const uint16_t *src = in0 + j * a.V + rel;
+                if (kInner || (rel >= begin && rel + 8 <= end)) x[u] = __ldcs(reinterpret_cast<const uint4 *>(src));
+                else if (rel + 8 > begin && rel < end) x[u] = load_edge(src, 0, 0, begin - rel, end - rel);
             }
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                if (j0 + u >= a.cols) break;
-                const int e = draft_entry[j0 + u];
+                const int j = j0 + u;
+                if (j >= a.cols) break;
+                const int e = draft_entry[j];
                 if (e >= 0) {          // the same for the whole CTA
                     __syncthreads();
                     if (tid == 0) {
-                        count[e] += 1u;
+                        count[place(e)] += 1u;
                         touched[e >> 5] |= 1u << (e & 31);
                     }
                     __syncthreads();
                 }
-                const int64_t t = t0 + 8 * tid - mis[u];
-                if (!kInner && (t + 8 <= 0 || t >= a.V)) continue;
-                const int e0 = 8 + 8 * tid - mis[u];
+                const int rel = 8 * tid - ((mis0 + j * v7) & 7);
+                if (!kInner && (rel + 8 <= begin || rel >= end)) continue;
+                const int e0 = rel + 8;
                 uint32_t todo = __funnelshift_r(touched[e0 >> 5], touched[(e0 >> 5) + 1], (uint32_t)(e0 & 31)) & allowed[u];
                 uint4 w = x[u];
+                // many seen tokens in one of the warp's vectors: all eight of
+                // each at once, so that their reads overlap (a vector with few goes
+                // one by one: a third of the instructions)
+                if (__any_sync(__activemask(), __popc(todo) > 2)) {
+                    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t out[4];
+                    const int low = e0 & 7, at0 = e0 >> 3;   // low: the same for every thread
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int p0 = (low + 2 * k) & 7, p1 = (low + 2 * k + 1) & 7;
+                        const uint32_t a0 = rule(in[k] & 0xFFFFu, p0 * kPitch + at0 + (low + 2 * k >= 8));
+                        const uint32_t a1 = rule(in[k] >> 16, p1 * kPitch + at0 + (low + 2 * k + 1 >= 8));
+                        out[k] = ((todo >> (2 * k)) & 1u ? a0 : in[k] & 0xFFFFu) |
+                                 ((todo >> (2 * k + 1)) & 1u ? a1 << 16 : in[k] & 0xFFFF0000u);
+                    }
+                    w = make_uint4(out[0], out[1], out[2], out[3]);
+                    todo = 0u;
+                }
                 while (todo) {
                     const int i = __ffs(todo) - 1;
                     todo &= todo - 1;
                     const uint32_t old = i < 4 ? (i < 2 ? w.x : w.y) : (i < 6 ? w.z : w.w);
-                    const uint32_t raw = rule((i & 1) ? old >> 16 : old & 0xFFFFu, e0 + i);
+                    const uint32_t raw = rule((i & 1) ? old >> 16 : old & 0xFFFFu, place(e0 + i));
                     const uint32_t now = __byte_perm(old, raw, (i & 1) ? 0x5410 : 0x3254);
                     if (i < 2) w.x = now;
                     else if (i < 4) w.y = now;
                     else if (i < 6) w.z = now;
                     else w.w = now;
                 }
-                auto keep = [&](uint32_t v, int k) -> uint32_t {   // 16 bits per allowed bit, else -inf
-                    const uint32_t two = (allowed[u] >> (2 * k)) & 3u;
-                    const uint32_t m = (two & 1u) * 0xFFFFu + (two >> 1) * 0xFFFF0000u;
-                    return (v & m) | (0xFF80FF80u & ~m);
-                };
-                if (allowed[u] != 0xFFu) w = make_uint4(keep(w.x, 0), keep(w.y, 1), keep(w.z, 2), keep(w.w, 3));
-                uint16_t *dst = a.out + (col0 + j0 + u) * a.V + t;
-                if (kInner || (same_phase && t >= 0 && t + 8 <= a.V)) {
+                if (allowed[u] != 0xFFu) {
+                    // bit k of four to the top of byte k, then 16 copies of each
+                    // top bit: the words' masks
+                    const uint32_t lo = (allowed[u] & 15u) * 0x10204080u, hi = (allowed[u] >> 4) * 0x10204080u;
+                    auto keep = [](uint32_t v, uint32_t m) { return (v & m) | (0xFF80FF80u & ~m); };
+                    w.x = keep(w.x, copies(lo, 0x9988));
+                    w.y = keep(w.y, copies(lo, 0xBBAA));
+                    w.z = keep(w.z, copies(hi, 0x9988));
+                    w.w = keep(w.w, copies(hi, 0xBBAA));
+                }
+                uint16_t *dst = out0 + j * a.V + rel;
+                if (kInner || (same_phase && rel >= begin && rel + 8 <= end)) {
                     __stcs(reinterpret_cast<uint4 *>(dst), w);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t word = i < 4 ? (i < 2 ? w.x : w.y) : (i < 6 ? w.z : w.w);
-                        if (t + i >= 0 && t + i < a.V) dst[i] = (uint16_t)(word >> (16 * (i & 1)));
+                        if (rel + i >= begin && rel + i < end) dst[i] = (uint16_t)(word >> (16 * (i & 1)));
                     }
                 }
             }
