@@ -10,15 +10,21 @@
 
 namespace rules {
 
-constexpr int kThreads = 512;
-constexpr int kSlice = 8 * kThreads;     // tokens of a slice: one 16-byte vector a thread and column
-constexpr int kWindow = kSlice + 8;      // a column's vectors may start up to 7 elements before the slice
-constexpr int kBatch = 4;                // columns whose loads are in flight together
-// Counts and biases lie by token mod 8: element i of every thread's vector is
-// read by consecutive threads from consecutive words.
-constexpr int kPitch = kWindow / 8;
-__device__ __forceinline__ int place(int e) { return (e & 7) * kPitch + (e >> 3); }
-constexpr uint32_t kSeen = 0x80000000u;  // the token is in the prompt; the other bits count the output
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kSlice = 4096;             // tokens of a slice
+constexpr int kPieces = 4;               // of a slice: a warp works on one piece of one column at a time
+constexpr int kPiece = kSlice / kPieces;
+constexpr int kPer = kPiece / 8 / 32;    // 16-byte vectors a lane has in a piece
+constexpr int kWindow = kSlice + 8;      // a column's vectors may start up to 7 tokens before the slice
+constexpr int kRing = 2;                 // pieces a warp has in shared memory
+constexpr int kList = kPiece + 8;        // listed tokens of a piece, in any phase
+constexpr int kMaxCols = SPEC_MAX_GAMMA + 1;
+constexpr uint32_t kSeen = 0x80000000u;  // the token is in the prompt
+constexpr uint32_t kDraft = 0x40000000u; // the token is one of the drafts; the other bits count the output
+constexpr int32_t kNoId = INT32_MIN;        // an id of no window
+constexpr uint32_t kMasked = 0xFF80FF80u;   // two bf16 -inf
+static_assert(kWindow % 4 == 0, "");
+static_assert(kWarps % kPieces == 0, "a warp stays with one piece");
 
 struct Args {
     const uint16_t *logits;
@@ -38,8 +44,10 @@ struct Args {
     const int32_t *mask_rows;
 };
 
-struct Yes { static constexpr bool value = true; };
-struct No { static constexpr bool value = false; };
+// dynamic shared memory: the warps' rings, the counts, the lists, and the biases if any
+constexpr int kCountAt = kWarps * kRing * kPiece * 2, kListAt = kCountAt + kWindow * 4;
+constexpr int kBiasAt = kListAt + kPieces * kList * 2;
+constexpr int smem_bytes(bool biases) { return kBiasAt + (biases ? kWindow * 4 : 0); }
 
 __device__ __forceinline__ uint16_t to_bf16(float f)
 {
@@ -56,69 +64,166 @@ __device__ __forceinline__ uint32_t copies(uint32_t v, uint32_t selector)
     return d;
 }
 
+// One bulk copy shared -> global, and the bulk groups of the issuing thread.
+__device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// all but the newest n groups have read their shared memory
+template <int n>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(n) : "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 __device__ __forceinline__ int64_t clamp_len(int32_t n, int64_t most) { return n < 0 ? 0 : n > most ? most : n; }
 
-// One CTA per (slice of the vocabulary, lane): it counts the lane's history
-// over its slice in shared memory, then streams the slice of every column of
-// the lane.  A bit per token says whether anything but the mask can change it:
-// a vector none of whose tokens was seen costs one test, and only the seen
-// tokens of the others go through the rules, one after the other.  The mask is read first,
-// and a vector that it leaves nothing of is not read at all.
-__global__ void __launch_bounds__(kThreads, 3) process_kernel(const __grid_constant__ Args a)
+// One CTA per (slice of the vocabulary, lane).  It counts the lane's history
+// over its slice in shared memory and lists the tokens that anything but the
+// mask can change.  From there on its warps work alone, without barriers: a warp
+// takes one piece of the slice through the lane's columns, each piece brought
+// into the warp's ring by a bulk copy, its listed tokens rewritten and its vectors masked
+// in place, and taken out by a bulk copy, with the next pieces on
+// their way in.  Instructions so go to listed tokens and masks only.  (With every
+// vector in registers and tested for seen tokens, 64 x 16 columns of 248,046 took 243 us,
+// bound by instructions; with columns staged by the whole CTA 257 us, bound by barriers.)
+__global__ void __launch_bounds__(kThreads, 2) process_kernel(const __grid_constant__ Args a)
 {
-    __shared__ uint32_t count[kWindow];
-    __shared__ float bias[kWindow];
-    __shared__ uint32_t touched[kWindow / 32 + 2];
-    __shared__ int32_t draft_entry[SPEC_MAX_GAMMA + 1], mask_row[SPEC_MAX_GAMMA + 1];
-    const int tid = threadIdx.x;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint32_t *count = reinterpret_cast<uint32_t *>(smem + kCountAt);
+    uint16_t *lists = reinterpret_cast<uint16_t *>(smem + kListAt);   // [kPieces][kList]
+    float *bias = reinterpret_cast<float *>(smem + kBiasAt);          // only with biases
+    __shared__ uint32_t touched[kWindow / 32 + 1];
+    __shared__ int n_listed[kPieces];
+    __shared__ int32_t draft_entry[kMaxCols], mask_row[kMaxCols];
+    __shared__ uint64_t full[kWarps][kRing];
+    const int tid = threadIdx.x, warp = tid >> 5, wl = tid & 31;
     const int64_t lane = blockIdx.y, t0 = (int64_t)blockIdx.x * kSlice;
     const int64_t w0 = t0 - 8;   // the token of window entry 0
     pdl_launch_dependents();
-    for (int i = tid; i < kWindow; i += kThreads) {
-        count[i] = 0u;
-        bias[i] = 0.f;
+    {
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = tid; i < kWindow / 4; i += kThreads) {
+            reinterpret_cast<uint4 *>(count)[i] = zero;
+            if (a.bias_ids) reinterpret_cast<uint4 *>(bias)[i] = zero;
+        }
     }
-    if (tid < kWindow / 32 + 2) touched[tid] = 0u;
+    for (int i = tid; i < kWindow / 32 + 1; i += kThreads) touched[i] = 0u;
+    if (tid < kWarps * kRing) mbar_init(&full[0][0] + tid, 1);
+    if (tid == 0) s_gave_up = 0u;
+    fence_mbar_init();
     pdl_wait();
     __syncthreads();
 
-    auto entry = [&](int32_t id) -> int {   // window entry of an id, -1 outside
-        const int64_t e = (int64_t)id - w0;
-        return id >= 0 && id < a.V && e >= 0 && e < kWindow ? (int)e : -1;
+    // Vectors are 8 tokens, 16-byte aligned: the column's part of the slice starts
+    // at token t0 - mis.  Element i of piece q is token t0 - mis + q * kPiece + i.
+    const int64_t col0 = lane * a.cols;
+    const int mis0 = (int)(((reinterpret_cast<uintptr_t>(a.logits) & 15) / 2 + col0 * a.V + t0) & 7), v7 = (int)(a.V & 7);
+    const bool same_phase = ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
+    const int64_t left = a.V - t0;                        // tokens from t0 to the column's end
+    const int end = left > kSlice ? kSlice : (int)left, begin = t0 > 0 ? -8 : 0;   // tokens [begin, end) are the column's
+    const int piece = warp % kPieces, col_step = kWarps / kPieces, first_col = warp / kPieces;
+    struct Part {
+        int mis, lo, hi;   // elements [lo, hi) are the column's
+        int v0, v1;        // vectors wholly inside: by bulk copy (the rest token by token)
     };
-    auto touch = [&](int e) { atomicOr(&touched[e >> 5], 1u << (e & 31)); };
+    auto part = [&](int j) -> Part {
+        Part p;
+        p.mis = (mis0 + j * v7) & 7;
+        p.lo = begin + p.mis - piece * kPiece;
+        p.hi = end + p.mis - piece * kPiece;
+        p.v0 = p.lo > 0 ? 1 : 0;                          // lo is at most 7
+        const int n = p.hi >> 3;
+        p.v1 = n > kPiece / 8 ? kPiece / 8 : n < p.v0 ? p.v0 : n;
+        return p;
+    };
+    uint16_t *ring = reinterpret_cast<uint16_t *>(smem) + warp * kRing * kPiece;
+    auto offset = [&](int j, const Part &p) -> int64_t { return (col0 + j) * a.V + t0 - p.mis + piece * kPiece; };
+    auto fetch = [&](int k) {                              // the warp's k-th piece; one thread
+        const int j = first_col + k * col_step;
+        const Part p = part(j);
+        const uint32_t bytes = (uint32_t)(p.v1 - p.v0) * 16;
+        uint64_t *bar = &full[warp][k % kRing];
+        mbar_arrive_expect_tx(bar, bytes);
+        if (bytes) bulk_g2s(ring + (k % kRing) * kPiece + 8 * p.v0, a.logits + offset(j, p) + 8 * p.v0, bytes, bar);
+    };
+    const int mine = a.cols > first_col ? (a.cols - first_col + col_step - 1) / col_step : 0;   // pieces of this warp
+    if (wl == 0)
+        for (int k = 0; k < kRing && k < mine; ++k) fetch(k);
+
+    // Window entry of an id, or at least `limit`: one unsigned comparison keeps ids
+    // outside the window and the vocabulary out (where the window starts below
+    // zero, ids -8 .. -1 land on entries that are no column's).
+    const uint32_t limit = (uint32_t)(a.V - w0 < kWindow ? a.V - w0 : kWindow);
+    auto entry = [&](int32_t id) -> uint32_t { return (uint32_t)id - (uint32_t)w0; };
+    auto touch = [&](uint32_t e) {   // (common tokens set their bit once)
+        const uint32_t bit = 1u << (e & 31);
+        if (!(*reinterpret_cast<volatile uint32_t *>(&touched[e >> 5]) & bit)) atomicOr(&touched[e >> 5], bit);
+    };
     if (tid < a.cols) {
         // the draft that counts as output from column tid on; the column's mask
-        draft_entry[tid] = tid > 0 && a.drafts ? entry(__ldg(a.drafts + lane * (a.cols - 1) + tid - 1)) : -1;
+        const uint32_t e = tid > 0 && a.drafts ? entry(__ldg(a.drafts + lane * (a.cols - 1) + tid - 1)) : limit;
+        draft_entry[tid] = e < limit ? (int)e : -1;
+        if (e < limit) {
+            atomicOr(&count[e], kDraft);
+            touch(e);
+        }
         const int32_t row = a.mask ? __ldg(a.mask_rows + lane * a.cols + tid) : -1;
         mask_row[tid] = row >= 0 && row < a.mask_count ? row : -1;
     }
     if (a.history) {
+        const int32_t *h = a.history + lane * a.history_stride;
         const int64_t whole = clamp_len(__ldg(a.history_lens + lane), a.history_stride);
         const int64_t prompt = clamp_len(__ldg(a.prompt_lens + lane), whole);
-        const int32_t *h = a.history + lane * a.history_stride;
-        constexpr int kAhead = 8;   // ids in flight a thread
-        for (int64_t i0 = tid; i0 < whole; i0 += kAhead * kThreads) {
-            int32_t id[kAhead];
+        auto met = [&](int32_t id, int64_t i) {
+            const uint32_t e = entry(id);
+            if (e < limit) {
+                if (i < prompt) atomicOr(&count[e], kSeen);
+                else atomicAdd(&count[e], 1u);
+                touch(e);
+            }
+        };
+        // Four ids a load from the first 16-byte boundary on, kAhead loads in
+        // flight.  Few ids fall into the slice: a bit each, and the code that counts
+        // one stands once (unrolled for every id it was 13 KB, and
+        // fetching it took a CTA 3 us).
+        const int64_t head0 = (16 - (reinterpret_cast<uintptr_t>(h) & 15)) / 4 % 4, head = head0 < whole ? head0 : whole;
+        const int64_t quads = (whole - head) / 4;
+        const int4 *h4 = reinterpret_cast<const int4 *>(h + head);
+        constexpr int kAhead = 8;
+#pragma unroll 1
+        for (int64_t q = tid; q < quads; q += kAhead * kThreads) {
+            int4 id[kAhead];
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) id[u] = i0 + u * kThreads < whole ? __ldg(h + i0 + u * kThreads) : -1;
+            for (int u = 0; u < kAhead; ++u)
+                id[u] = q + u * kThreads < quads ? __ldg(h4 + q + u * kThreads) : make_int4(kNoId, kNoId, kNoId, kNoId);
+            uint32_t hits = 0u;
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int e = entry(id[u]);
-                if (e >= 0) {
-                    if (i0 + u * kThreads < prompt) atomicOr(&count[place(e)], kSeen);
-                    else atomicAdd(&count[place(e)], 1u);
-                    touch(e);
-                }
+            for (int u = 0; u < kAhead; ++u)
+                hits |= (entry(id[u].x) < limit ? 1u << (4 * u) : 0u) | (entry(id[u].y) < limit ? 2u << (4 * u) : 0u) |
+                        (entry(id[u].z) < limit ? 4u << (4 * u) : 0u) | (entry(id[u].w) < limit ? 8u << (4 * u) : 0u);
+#pragma unroll 1
+            while (hits) {
+                const int u = (__ffs(hits) - 1) >> 2;
+                const uint32_t some = hits >> (4 * u);
+                const int64_t at = q + u * kThreads, i = head + 4 * at;
+                const int4 four = __ldg(h4 + at);         // (from L1)
+                if (some & 1u) met(four.x, i);
+                if (some & 2u) met(four.y, i + 1);
+                if (some & 4u) met(four.z, i + 2);
+                if (some & 8u) met(four.w, i + 3);
+                hits &= ~(15u << (4 * u));
             }
         }
+        const int64_t tail = head + 4 * quads, i = tid < head ? tid : tail + tid - head;
+        if (i < whole && (tid < head || i >= tail)) met(__ldg(h + i), i);
     }
     if (a.bias_ids) {
         const int64_t nb = clamp_len(__ldg(a.bias_lens + lane), a.max_bias);
         for (int64_t i = tid; i < nb; i += kThreads) {
-            const int e = entry(__ldg(a.bias_ids + lane * a.max_bias + i));
-            if (e >= 0) {
-                atomicAdd(&bias[place(e)], __ldg(a.bias_vals + lane * a.max_bias + i));
+            const uint32_t e = entry(__ldg(a.bias_ids + lane * a.max_bias + i));
+            if (e < limit) {
+                atomicAdd(&bias[e], __ldg(a.bias_vals + lane * a.max_bias + i));
                 touch(e);
             }
         }
@@ -130,130 +235,132 @@ __global__ void __launch_bounds__(kThreads, 3) process_kernel(const __grid_const
         p = __ldg(a.penalties + 3 * lane + 2);
     }
     const float over_r = 1.f / r;   // one divide a lane; x * (1 / r) is within 1.5 fp32 units of x / r
+    const int64_t words = (a.V + 31) / 32;
+    const uint32_t *mask0 = a.mask ? a.mask + (t0 >> 5) : nullptr;
     __syncthreads();
 
-    auto rule = [&](uint32_t raw, int at) -> uint32_t {   // at: the token's place
-        const uint32_t c = count[at], n = c & ~kSeen;
-        const float x = bf16_as_float(raw);
-        const float y = __fmul_rn(x, c == 0u ? 1.f : x > 0.f ? over_r : r);
-        const float z = __fsub_rn(y, __fadd_rn(__fmul_rn(f, (float)n), n ? p : 0.f));
-        return to_bf16(__fadd_rn(z, bias[at]));
-    };
-    const int64_t words = (a.V + 31) / 32;
-    const bool same_phase = ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
-    const int base_mis = (int)((reinterpret_cast<uintptr_t>(a.logits) & 15) / 2);
-    const int64_t col0 = lane * a.cols;
-
-    // A vector starts at token t0 + rel of its column; rel = 8 * tid - mis, where
-    // mis (the same for the whole CTA) is the column's phase.
-    const uint16_t *in0 = a.logits + col0 * a.V + t0;
-    uint16_t *out0 = a.out + col0 * a.V + t0;
-    const uint32_t *mask0 = a.mask ? a.mask + (t0 >> 5) : nullptr;
-    const int mis0 = (int)((base_mis + col0 * a.V + t0) & 7), v7 = (int)(a.V & 7);
-    const int64_t left = a.V - t0;                  // tokens from t0 to the column's end
-    const int end = left > kSlice ? kSlice + 8 : (int)left, begin = t0 > 0 ? -8 : 0;   // tokens [begin, end) are the column's
-
-    // kInner: no vector of the slice reaches over an end of its column, in
-    // whatever phase, and input and output vectors line up
-    auto stream = [&](auto inner) {
-        constexpr bool kInner = decltype(inner)::value;
-        for (int j0 = 0; j0 < a.cols; j0 += kBatch) {
-            uint4 x[kBatch];
-            uint32_t allowed[kBatch];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                allowed[u] = 0xFFu;
-                const int j = j0 + u, row = j < a.cols ? mask_row[j] : -1;
-                if (row < 0) continue;
-                const int rel = 8 * tid - ((mis0 + j * v7) & 7), w = rel >> 5;   // w: floor, also below 0
-                const uint32_t *m = mask0 + row * words + w;
-                uint32_t lo = 0u, hi = 0u;
-                if (kInner || (rel < end && (t0 > 0 || w >= 0))) lo = __ldg(m);
-                if ((rel & 31) > 24 && (kInner || 32 * (w + 1) < end)) hi = __ldg(m + 1);
-                allowed[u] = __funnelshift_r(lo, hi, (uint32_t)(rel & 31)) & 0xFFu;
-            }
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                x[u] = make_uint4(0, 0, 0, 0);
-                const int j = j0 + u;
-                if (j >= a.cols || allowed[u] == 0u) continue;
-                const int rel = 8 * tid - ((mis0 + j * v7) & 7);
-                const uint16_t *src = in0 + j * a.V + rel;
-                if (kInner || (rel >= begin && rel + 8 <= end)) x[u] = __ldcs(reinterpret_cast<const uint4 *>(src));
-                else if (rel + 8 > begin && rel < end) x[u] = load_edge(src, 0, 0, begin - rel, end - rel);
-            }
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int j = j0 + u;
-                if (j >= a.cols) break;
-                const int e = draft_entry[j];
-                if (e >= 0) {          // the same for the whole CTA
-                    __syncthreads();
-                    if (tid == 0) {
-                        count[place(e)] += 1u;
-                        touched[e >> 5] |= 1u << (e & 31);
-                    }
-                    __syncthreads();
-                }
-                const int rel = 8 * tid - ((mis0 + j * v7) & 7);
-                if (!kInner && (rel + 8 <= begin || rel >= end)) continue;
-                const int e0 = rel + 8;
-                uint32_t todo = __funnelshift_r(touched[e0 >> 5], touched[(e0 >> 5) + 1], (uint32_t)(e0 & 31)) & allowed[u];
-                uint4 w = x[u];
-                // many seen tokens in one of the warp's vectors: all eight of
-                // each at once, so that their reads overlap (a vector with few goes
-                // one by one: a third of the instructions)
-                if (__any_sync(__activemask(), __popc(todo) > 2)) {
-                    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t out[4];
-                    const int low = e0 & 7, at0 = e0 >> 3;   // low: the same for every thread
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int p0 = (low + 2 * k) & 7, p1 = (low + 2 * k + 1) & 7;
-                        const uint32_t a0 = rule(in[k] & 0xFFFFu, p0 * kPitch + at0 + (low + 2 * k >= 8));
-                        const uint32_t a1 = rule(in[k] >> 16, p1 * kPitch + at0 + (low + 2 * k + 1 >= 8));
-                        out[k] = ((todo >> (2 * k)) & 1u ? a0 : in[k] & 0xFFFFu) |
-                                 ((todo >> (2 * k + 1)) & 1u ? a1 << 16 : in[k] & 0xFFFF0000u);
-                    }
-                    w = make_uint4(out[0], out[1], out[2], out[3]);
-                    todo = 0u;
-                }
-                while (todo) {
-                    const int i = __ffs(todo) - 1;
-                    todo &= todo - 1;
-                    const uint32_t old = i < 4 ? (i < 2 ? w.x : w.y) : (i < 6 ? w.z : w.w);
-                    const uint32_t raw = rule((i & 1) ? old >> 16 : old & 0xFFFFu, place(e0 + i));
-                    const uint32_t now = __byte_perm(old, raw, (i & 1) ? 0x5410 : 0x3254);
-                    if (i < 2) w.x = now;
-                    else if (i < 4) w.y = now;
-                    else if (i < 6) w.z = now;
-                    else w.w = now;
-                }
-                if (allowed[u] != 0xFFu) {
-                    // bit k of four to the top of byte k, then 16 copies of each
-                    // top bit: the words' masks
-                    const uint32_t lo = (allowed[u] & 15u) * 0x10204080u, hi = (allowed[u] >> 4) * 0x10204080u;
-                    auto keep = [](uint32_t v, uint32_t m) { return (v & m) | (0xFF80FF80u & ~m); };
-                    w.x = keep(w.x, copies(lo, 0x9988));
-                    w.y = keep(w.y, copies(lo, 0xBBAA));
-                    w.z = keep(w.z, copies(hi, 0x9988));
-                    w.w = keep(w.w, copies(hi, 0xBBAA));
-                }
-                uint16_t *dst = out0 + j * a.V + rel;
-                if (kInner || (same_phase && rel >= begin && rel + 8 <= end)) {
-                    __stcs(reinterpret_cast<uint4 *>(dst), w);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t word = i < 4 ? (i < 2 ? w.x : w.y) : (i < 6 ? w.z : w.w);
-                        if (rel + i >= begin && rel + i < end) dst[i] = (uint16_t)(word >> (16 * (i & 1)));
-                    }
-                }
+    // The pieces' lists, in order, from the bits.  Entry e is element e - 8 + mis
+    // of the slice: a piece's list has the first eight entries of the next piece too.
+    uint16_t *list = lists + piece * kList;
+    if (warp < kPieces) {
+        constexpr int kBits = kPiece / 32;
+        const uint32_t *bits = touched + piece * kBits;
+        int n = 0;
+        for (int w0 = 0; w0 <= kBits; w0 += 32) {
+            uint32_t own = w0 + wl < kBits ? bits[w0 + wl] : w0 + wl == kBits ? bits[kBits] & 0xFFu : 0u;
+            for (uint32_t some = __ballot_sync(kFull, own != 0u); some; some &= some - 1) {
+                const int w = __ffs(some) - 1;
+                const uint32_t word = __shfl_sync(kFull, own, w);
+                if ((word >> wl) & 1u) list[n + __popc(word & lanemask_lt())] = (uint16_t)(piece * kPiece + 32 * (w0 + w) + wl);
+                n += __popc(word);
             }
         }
+        if (wl == 0) n_listed[piece] = n;
+    }
+    __syncthreads();
+    const int n = n_listed[piece];
+
+    // The mask words of a lane's vectors, a piece ahead of their use (a column's
+    // mask lies in memory of its own, read once).
+    auto mask_words = [&](int k, uint2 (&m)[kPer]) {
+        const int j = first_col + k * col_step, row = k < mine ? mask_row[j] : -1;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) m[u] = make_uint2(~0u, ~0u);
+        if (row < 0) return;
+        const int rel = piece * kPiece + 8 * wl - ((mis0 + j * v7) & 7), w = rel >> 5;   // w: floor, also below 0
+        const uint32_t *q = mask0 + row * words + w;
+        const bool both = (rel & 31) > 24;                // a vector's bits lie in two words
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            if (rel + 256 * u >= end) break;
+            if (u > 0 || t0 > 0 || w >= 0) m[u].x = __ldg(q + 8 * u);
+            if (both && 32 * (w + 8 * u + 1) < end) m[u].y = __ldg(q + 8 * u + 1);
+        }
     };
-    if (same_phase && t0 >= 8 && t0 + kSlice <= a.V) stream(Yes());
-    else stream(No());
+    uint2 words_now[kPer], words_next[kPer];
+    mask_words(0, words_now);
+    for (int k = 0; k < mine; ++k) {
+        const int j = first_col + k * col_step, row = mask_row[j];
+        const Part pt = part(j);
+        const int64_t at0 = offset(j, pt);
+        uint16_t *x = ring + (k % kRing) * kPiece;
+        mask_words(k + 1, words_next);
+        mbar_wait(&full[warp][k % kRing], (k / kRing) & 1);
+        if (pt.v0 > 0 || pt.v1 < kPiece / 8) {             // the ends of the column
+            const int e = wl < 8 ? 8 * (pt.v0 - 1) + wl : 8 * pt.v1 + wl - 8;
+            if (wl < 16 && e >= 0 && e < kPiece && e >= pt.lo && e < pt.hi) x[e] = a.logits[at0 + e];
+            __syncwarp();
+        }
+        const int first = pt.lo > 0 ? pt.lo : 0, many = (pt.hi < kPiece ? pt.hi : kPiece) - first;
+#pragma unroll 1
+        for (int i = wl; i < n; i += 32) {
+            const int e = list[i], at = e - 8 + pt.mis - piece * kPiece;
+            if ((uint32_t)(at - first) >= (uint32_t)many || many <= 0) continue;
+            const uint32_t c = count[e];
+            uint32_t m = c & ~(kSeen | kDraft);
+            if (c & kDraft)                                // its count grows along the columns
+                for (int d = 1; d <= j; ++d) m += draft_entry[d] == e;
+            const float v = bf16_as_float(x[at]);
+            const float factor = (c & kSeen) || m ? (v > 0.f ? over_r : r) : 1.f;
+            const float take = __fadd_rn(__fmul_rn(f, (float)m), m ? p : 0.f);
+            const float z = __fsub_rn(__fmul_rn(v, factor), take);
+            x[at] = to_bf16(a.bias_ids ? __fadd_rn(z, bias[e]) : z);
+        }
+        if (row >= 0) {
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) {
+                const uint32_t allowed = __funnelshift_r(words_now[u].x, words_now[u].y, (uint32_t)(8 * wl - pt.mis) & 31u) & 0xFFu;
+                if (allowed == 0xFFu || 8 * (wl + 32 * u) >= pt.hi) continue;
+                uint4 *at = reinterpret_cast<uint4 *>(x) + wl + 32 * u;
+                uint4 q = make_uint4(kMasked, kMasked, kMasked, kMasked);
+                if (allowed != 0u) {
+                    q = *at;
+                    // bit k of four to the top of byte k, then 16 copies of each top bit: the words' masks
+                    const uint32_t l = (allowed & 15u) * 0x10204080u, h = (allowed >> 4) * 0x10204080u;
+                    auto keep = [](uint32_t w, uint32_t m) { return (w & m) | (kMasked & ~m); };
+                    q.x = keep(q.x, copies(l, 0x9988));
+                    q.y = keep(q.y, copies(l, 0xBBAA));
+                    q.z = keep(q.z, copies(h, 0x9988));
+                    q.w = keep(q.w, copies(h, 0xBBAA));
+                }
+                *at = q;
+            }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (same_phase) {
+            if (pt.v0 > 0 || pt.v1 < kPiece / 8) {
+                const int e = wl < 8 ? 8 * (pt.v0 - 1) + wl : 8 * pt.v1 + wl - 8;
+                if (wl < 16 && e >= 0 && e < kPiece && e >= pt.lo && e < pt.hi) a.out[at0 + e] = x[e];
+            }
+            if (wl == 0) {
+                if (pt.v1 > pt.v0) bulk_s2g(a.out + at0 + 8 * pt.v0, x + 8 * pt.v0, (uint32_t)(pt.v1 - pt.v0) * 16);
+                bulk_commit();                             // a group a piece, empty or not
+            }
+        } else {
+            for (int e = wl; e < kPiece; e += 32)
+                if (e >= pt.lo && e < pt.hi) a.out[at0 + e] = x[e];
+        }
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) words_now[u] = words_next[u];
+        // The place of the piece before this one takes the next load: its store has
+        // had this piece's time to read it, and the warp's own reads are past a
+        // barrier (and a proxy fence).
+        if (wl == 0 && k > 0 && k - 1 + kRing < mine) {
+            bulk_wait_read<1>();
+            fetch(k - 1 + kRing);
+        }
+    }
+    if (wl == 0) {
+        bulk_wait_all();
+        // given up on a load: it may still be on its way into this CTA's memory (bounded)
+        if (*reinterpret_cast<volatile unsigned int *>(&s_gave_up))
+            for (int k = mine > kRing ? mine - kRing : 0; k < mine; ++k) {
+                const uint64_t since = global_ns();
+                while (!mbar_try_wait(&full[warp][k % kRing], (k / kRing) & 1) && global_ns() - since < kWaitLimitNs) {}
+            }
+    }
 }
 
 }  // namespace rules

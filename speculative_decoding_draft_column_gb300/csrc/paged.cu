@@ -81,6 +81,8 @@ spec_status device(Device **out)
         e = cudaFuncSetAttribute(paged::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  2 * (SPEC_PAGED_MAX_LANES + 1) * 8);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+        e = cudaFuncSetAttribute(rules::process_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, rules::smem_bytes(true));
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
         int smem_max = 0;
         e = cudaDeviceGetAttribute(&smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
         if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
@@ -371,7 +373,7 @@ spec_status spec_logits_process(const uint16_t *logits, int64_t lanes, int32_t c
     rules::Args a = {logits, out, lanes, V, cols, history, history_stride, prompt_lens, history_lens, drafts,
                      penalties, bias_ids, bias_vals, max_bias, bias_lens, mask, mask_count, mask_rows};
     const unsigned slices = (unsigned)((V + 7 + rules::kSlice - 1) / rules::kSlice);
-    return launch(rules::process_kernel, dim3(slices, (unsigned)lanes), rules::kThreads, 0, a);
+    return launch(rules::process_kernel, dim3(slices, (unsigned)lanes), rules::kThreads, (size_t)rules::smem_bytes(bias_ids != nullptr), a);
 }
 
 }  // extern "C"
