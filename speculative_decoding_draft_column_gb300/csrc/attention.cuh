@@ -75,6 +75,40 @@ struct Args {
     float *parts;          // [grid][2][kPartFloats]
 };
 
+// mbar_wait without the long suspension hint: the waits of this kernel's pipeline
+// are a fraction of a microsecond each, on the critical path.  Bounded like it.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity)
+{
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_test(bar, parity)) return true;
+        if (*reinterpret_cast<volatile unsigned int *>(&s_gave_up)) return false;
+        if (global_ns() - t0 > kWaitLimitNs) {
+            s_gave_up = 1u;
+            atomicOr(&g_wait_timeouts, 1u);
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity)
+{
+    for (int i = 0; i < 16; ++i)
+        if (mbar_test(bar, parity)) return true;
+    return wait_slow(bar, parity);
+}
+
 // ---- tcgen05 ----------------------------------------------------------------
 
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot)
@@ -96,19 +130,38 @@ __device__ __forceinline__ void commit(uint64_t *bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
+// Operand descriptors travel as their low words (address and leading offset);
+// the high word is the same for all.  One elected thread issues 16 products a unit,
+// so what it computes between them counts.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // rows 1,024 bytes a group of 8; version; 128-byte swizzle
+template <bool kAcc>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-                 "r"((uint32_t)acc)
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+                 "setp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+                 "n"(kAcc ? 1 : 0), "n"(kDescHi)
                  : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-                 "r"((uint32_t)acc)
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %5};\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+                 "r"((uint32_t)acc), "n"(kDescHi)
                  : "memory");
+}
+__device__ __forceinline__ void mma_ts_acc(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %5};\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+                 "n"(1), "n"(kDescHi)
+                 : "memory");
+}
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 #define R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
@@ -125,15 +178,20 @@ __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t a)
                  : "r"(a)
                  : "memory");
 }
-__device__ __forceinline__ void tmem_ld64(uint32_t (&r)[64], uint32_t a)
+// The load alone, and the wait for it: the values pass through the wait, so that
+// no use of them can move before it.
+__device__ __forceinline__ void tmem_issue32(uint32_t (&r)[32], uint32_t a)
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,"
-                 "%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, "
-                 "[%64];\n\ttcgen05.wait::ld.sync.aligned;"
-                 : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24), R8(r, 32), R8(r, 40), R8(r, 48), R8(r, 56)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24)
                  : "r"(a)
                  : "memory");
+}
+#define M8(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7])
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : M8(r, 0), M8(r, 8), M8(r, 16), M8(r, 24)::"memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32])
 {
@@ -142,26 +200,53 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32])
                  I8(r, 24), "r"(a)
                  : "memory");
 }
-// 64 columns of a row's scores; on an edge tile those outside [from, to) are -inf
-__device__ __forceinline__ void load_scores(uint32_t (&x)[64], uint32_t a, bool edge, int from, int to)
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16])
 {
-    tmem_ld64(x, a);
-    if (edge) {
-#pragma unroll
-        for (int e = 0; e < 64; ++e)
-            if (e < from || e >= to) x[e] = 0xFF800000u;
-    }
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+                 "%15};" ::I8(r, 0), I8(r, 8), "r"(a)
+                 : "memory");
 }
 
-// Shared-memory operand descriptor, 128-byte swizzle.  Rows of 128 bytes in
-// groups of 8 (1,024 bytes apart: the stride offset).  For K-major operands the
-// leading offset is unused; for the MN-major V it is the distance between blocks of 64
-// head elements.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading)
+// On an edge tile the scores outside [from, to) of 32 are -inf.
+__device__ __forceinline__ void mask_scores(uint32_t (&x)[32], int from, int to)
 {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (e < from || e >= to) x[e] = 0xFF800000u;
 }
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t two(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void halves(uint64_t v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Low word of a shared-memory operand descriptor.  Rows of 128 bytes in groups of
+// 8; for K-major operands the leading offset is unused, for the MN-major V it is the
+// distance between blocks of 64 head elements.
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t leading) { return ((addr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16); }
 
 // Instruction descriptor: fp32 accumulator, A and B both bf16 or both fp16, M =
 // 128, N columns, B K-major or MN-major.
@@ -448,7 +533,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++idx) {
                     const uint32_t st = idx % S::kStages, use = idx / S::kStages;
-                    ok = ok && mbar_wait(&bar.empty[st], (use & 1) ^ 1);
+                    ok = ok && wait(&bar.empty[st], (use & 1) ^ 1);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
                     if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], bytes);
@@ -475,54 +560,69 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             }
         }
     } else if (warp == kMma) {
-        // ---- the products, issued by one thread
-        if (lane == 0) {
-            constexpr uint32_t kQk = instr(F16, S::BK, false), kPv = instr(F16, D, true);
-            uint32_t tile_n = 0, items = 0, units[2] = {0, 0};   // tiles, items so far; units per S buffer
-            bool ok = true;
-            Segment s;
-            const uint32_t q0 = smem_u32(q_smem), kv0 = smem_u32(kv_smem);
-            while (ok && next_segment<S>(a, run, s)) {
-                const int U = QT == 2 ? 2 * s.tiles : s.tiles;
-                auto qk = [&](int i) -> bool {
-                    const uint32_t t = tile_n + (QT == 2 ? i >> 1 : i), idx = 2 * t, st = idx % S::kStages;
-                    const int b = i & 1;
-                    if (!mbar_wait(&bar.full[st], (idx / S::kStages) & 1)) return false;
-                    fence_after();
-                    const uint32_t qa = q0 + (QT == 2 ? b * S::kQBytes : 0), ka = kv0 + st * S::kStageBytes;
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_ss(tmem + b * S::BK, operand(qa + (k >> 2) * (128 * 128) + (k & 3) * 32, 16),
-                               operand(ka + (k >> 2) * (S::BK * 128) + (k & 3) * 32, 16), kQk, k > 0);
-                    commit(&bar.s_full[b]);
-                    if (QT == 1 || b == 1) commit(&bar.empty[st]);
-                    return true;
-                };
-                ok = mbar_wait(&bar.q_full, items & 1);
-                fence_after();
-                ok = ok && qk(0);
-                for (int i = 0; i < U && ok; ++i) {
-                    if (i + 1 < U) ok = qk(i + 1);
-                    const uint32_t t = tile_n + (QT == 2 ? i >> 1 : i), idx = 2 * t + 1, st = idx % S::kStages;
-                    const int b = i & 1, ob = S::NS == 2 ? b : 0;
-                    ok = ok && mbar_wait(&bar.p_full[b], units[b] & 1);
-                    ok = ok && mbar_wait(&bar.full[st], (idx / S::kStages) & 1);
-                    if (!ok) break;
-                    ++units[b];
-                    fence_after();
-                    const uint32_t va = kv0 + st * S::kStageBytes;
-                    const bool first = S::NS == 2 ? i < 2 : i < 1;
-#pragma unroll
-                    for (int k = 0; k < S::BK / 16; ++k)
-                        mma_ts(tmem + S::kO + ob * D, tmem + b * S::BK + k * 8, operand(va + k * 2048, S::BK * 128), kPv,
-                               !first || k > 0);
-                    commit(&bar.o_done[ob]);
-                    if (QT == 1 || b == 1) commit(&bar.empty[st]);
-                }
-                tile_n += s.tiles;
-                ++items;
+        // ---- the products, issued by one thread (the warp walks along with it)
+        constexpr uint32_t kQk = instr(F16, S::BK, false), kPv = instr(F16, D, true);
+        const bool leader = elect_one();
+        uint32_t items = 0, units[2] = {0, 0};               // items so far; units per S buffer
+        uint32_t k_stage = 0, k_phase = 0, v_stage = 1, v_phase = 0;   // of the next K and V tile (every second stage use)
+        static_assert(S::kStages >= 3, "");
+        auto advance = [](uint32_t &st, uint32_t &ph) {
+            st += 2;
+            if (st >= (uint32_t)S::kStages) {
+                st -= S::kStages;
+                ph ^= 1;
             }
-            // everything issued is complete before TMEM is freed
+        };
+        bool ok = true;
+        Segment s;
+        const uint32_t q_desc = operand(smem_u32(q_smem), 16), k_desc = operand(smem_u32(kv_smem), 16),
+                       v_desc = operand(smem_u32(kv_smem), S::BK * 128);
+        while (ok && next_segment<S>(a, run, s)) {
+            const int U = QT == 2 ? 2 * s.tiles : s.tiles;
+            auto qk = [&](int i) -> bool {
+                const int b = i & 1;
+                if (!wait(&bar.full[k_stage], k_phase)) return false;
+                fence_after();
+                if (leader) {
+                    const uint32_t qa = q_desc + (QT == 2 ? b * (S::kQBytes >> 4) : 0), ka = k_desc + k_stage * (S::kStageBytes >> 4);
+                    const uint32_t d = tmem + b * S::BK;
+                    mma_ss<false>(d, qa, ka, kQk);
+#pragma unroll
+                    for (int k = 1; k < D / 16; ++k)
+                        mma_ss<true>(d, qa + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, ka + (k >> 2) * (S::BK * 128 >> 4) + (k & 3) * 2, kQk);
+                    commit(&bar.s_full[b]);
+                    if (QT == 1 || b == 1) commit(&bar.empty[k_stage]);
+                }
+                __syncwarp();
+                if (QT == 1 || b == 1) advance(k_stage, k_phase);
+                return true;
+            };
+            ok = wait(&bar.q_full, items & 1);
+            fence_after();
+            ok = ok && qk(0);
+            for (int i = 0; i < U && ok; ++i) {
+                if (i + 1 < U) ok = qk(i + 1);
+                const int b = i & 1, ob = S::NS == 2 ? b : 0;
+                ok = ok && wait(&bar.full[v_stage], v_phase);
+                ok = ok && wait(&bar.p_full[b], units[b] & 1);
+                if (!ok) break;
+                ++units[b];
+                fence_after();
+                if (leader) {
+                    const uint32_t va = v_desc + v_stage * (S::kStageBytes >> 4), d = tmem + S::kO + ob * D, pa = tmem + b * S::BK;
+                    mma_ts(d, pa, va, kPv, S::NS == 2 ? i >= 2 : i >= 1);
+#pragma unroll
+                    for (int k = 1; k < S::BK / 16; ++k) mma_ts_acc(d, pa + k * 8, va + k * (2048 >> 4), kPv);
+                    commit(&bar.o_done[ob]);
+                    if (QT == 1 || b == 1) commit(&bar.empty[v_stage]);
+                }
+                __syncwarp();
+                if (QT == 1 || b == 1) advance(v_stage, v_phase);
+            }
+            ++items;
+        }
+        // everything issued is complete before TMEM is freed
+        if (leader) {
             commit(&bar.drain);
             const uint64_t t0 = global_ns();
             while (!mbar_try_wait(&bar.drain, 0) && global_ns() - t0 < kWaitLimitNs) {}
@@ -572,33 +672,46 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 const int t = QT == 2 || S::NS == 1 ? i : 2 * i + st;
                 const int b = S::NS == 2 ? st : i & 1;
                 const int key0 = (s.tile + t) * S::BK;
-                mbar_wait(&bar.s_full[b], s_n[b] & 1);
+                wait(&bar.s_full[b], s_n[b] & 1);
                 ++s_n[b];
                 fence_after();
                 if (live) {
                     const uint32_t sa = tmem + lane_base + b * S::BK;
-                    const int from = klo - key0, to = khi - key0;   // columns of this row in the tile
+                    // columns of this row in the tile; what a row past the item's holds is nobody's
+                    const int from = valid ? klo - key0 : 0, to = valid ? khi - key0 : S::BK;
                     const bool edge = __any_sync(kFull, from > 0 || to < S::BK);
-                    // two passes over S in TMEM, 64 columns at a time (a row's
-                    // whole tile in registers would spill)
-                    float top = -INFINITY;
+                    // Two passes over S in TMEM, 32 columns at a time with the next 32
+                    // on their way (a row's whole tile in registers would spill).
+                    uint32_t xa[32], xb[32];
+                    float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto top_of = [&](uint32_t (&x)[32], int c) {
+                        if (edge) mask_scores(x, from - c, to - c);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                top4[k] = max3(top4[k], __uint_as_float(x[e + k]), __uint_as_float(x[e + 4 + k]));
+                    };
+                    tmem_issue32(xa, sa);
 #pragma unroll
                     for (int c = 0; c < S::BK; c += 64) {
-                        uint32_t x[64];
-                        load_scores(x, sa + c, edge, from - c, to - c);
-#pragma unroll
-                        for (int e = 0; e < 64; e += 2)
-                            top = fmaxf(top, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+                        tmem_wait32(xa);
+                        tmem_issue32(xb, sa + c + 32);
+                        top_of(xa, c);
+                        tmem_wait32(xb);
+                        tmem_issue32(xa, c + 64 < S::BK ? sa + c + 64 : sa);   // at the end: the second pass's first
+                        top_of(xb, c + 32);
                     }
+                    float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
                     top *= a.c;
                     // a new reference only past the lag (or for a row's first key)
-                    const bool move = top > m + kLag || (m == -INFINITY && top > -INFINITY);
+                    const bool move = valid && (top > m + kLag || (m == -INFINITY && top > -INFINITY));
                     if (__any_sync(kFull, move)) {
                         const float f = move ? exp2_fast(m - top) : 1.f;
                         if (move) m = top;
                         l *= f;
                         if (done > 0) {
-                            mbar_wait(&bar.o_done[st], (pv_n - 1) & 1);
+                            wait(&bar.o_done[st], (pv_n - 1) & 1);
                             fence_after();
                             const uint32_t oa = tmem + lane_base + S::kO + st * D;
 #pragma unroll 1
@@ -612,28 +725,41 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m;
-                    float sum = 0.f;
+                    const uint64_t cc = two(a.c, a.c), mm = two(-ref, -ref);
+                    uint64_t sum[2] = {0ull, 0ull};
+                    // P of columns c .. c+31 covers columns c/2 .. c/2+15 of S, read before
+                    auto weights = [&](uint32_t (&x)[32], int c) {
+                        if (edge) mask_scores(x, from - c, to - c);
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int c = 0; c < S::BK; c += 64) {
-                        // P of columns c .. c+63 covers columns c/2 .. c/2+31 of S, read before
-                        uint32_t x[64], pk[32];
-                        load_scores(x, sa + c, edge, from - c, to - c);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float p0 = exp2_fast(fmaf(__uint_as_float(x[2 * e]), a.c, -ref));
-                            const float p1 = exp2_fast(fmaf(__uint_as_float(x[2 * e + 1]), a.c, -ref));
-                            sum += p0 + p1;
+                        for (int e = 0; e < 16; ++e) {
+                            float p0, p1;
+                            halves(fma2(two(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), cc, mm), p0, p1);
+                            p0 = exp2_fast(p0);
+                            p1 = exp2_fast(p1);
+                            sum[e & 1] = add2(sum[e & 1], two(p0, p1));
                             pk[e] = pack2<F16>(p0, p1);
                         }
-                        tmem_st32(sa + c / 2, pk);
+                        tmem_st16(sa + c / 2, pk);
+                    };
+#pragma unroll
+                    for (int c = 0; c < S::BK; c += 64) {
+                        tmem_wait32(xa);
+                        tmem_issue32(xb, sa + c + 32);
+                        weights(xa, c);
+                        tmem_wait32(xb);
+                        if (c + 64 < S::BK) tmem_issue32(xa, sa + c + 64);
+                        weights(xb, c + 32);
                     }
-                    l += sum;
+                    float s0, s1;
+                    halves(add2(sum[0], sum[1]), s0, s1);
+                    l += s0 + s1;
                 }
                 // V rows that no row of the item may see hold anything, NaN
                 // included: 0 * NaN must not reach O
                 if (key0 < s.r.lo || key0 + S::BK > s.r.hi) {
                     const uint32_t idx = 2 * (tile_n + t) + 1, vs = idx % S::kStages;
-                    mbar_wait(&bar.full[vs], (idx / S::kStages) & 1);
+                    wait(&bar.full[vs], (idx / S::kStages) & 1);
                     uint8_t *v = kv_smem + vs * S::kStageBytes;
                     constexpr int kPer = 128 / S::BK;               // threads of a key row
                     const int kr = row / kPer, part = row % kPer;
@@ -650,7 +776,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 // product before it, and a barrier's parity tells only its last two phases
                 // apart, so that every phase is waited for.  (With two streams, S of a
                 // stream's unit comes after its last product.)
-                if (S::NS == 1 && done > 0) mbar_wait(&bar.o_done[st], (pv_n - 1) & 1);
+                if (S::NS == 1 && done > 0) wait(&bar.o_done[st], (pv_n - 1) & 1);
                 wait_st();
                 fence_before();
                 __syncwarp();
@@ -658,7 +784,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 ++pv_n;
             }
             tile_n += s.tiles;
-            if (U > 0) mbar_wait(&bar.o_done[st], (pv_n - 1) & 1);
+            if (U > 0) wait(&bar.o_done[st], (pv_n - 1) & 1);
             fence_after();
 
             // where the rows go: the output, or this CTA's part of the item
