@@ -18,14 +18,19 @@
 // two row tiles in a CTA (QT = 2, chunks) each stream has its rows and both
 // use every K/V tile; with one row tile (QT = 1) the streams take the K/V tiles
 // in turn, each with its own m, sum and O, and are joined at the end.  Heads of 256
-// leave TMEM for one O only: one stream over two S buffers.
+// leave TMEM for one O only: one stream over two S buffers.  Each stream has two
+// warpgroups, one for each half of a tile's columns: a softmax thread holds half a row's
+// scores, and the pair agrees on the maximum through shared memory.
 //
 // Work.  An item is (lane, key/value head, row tiles); its units are the K/V
 // tiles in reach.  All units of the step, in item order, are cut into equal runs,
 // one per CTA of a grid of one CTA per SM, from the lengths in device memory:
 // ragged batches balance by themselves and a single long lane is split over
 // the whole GPU.  A CTA whose run starts or ends inside an item leaves its part
-// (m, sum, O) in the workspace, and the last part's CTA joins them in order.
+// (m, sum, O) in the workspace, and a second kernel joins the parts in order, spread
+// over the whole GPU (joined by the last part's CTA, an item in 152 parts of 128
+// rows took 250 us longer).  The loader warp works the items out and hands
+// them to the others through a ring in shared memory.
 #pragma once
 
 #include <cuda.h>
@@ -37,7 +42,7 @@ namespace attn {
 constexpr float kLag = 8.f;      // log2 units the running maximum may lag
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMaxSms = 512;     // tickets at the start of the workspace
+constexpr int kMaxSms = 512;     // entries of the join table at the start of the workspace
 
 template <int D_, int QT_>
 struct Shape {
@@ -47,10 +52,13 @@ struct Shape {
     static constexpr int NB = D / 64;                          // 128-byte-wide blocks of an operand
     static constexpr int kQBytes = 128 * D * 2;                // one row tile
     static constexpr int kStageBytes = BK * D * 2;             // a K or a V tile
-    static constexpr int kStages = (224 * 1024 - QT * kQBytes) / kStageBytes < 12
-                                       ? (224 * 1024 - QT * kQBytes) / kStageBytes : 12;
-    static constexpr int kThreads = NS * 128 + 64;             // softmax warpgroups, loader, MMA
-    static constexpr int kPayload = QT * kQBytes + kStages * kStageBytes + 2048;   // operands, then the streams' swap area
+    static constexpr int QB = QT == 1 && D <= 128 ? 2 : 1;     // Q buffers
+    static constexpr int kStages = (224 * 1024 - QB * QT * kQBytes) / kStageBytes < 12
+                                       ? (224 * 1024 - QB * QT * kQBytes) / kStageBytes : 12;
+    static constexpr int kSoftmaxWarps = NS * 8;
+    static constexpr int kThreads = kSoftmaxWarps * 32 + 128;  // softmax; K/V loader, MMA, two Q loaders
+    static constexpr int kSwap = 512;                          // floats that softmax warps exchange through
+    static constexpr int kPayload = QB * QT * kQBytes + kStages * kStageBytes + kSwap * 4;
     static constexpr int kRows = QT * 128;
     // TMEM columns: S buffers, then O
     static constexpr int kO = 2 * BK;
@@ -71,8 +79,16 @@ struct Args {
     int64_t window;
     uint16_t *out;
     float *lse;
-    unsigned int *tickets;
+    struct Join *joins;    // [grid]
     float *parts;          // [grid][2][kPartFloats]
+};
+
+// An item in parts: those of CTA `cta` (its second slot) and of the CTAs after it
+// (their first slots).  Entry `cta` of a table with one entry a CTA.
+struct Join {
+    int32_t parts;         // 0: the CTA begins no item that others finish
+    int32_t rows;          // of the item's row tiles, in use
+    int32_t first, head, rt, pad[3];
 };
 
 // mbar_wait without the long suspension hint: the waits of this kernel's pipeline
@@ -178,26 +194,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t a)
                  : "r"(a)
                  : "memory");
 }
-// The load alone, and the wait for it: the values pass through the wait, so that
-// no use of them can move before it.
-__device__ __forceinline__ void tmem_issue32(uint32_t (&r)[32], uint32_t a)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-                 : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24)
-                 : "r"(a)
-                 : "memory");
-}
-#define M8(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7])
-__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : M8(r, 0), M8(r, 8), M8(r, 16), M8(r, 24)::"memory");
-}
 __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
                  "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::I8(r, 0), I8(r, 8), I8(r, 16),
                  I8(r, 24), "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t a)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : R8(r, 0), R8(r, 8)
+                 : "r"(a)
                  : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16])
@@ -396,11 +405,38 @@ __device__ __forceinline__ int64_t run_owner(int64_t u, int64_t total, int64_t g
 
 // ---- the kernel ---------------------------------------------------------------
 
+// What the other warps need of a segment.
+struct Item {
+    int32_t first, n, seq, head, rt;
+    int32_t lo, hi, tile, tiles;   // tiles == 0: no more items
+    int32_t slot;                  // -1: a whole item; else where its part goes
+    int32_t pad[2];
+};
+constexpr int kItems = 4;
+
 template <typename S>
 struct Bars {
     uint64_t full[S::kStages], empty[S::kStages];
-    uint64_t s_full[2], p_full[2], o_done[2], q_full, drain;
+    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t q_full[2], q_empty[2], item_full[kItems], item_empty[kItems], drain;
 };
+
+__device__ __forceinline__ void named_barrier(int id, int threads)
+{
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// a barrier that tells every thread whether any of them says so
+__device__ __forceinline__ bool named_barrier_any(int id, int threads, bool mine)
+{
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any)
+                 : "r"(id), "r"(threads), "r"((uint32_t)mine)
+                 : "memory");
+    return any != 0;
+}
+constexpr int kAllSoftmax = 9;   // barrier ids: 1 .. 8 a pair of warps with the same rows, 9 all softmax warps
 
 template <int D, int QT, bool F16>
 __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(const __grid_constant__ Args a)
@@ -408,12 +444,12 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
     using S = Shape<D, QT>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars<S> bar;
+    __shared__ Item items[kItems];
     __shared__ uint32_t tmem_slot;
     __shared__ Plan plan;
     __shared__ int64_t warp_units[S::kThreads / 32];
-    __shared__ unsigned int last_part;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kLoader = S::NS * 4, kMma = kLoader + 1;
+    constexpr int kLoader = S::kSoftmaxWarps, kMma = kLoader + 1, kQLoader = kLoader + 2;
 
     pdl_launch_dependents();
     if (tid == 0) {
@@ -424,10 +460,15 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 4);
+            mbar_init(&bar.p_full[i], 8);
             mbar_init(&bar.o_done[i], 1);
+            mbar_init(&bar.q_full[i], 2);
+            mbar_init(&bar.q_empty[i], 1);
         }
-        mbar_init(&bar.q_full, S::NS * 4);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&bar.item_full[i], 1);
+            mbar_init(&bar.item_empty[i], S::kSoftmaxWarps + 3);
+        }
         mbar_init(&bar.drain, 1);
         fence_mbar_init();
     }
@@ -435,6 +476,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         asm volatile("prefetch.tensormap [%0];" ::"l"(&a.kmap) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&a.vmap) : "memory");
     }
+    if (warp == kMma) tmem_alloc(&tmem_slot);
     pdl_wait();
 
     // Units of the step and the lane where this CTA's run starts: each thread
@@ -451,7 +493,9 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             if (lane >= d) incl += y;
         }
         if (lane == 31) warp_units[warp] = incl;
+        fence_before();
         __syncthreads();
+        fence_after();
         int64_t before = incl - mine, total = 0;
         for (int w = 0; w < S::kThreads / 32; ++w) {
             if (w < warp) before += warp_units[w];
@@ -478,48 +522,67 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         }
         __syncthreads();
     }
-    if ((int64_t)blockIdx.x >= plan.grid) return;
-
-    if (warp == kMma) tmem_alloc(&tmem_slot);
-    fence_before();
-    __syncthreads();
-    fence_after();
     const uint32_t tmem = tmem_slot;
 
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *q_smem = smem, *kv_smem = smem + QT * S::kQBytes;
-    float2 *ml_swap = reinterpret_cast<float2 *>(kv_smem + S::kStages * S::kStageBytes);   // [2][128]
-
-    Run run;
-    {
-        const int64_t total = plan.total;
-        run.u = run_start(blockIdx.x, total, plan.grid);
-        run.end = run_start(blockIdx.x + 1, total, plan.grid);
-        run.lane = plan.lane;
-        run.ln = lane_of(a, run.lane);
-        run.rts = row_tiles<S>(a, run.ln.n);
-        const int64_t per_head = head_units<S>(a, run.ln), off = run.u - plan.lane_u;
-        run.head = (int)(off / per_head);
-        run.item0 = plan.lane_u + run.head * per_head;
-        run.rt = 0;
-        for (;;) {
-            const int t = reach_of<S>(a, run.ln.n, run.ln.seq, run.rt).tiles;
-            if (run.u < run.item0 + t) break;
-            run.item0 += t;
-            ++run.rt;
-        }
-    }
+    uint8_t *q_smem = smem, *kv_smem = smem + S::QB * QT * S::kQBytes;
+    float *swap = reinterpret_cast<float *>(kv_smem + S::kStages * S::kStageBytes);
 
     if (warp == kLoader) {
-        // ---- K and V tiles: a lane of the warp per page, in the order K0 V0 K1 V1 ...
+        // ---- the items of this CTA's run, and their K and V tiles: a lane of
+        // the warp per page, in the order K0 V0 K1 V1 ...
+        Run run;
+        run.u = run.end = 0;
+        if ((int64_t)blockIdx.x < plan.grid) {
+            const int64_t total = plan.total;
+            run.u = run_start(blockIdx.x, total, plan.grid);
+            run.end = run_start(blockIdx.x + 1, total, plan.grid);
+            run.lane = plan.lane;
+            run.ln = lane_of(a, run.lane);
+            run.rts = row_tiles<S>(a, run.ln.n);
+            const int64_t per_head = head_units<S>(a, run.ln), off = run.u - plan.lane_u;
+            run.head = (int)udiv(off, per_head);
+            run.item0 = plan.lane_u + run.head * per_head;
+            run.rt = 0;
+            for (;;) {
+                const int t = reach_of<S>(a, run.ln.n, run.ln.seq, run.rt).tiles;
+                if (run.u < run.item0 + t) break;
+                run.item0 += t;
+                ++run.rt;
+            }
+        }
         const int rows = min(1 << a.log_page, S::BK);            // rows of a box
         const int boxes = S::BK / rows;
         const bool whole = rows == S::BK;                        // one box brings all blocks
         const uint32_t box_bytes = (uint32_t)rows * D * 2;
         uint32_t idx = 0;                                        // stage uses so far
         bool ok = true;
-        Segment s;
-        while (ok && next_segment<S>(a, run, s)) {
+        Join join;
+        join.parts = 0;
+        for (uint32_t n = 0; ok; ++n) {
+            Segment s;
+            const bool more = next_segment<S>(a, run, s);
+            ok = __all_sync(kFull, wait(&bar.item_empty[n % kItems], ((n / kItems) & 1) ^ 1));
+            if (!ok) break;
+            if (lane == 0) {
+                Item &it = items[n % kItems];
+                it.tiles = 0;
+                if (more) {
+                    const bool split = s.tiles < s.item_tiles, begins = s.tile == s.r.tile0;
+                    it.first = s.ln.first; it.n = s.ln.n; it.seq = s.ln.seq; it.head = s.head; it.rt = s.rt;
+                    it.lo = s.r.lo; it.hi = s.r.hi; it.tile = s.tile; it.tiles = s.tiles;
+                    it.slot = !split ? -1 : begins ? 1 : 0;
+                    if (split && begins) {
+                        const int64_t left = (int64_t)s.ln.n * a.group - (int64_t)s.rt * S::kRows;
+                        join.parts = (int32_t)(run_owner(s.item0 + s.item_tiles - 1, plan.total, plan.grid) - blockIdx.x) + 1;
+                        join.rows = (int32_t)(left < S::kRows ? left : S::kRows);
+                        join.first = s.ln.first; join.head = s.head; join.rt = s.rt;
+                    }
+                }
+                mbar_arrive(&bar.item_full[n % kItems]);
+            }
+            __syncwarp();
+            if (!more) break;
             for (int t = 0; t < s.tiles && ok; ++t) {
                 const int key0 = (s.tile + t) * S::BK, k0 = key0 + lane * rows;
                 const bool mine = lane < boxes && k0 < s.r.hi && k0 + rows > s.r.lo;
@@ -551,6 +614,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 }
             }
         }
+        if (lane == 0) a.joins[blockIdx.x] = join;
         if (!ok) {
             // given up: the copies in flight still have to land (each stage's
             // last use; bounded, whatever the other waits did)
@@ -563,7 +627,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         // ---- the products, issued by one thread (the warp walks along with it)
         constexpr uint32_t kQk = instr(F16, S::BK, false), kPv = instr(F16, D, true);
         const bool leader = elect_one();
-        uint32_t items = 0, units[2] = {0, 0};               // items so far; units per S buffer
+        uint32_t units[2] = {0, 0};                          // units per S buffer
         uint32_t k_stage = 0, k_phase = 0, v_stage = 1, v_phase = 0;   // of the next K and V tile (every second stage use)
         static_assert(S::kStages >= 3, "");
         auto advance = [](uint32_t &st, uint32_t &ph) {
@@ -574,17 +638,22 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             }
         };
         bool ok = true;
-        Segment s;
         const uint32_t q_desc = operand(smem_u32(q_smem), 16), k_desc = operand(smem_u32(kv_smem), 16),
                        v_desc = operand(smem_u32(kv_smem), S::BK * 128);
-        while (ok && next_segment<S>(a, run, s)) {
-            const int U = QT == 2 ? 2 * s.tiles : s.tiles;
+        for (uint32_t n = 0; ok; ++n) {
+            if (!__all_sync(kFull, wait(&bar.item_full[n % kItems], (n / kItems) & 1))) break;
+            const int tiles = items[n % kItems].tiles;
+            __syncwarp();
+            if (tiles == 0) break;
+            if (lane == 0) mbar_arrive(&bar.item_empty[n % kItems]);
+            const int U = QT == 2 ? 2 * tiles : tiles;
+            const uint32_t qb = n % S::QB;
             auto qk = [&](int i) -> bool {
                 const int b = i & 1;
-                if (!wait(&bar.full[k_stage], k_phase)) return false;
+                if ((QT == 1 || b == 0) && !wait(&bar.full[k_stage], k_phase)) return false;
                 fence_after();
                 if (leader) {
-                    const uint32_t qa = q_desc + (QT == 2 ? b * (S::kQBytes >> 4) : 0), ka = k_desc + k_stage * (S::kStageBytes >> 4);
+                    const uint32_t qa = q_desc + (qb * QT + (QT == 2 ? b : 0)) * (S::kQBytes >> 4), ka = k_desc + k_stage * (S::kStageBytes >> 4);
                     const uint32_t d = tmem + b * S::BK;
                     mma_ss<false>(d, qa, ka, kQk);
 #pragma unroll
@@ -592,18 +661,19 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                         mma_ss<true>(d, qa + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, ka + (k >> 2) * (S::BK * 128 >> 4) + (k & 3) * 2, kQk);
                     commit(&bar.s_full[b]);
                     if (QT == 1 || b == 1) commit(&bar.empty[k_stage]);
+                    if (i == U - 1) commit(&bar.q_empty[qb]);
                 }
                 __syncwarp();
                 if (QT == 1 || b == 1) advance(k_stage, k_phase);
                 return true;
             };
-            ok = wait(&bar.q_full, items & 1);
+            ok = wait(&bar.q_full[qb], (n / S::QB) & 1);
             fence_after();
             ok = ok && qk(0);
             for (int i = 0; i < U && ok; ++i) {
                 if (i + 1 < U) ok = qk(i + 1);
                 const int b = i & 1, ob = S::NS == 2 ? b : 0;
-                ok = ok && wait(&bar.full[v_stage], v_phase);
+                if (QT == 1 || b == 0) ok = ok && wait(&bar.full[v_stage], v_phase);
                 ok = ok && wait(&bar.p_full[b], units[b] & 1);
                 if (!ok) break;
                 ++units[b];
@@ -612,14 +682,15 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     const uint32_t va = v_desc + v_stage * (S::kStageBytes >> 4), d = tmem + S::kO + ob * D, pa = tmem + b * S::BK;
                     mma_ts(d, pa, va, kPv, S::NS == 2 ? i >= 2 : i >= 1);
 #pragma unroll
-                    for (int k = 1; k < S::BK / 16; ++k) mma_ts_acc(d, pa + k * 8, va + k * (2048 >> 4), kPv);
+                    for (int k = 1; k < S::BK / 16; ++k)   // the halves' weights lie half a tile apart
+                        mma_ts_acc(d, pa + k / (S::BK / 32) * (S::BK / 2) + k % (S::BK / 32) * 8, va + k * (2048 >> 4), kPv);
                     commit(&bar.o_done[ob]);
                     if (QT == 1 || b == 1) commit(&bar.empty[v_stage]);
                 }
                 __syncwarp();
                 if (QT == 1 || b == 1) advance(v_stage, v_phase);
             }
-            ++items;
+            ok = __all_sync(kFull, ok);
         }
         // everything issued is complete before TMEM is freed
         if (leader) {
@@ -628,109 +699,123 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             while (!mbar_try_wait(&bar.drain, 0) && global_ns() - t0 < kWaitLimitNs) {}
         }
         __syncwarp();
-    } else {
-        // ---- softmax, correction and epilogue: warpgroup `st` is stream st
-        const int st = warp >> 2, row = tid & 127;                // row of the tile
-        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const int wg_rows = QT == 2 ? 128 : 128 * S::NS;          // threads that load one Q tile together
-        uint32_t tile_n = 0, s_n[2] = {0, 0}, pv_n = 0;           // tiles so far, units per S buffer, PVs of this stream
-        Segment s;
-        while (next_segment<S>(a, run, s)) {
-            const int64_t rows_all = (int64_t)s.ln.n * a.group;
-            const int64_t tile_row0 = (int64_t)s.rt * S::kRows + (QT == 2 ? st * 128 : 0);
-            // Q: 16-byte pieces, consecutive threads on consecutive pieces of a row
-            {
-                constexpr int kPieces = D / 8;
-                uint8_t *dst = q_smem + (QT == 2 ? st * S::kQBytes : 0);
-                const int t0 = QT == 2 ? row : tid;
-                const int64_t have = rows_all - tile_row0;
-                const int valid = have < 0 ? 0 : have < 128 ? (int)have : 128;
-                for (int i = t0; i < valid * kPieces; i += wg_rows) {
-                    const int r = i / kPieces, p = i % kPieces;
-                    const int64_t gr = tile_row0 + r, tok = gr / a.group;
-                    const int h = s.head * a.group + (int)(gr - tok * a.group);
-                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(a.q + (s.ln.first + tok) * a.qs_t + h * a.qs_h) + p);
-                    *reinterpret_cast<uint4 *>(dst + (p >> 3) * (128 * 128) + r * 128 + (((p & 7) ^ (r & 7)) << 4)) = x;
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.q_full);
+    } else if (warp >= kQLoader) {
+        // ---- Q: 16-byte pieces of the item's rows, consecutive lanes on
+        // consecutive pieces; rows past the item's keep what is there
+        const int t0 = tid - kQLoader * 32;
+        constexpr int kPieces = D / 8;
+        for (uint32_t n = 0;; ++n) {
+            if (!__all_sync(kFull, wait(&bar.item_full[n % kItems], (n / kItems) & 1))) break;
+            const Item it = items[n % kItems];
+            __syncwarp();
+            if (it.tiles == 0) break;
+            if (lane == 0) mbar_arrive(&bar.item_empty[n % kItems]);
+            const uint32_t qb = n % S::QB;
+            if (!__all_sync(kFull, wait(&bar.q_empty[qb], ((n / S::QB) & 1) ^ 1))) break;
+            const int64_t row0 = (int64_t)it.rt * S::kRows, have = (int64_t)it.n * a.group - row0;
+            const int valid = have < S::kRows ? (int)have : S::kRows;
+            uint8_t *dst = q_smem + qb * QT * S::kQBytes;
+#pragma unroll 8
+            for (int i = t0; i < valid * kPieces; i += 64) {
+                const int r = i / kPieces, p = i % kPieces;
+                const uint32_t gr = (uint32_t)row0 + r, tok = gr / (uint32_t)a.group;   // rows fit 31 bits (checked)
+                const int h = it.head * a.group + (int)(gr - tok * a.group);
+                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)(it.first + (int)tok) * a.qs_t + h * a.qs_h) + p);
+                *reinterpret_cast<uint4 *>(dst + (r >> 7) * S::kQBytes + (p >> 3) * (128 * 128) + (r & 127) * 128 +
+                                           (((p & 7) ^ (r & 7)) << 4)) = x;
             }
-            const int64_t gr = tile_row0 + row;
-            const bool valid = gr < rows_all;
-            const int64_t tok = valid ? gr / a.group : 0;
-            const int h = s.head * a.group + (int)(valid ? gr - tok * a.group : 0);
-            const int pos = s.ln.seq - s.ln.n + (int)tok;
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.q_full[qb]);
+        }
+    } else {
+        // ---- softmax, correction and epilogue: stream `st`, columns [half * kW, half * kW + kW) of its tiles
+        constexpr int kW = S::BK / 2;
+        const int st = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;   // row of the tile
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        const int pair = 1 + st * 4 + quad;                       // barrier of the two warps with these rows
+        uint32_t tile_n = 0, s_n[2] = {0, 0}, pv_n = 0;           // tiles so far, units per S buffer, PVs of this stream
+        for (uint32_t n = 0;; ++n) {
+            const bool ok = wait(&bar.item_full[n % kItems], (n / kItems) & 1);
+            // all softmax warps go on or none does: the barriers below count on it
+            if (named_barrier_any(kAllSoftmax, S::kSoftmaxWarps * 32, !ok)) break;
+            const Item &it = items[n % kItems];
+            const int tiles = it.tiles;
+            if (tiles == 0) break;
+            const int lo = it.lo, hi = it.hi, tile0 = it.tile;
+            const int64_t gr = (int64_t)it.rt * S::kRows + (QT == 2 ? st * 128 : 0) + row;
+            const bool valid = gr < (int64_t)it.n * a.group;
+            const int tok = valid ? (int)((uint32_t)gr / (uint32_t)a.group) : 0;
+            const int pos = it.seq - it.n + tok;
             const int64_t klo64 = a.window > 0 ? (int64_t)pos - a.window + 1 : 0;
             const int klo = klo64 > 0 ? (int)klo64 : 0, khi = valid ? pos + 1 : klo;   // keys of this row
             const bool live = __any_sync(kFull, khi > klo);
 
-            float m = -INFINITY, l = 0.f;
-            int done = 0;                                          // units of this stream so far
-            const int U = QT == 2 || S::NS == 1 ? s.tiles : (s.tiles - st + 1) >> 1;
-            for (int i = 0; i < U; ++i, ++done) {
+            float m = -INFINITY, l = 0.f;                          // l: of this half's columns
+            const int U = QT == 2 || S::NS == 1 ? tiles : (tiles - st + 1) >> 1;
+            for (int i = 0; i < U; ++i) {
                 const int t = QT == 2 || S::NS == 1 ? i : 2 * i + st;
                 const int b = S::NS == 2 ? st : i & 1;
-                const int key0 = (s.tile + t) * S::BK;
-                wait(&bar.s_full[b], s_n[b] & 1);
-                ++s_n[b];
+                const int key0 = (tile0 + t) * S::BK;
+                if (S::NS == 2 || b == 0) wait(&bar.s_full[b], s_n[0]++ & 1);
+                else wait(&bar.s_full[1], s_n[1]++ & 1);
                 fence_after();
                 if (live) {
-                    const uint32_t sa = tmem + lane_base + b * S::BK;
-                    // columns of this row in the tile; what a row past the item's holds is nobody's
-                    const int from = valid ? klo - key0 : 0, to = valid ? khi - key0 : S::BK;
-                    const bool edge = __any_sync(kFull, from > 0 || to < S::BK);
-                    // Two passes over S in TMEM, 32 columns at a time with the next 32
-                    // on their way (a row's whole tile in registers would spill).
-                    uint32_t xa[32], xb[32];
+                    const uint32_t sa = tmem + lane_base + b * S::BK + half * kW;
+                    // columns of this row in the half tile; what a row past the item's holds is nobody's
+                    const int from = valid ? klo - key0 - half * kW : 0, to = valid ? khi - key0 - half * kW : kW;
+                    const bool edge = __any_sync(kFull, from > 0 || to < kW);
+                    // two passes over S in TMEM (other warps hide the loads; the
+                    // half row in registers would not fit)
                     float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    auto top_of = [&](uint32_t (&x)[32], int c) {
+#pragma unroll
+                    for (int c = 0; c < kW; c += 32) {
+                        uint32_t x[32];
+                        tmem_ld32(x, sa + c);
                         if (edge) mask_scores(x, from - c, to - c);
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 top4[k] = max3(top4[k], __uint_as_float(x[e + k]), __uint_as_float(x[e + 4 + k]));
-                    };
-                    tmem_issue32(xa, sa);
-#pragma unroll
-                    for (int c = 0; c < S::BK; c += 64) {
-                        tmem_wait32(xa);
-                        tmem_issue32(xb, sa + c + 32);
-                        top_of(xa, c);
-                        tmem_wait32(xb);
-                        tmem_issue32(xa, c + 64 < S::BK ? sa + c + 64 : sa);   // at the end: the second pass's first
-                        top_of(xb, c + 32);
                     }
-                    float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-                    top *= a.c;
+                    float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * a.c;
+                    // the other half's maximum; a row's two threads decide alike.  (One
+                    // stream: a slot per S buffer, since S of the next unit may be there
+                    // before the other half has read this one's.)
+                    float *mx = swap + (S::NS == 2 ? st : b) * 256 + row;
+                    mx[half * 128] = top;
+                    named_barrier(pair, 64);
+                    top = fmaxf(top, mx[(half ^ 1) * 128]);
                     // a new reference only past the lag (or for a row's first key)
                     const bool move = valid && (top > m + kLag || (m == -INFINITY && top > -INFINITY));
                     if (__any_sync(kFull, move)) {
                         const float f = move ? exp2_fast(m - top) : 1.f;
                         if (move) m = top;
                         l *= f;
-                        if (done > 0) {
+                        if (i > 0) {
                             wait(&bar.o_done[st], (pv_n - 1) & 1);
                             fence_after();
-                            const uint32_t oa = tmem + lane_base + S::kO + st * D;
+                            const uint32_t oa = tmem + lane_base + S::kO + st * D + half * (D / 2);
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
+                            for (int c = 0; c < D / 2; c += 32) {
                                 uint32_t o[32];
-                                tmem_ld32(o, oa + c * 32);
+                                tmem_ld32(o, oa + c);
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st32(oa + c * 32, o);
+                                tmem_st32(oa + c, o);
                             }
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m;
                     const uint64_t cc = two(a.c, a.c), mm = two(-ref, -ref);
                     uint64_t sum[2] = {0ull, 0ull};
-                    // P of columns c .. c+31 covers columns c/2 .. c/2+15 of S, read before
-                    auto weights = [&](uint32_t (&x)[32], int c) {
+#pragma unroll
+                    for (int c = 0; c < kW; c += 32) {
+                        // P of columns c .. c+31 covers columns c/2 .. c/2+15 of this half's S, read before
+                        uint32_t x[32], pk[16];
+                        tmem_ld32(x, sa + c);
                         if (edge) mask_scores(x, from - c, to - c);
-                        uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float p0, p1;
@@ -741,15 +826,6 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                             pk[e] = pack2<F16>(p0, p1);
                         }
                         tmem_st16(sa + c / 2, pk);
-                    };
-#pragma unroll
-                    for (int c = 0; c < S::BK; c += 64) {
-                        tmem_wait32(xa);
-                        tmem_issue32(xb, sa + c + 32);
-                        weights(xa, c);
-                        tmem_wait32(xb);
-                        if (c + 64 < S::BK) tmem_issue32(xa, sa + c + 64);
-                        weights(xb, c + 32);
                     }
                     float s0, s1;
                     halves(add2(sum[0], sum[1]), s0, s1);
@@ -757,13 +833,13 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 }
                 // V rows that no row of the item may see hold anything, NaN
                 // included: 0 * NaN must not reach O
-                if (key0 < s.r.lo || key0 + S::BK > s.r.hi) {
+                if (key0 < lo || key0 + S::BK > hi) {
                     const uint32_t idx = 2 * (tile_n + t) + 1, vs = idx % S::kStages;
                     wait(&bar.full[vs], (idx / S::kStages) & 1);
                     uint8_t *v = kv_smem + vs * S::kStageBytes;
-                    constexpr int kPer = 128 / S::BK;               // threads of a key row
-                    const int kr = row / kPer, part = row % kPer;
-                    if (key0 + kr < s.r.lo || key0 + kr >= s.r.hi) {
+                    constexpr int kPer = 256 / S::BK;               // threads of a key row
+                    const int kr = (half * 128 + row) / kPer, part = row % kPer;
+                    if (key0 + kr < lo || key0 + kr >= hi) {
 #pragma unroll
                         for (int blk = 0; blk < S::NB; ++blk)
 #pragma unroll
@@ -776,50 +852,62 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 // product before it, and a barrier's parity tells only its last two phases
                 // apart, so that every phase is waited for.  (With two streams, S of a
                 // stream's unit comes after its last product.)
-                if (S::NS == 1 && done > 0) wait(&bar.o_done[st], (pv_n - 1) & 1);
+                if (S::NS == 1 && i > 0) wait(&bar.o_done[st], (pv_n - 1) & 1);
                 wait_st();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[b]);
                 ++pv_n;
             }
-            tile_n += s.tiles;
+            tile_n += tiles;
             if (U > 0) wait(&bar.o_done[st], (pv_n - 1) & 1);
             fence_after();
 
-            // where the rows go: the output, or this CTA's part of the item
-            const bool split = s.tiles < s.item_tiles;
-            const int slot = s.tile == s.r.tile0 ? 1 : 0;          // an item begun here, or one begun before
-            float *part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * S::kPartFloats + (QT == 2 ? st * 128 * (D + 2) : 0);
-            float f0 = 1.f, f1 = 0.f;                              // weights of the two streams' O
-            int c0 = 0, c1 = D;                                    // columns this thread writes
-            if (QT == 1 && S::NS == 2) {
-                // join the streams: the same row of the other warpgroup; each takes half the columns
-                ml_swap[st * 128 + row] = make_float2(m, l);
+            // the row's sum over the halves (and the streams), and the columns this thread writes
+            float f0 = 1.f, f1 = 0.f;                              // weights of the streams' O
+            int c0 = half * (D / 2);
+            constexpr bool kStreams = QT == 1 && S::NS == 2;
+            constexpr int kCols = kStreams ? D / 4 : D / 2;
+            if (kStreams) {
+                swap[st * 256 + half * 128 + row] = l;
                 fence_before();
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                named_barrier(kAllSoftmax, S::kSoftmaxWarps * 32);
                 fence_after();
-                const float2 e0 = ml_swap[row], e1 = ml_swap[128 + row];
-                m = fmaxf(e0.x, e1.x);
-                f0 = e0.x == -INFINITY ? 0.f : exp2_fast(e0.x - m);
-                f1 = e1.x == -INFINITY ? 0.f : exp2_fast(e1.x - m);
-                l = e0.y * f0 + e1.y * f1;
-                c0 = st * (D / 2);
-                c1 = c0 + D / 2;
+                const float l0 = swap[row] + swap[128 + row], l1 = swap[256 + row] + swap[384 + row];
+                named_barrier(kAllSoftmax, S::kSoftmaxWarps * 32);
+                if (half == 0) swap[st * 128 + row] = m;
+                named_barrier(kAllSoftmax, S::kSoftmaxWarps * 32);
+                const float m0 = swap[row], m1 = swap[128 + row];
+                m = fmaxf(m0, m1);
+                f0 = m0 == -INFINITY ? 0.f : exp2_fast(m0 - m);
+                f1 = m1 == -INFINITY ? 0.f : exp2_fast(m1 - m);
+                l = l0 * f0 + l1 * f1;
+                c0 = (st * 2 + half) * kCols;
+            } else if (live) {
+                float *mx = swap + st * 256 + row;
+                mx[half * 128] = l;
+                named_barrier(pair, 64);
+                l += mx[(half ^ 1) * 128];
             }
+
+            // where the rows go: the output, or this CTA's part of the item
+            const int slot = it.slot;
+            const bool split = slot >= 0;
+            float *part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * S::kPartFloats + (QT == 2 ? st * 128 * (D + 2) : 0);
             const float inv = split ? 1.f : l > 0.f ? 1.f / l : 0.f;
-            const int64_t out_row = ((int64_t)s.ln.first + tok) * a.heads_q + h;
+            const int h = it.head * a.group + (int)(valid ? gr - (int64_t)tok * a.group : 0);
+            const int64_t out_row = ((int64_t)it.first + tok) * a.heads_q + h;
             if (live) {
                 const uint32_t oa = tmem + lane_base + S::kO + (QT == 2 ? st * D : 0);
 #pragma unroll 1
-                for (int c = c0; c < c1; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(o, oa + c);
-                    if (QT == 1 && S::NS == 2 && s.tiles > 1) {
-                        uint32_t o1[32];
-                        tmem_ld32(o1, oa + D + c);
+                for (int c = c0; c < c0 + kCols; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(o, oa + c);
+                    if (kStreams && tiles > 1) {
+                        uint32_t o1[16];
+                        tmem_ld16(o1, oa + D + c);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
+                        for (int e = 0; e < 16; ++e) {
                             const float v0 = f0 > 0.f ? __uint_as_float(o[e]) * f0 : 0.f;
                             const float v1 = f1 > 0.f ? __uint_as_float(o1[e]) * f1 : 0.f;
                             o[e] = __float_as_uint(v0 + v1);
@@ -827,19 +915,19 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     }
                     if (l <= 0.f) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                        for (int e = 0; e < 16; ++e) o[e] = 0u;
                     }
                     if (!valid) continue;
                     if (split) {
                         float4 *dst = reinterpret_cast<float4 *>(part) + (c / 4) * 128 + row;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
+                        for (int e = 0; e < 4; ++e)
                             dst[e * 128] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
                                                        __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
                     } else {
                         uint4 *dst = reinterpret_cast<uint4 *>(a.out + out_row * D + c);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
+                        for (int e = 0; e < 2; ++e) {
                             uint32_t w[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
@@ -849,7 +937,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     }
                 }
             } else if (valid && !split) {                          // a warp of rows without keys
-                for (int c = c0; c < c1; c += 8) *reinterpret_cast<uint4 *>(a.out + out_row * D + c) = make_uint4(0, 0, 0, 0);
+                for (int c = c0; c < c0 + kCols; c += 8) *reinterpret_cast<uint4 *>(a.out + out_row * D + c) = make_uint4(0, 0, 0, 0);
             }
             if (valid && c0 == 0) {
                 if (split) {
@@ -861,69 +949,129 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 }
             }
             fence_before();
-
-            if (split) {
-                // publish, and the last part's CTA joins all parts in order
-                constexpr int kT = S::NS * 128;
-                const int64_t first_cta = run_owner(s.item0, plan.total, plan.grid);
-                const int n_parts = (int)(run_owner(s.item0 + s.item_tiles - 1, plan.total, plan.grid) - first_cta) + 1;
-                __threadfence();
-                asm volatile("bar.sync 2, %0;" ::"n"(kT) : "memory");
-                if (tid == 0) {
-                    last_part = atom_add_acq_rel(a.tickets + first_cta, 1u) == (unsigned)n_parts - 1 ? 1u : 0u;
-                    if (last_part) a.tickets[first_cta] = 0u;
-                }
-                asm volatile("bar.sync 2, %0;" ::"n"(kT) : "memory");
-                if (last_part) {
-                    __threadfence();
-                    for (int qt = 0; qt < QT; ++qt) {
-                        const int64_t r0 = (int64_t)s.rt * S::kRows + qt * 128;
-                        const int64_t have = rows_all - r0;
-                        const int nr = have < 0 ? 0 : have < 128 ? (int)have : 128;
-                        for (int i = tid; i < nr * (D / 8); i += kT) {
-                            const int r = i % nr, c = i / nr * 8;
-                            auto part_of = [&](int p) -> const float * {
-                                return a.parts + ((first_cta + p) * 2 + (p == 0 ? 1 : 0)) * S::kPartFloats + qt * 128 * (D + 2);
-                            };
-                            float M = -INFINITY;
-#pragma unroll 4
-                            for (int p = 0; p < n_parts; ++p) M = fmaxf(M, __ldcg(part_of(p) + 128 * D + r));
-                            float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-                            for (int p = 0; p < n_parts; ++p) {
-                                const float *pp = part_of(p);
-                                const float mp = __ldcg(pp + 128 * D + r), lp = __ldcg(pp + 128 * D + 128 + r);
-                                if (mp == -INFINITY) continue;
-                                const float f = exp2_fast(mp - M);
-                                const float4 x = __ldcg(reinterpret_cast<const float4 *>(pp) + (c / 4) * 128 + r);
-                                const float4 y = __ldcg(reinterpret_cast<const float4 *>(pp) + (c / 4 + 1) * 128 + r);
-                                L = fmaf(lp, f, L);
-                                o[0] = fmaf(x.x, f, o[0]); o[1] = fmaf(x.y, f, o[1]);
-                                o[2] = fmaf(x.z, f, o[2]); o[3] = fmaf(x.w, f, o[3]);
-                                o[4] = fmaf(y.x, f, o[4]); o[5] = fmaf(y.y, f, o[5]);
-                                o[6] = fmaf(y.z, f, o[6]); o[7] = fmaf(y.w, f, o[7]);
-                            }
-                            const float iv = L > 0.f ? 1.f / L : 0.f;
-                            const int64_t g = r0 + r, tk = g / a.group;
-                            const int64_t orow = ((int64_t)s.ln.first + tk) * a.heads_q + s.head * a.group + (g - tk * a.group);
-                            *reinterpret_cast<uint4 *>(a.out + orow * D + c) =
-                                make_uint4(pack2<F16>(o[0] * iv, o[1] * iv), pack2<F16>(o[2] * iv, o[3] * iv),
-                                           pack2<F16>(o[4] * iv, o[5] * iv), pack2<F16>(o[6] * iv, o[7] * iv));
-                            if (c == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
-                        }
-                    }
-                }
-            }
-            if (S::NS == 2 && QT == 1) {
-                // Q and the swap area are reused by the next item
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.item_empty[n % kItems]);
+            // (O, the swap area and the pair barriers are used again only past the
+            // barrier at the next item's start)
         }
     }
     __syncthreads();
     if (warp == kMma) {
         fence_after();
         tmem_free(tmem);
+    }
+}
+
+// ---- the join -----------------------------------------------------------------
+
+constexpr int kJoinThreads = 256;
+
+// Join the parts of every split item: out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p,
+// lse = M + log2 of the sum.  A thread takes four columns of a row; of an item in many parts,
+// eight threads share them, each with its own running maximum.  The parts lie in L2; the
+// kernel is bound by their latency.
+template <int D, int QT, bool F16>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a, int ctas)
+{
+    using S = Shape<D, QT>;
+    __shared__ int32_t before[kMaxSms + 1];   // tasks before each entry
+    __shared__ int32_t warp_tasks[kJoinThreads / 32];
+    __shared__ float red[kJoinThreads][6];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kFew = 8;                   // up to so many parts a thread takes them all
+    constexpr int kEach = 4;                  // elements (four columns of a row) of a thread then
+    auto elements = [](int parts) { return parts > kFew ? kJoinThreads / 8 : kJoinThreads * kEach; };   // of a task
+    pdl_launch_dependents();
+    pdl_wait();
+    {
+        static_assert(kMaxSms == 2 * kJoinThreads, "");
+        int32_t mine[2], sum = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = 2 * tid + k;
+            mine[k] = 0;
+            if (c < ctas) {
+                const int parts = __ldcg(&a.joins[c].parts), rows = __ldcg(&a.joins[c].rows);
+                if (parts > 0) mine[k] = (rows * (D / 4) + elements(parts) - 1) / elements(parts);
+            }
+            sum += mine[k];
+        }
+        int total;
+        const int excl = warp_exclusive_sum(sum, lane, total);
+        if (lane == 0) warp_tasks[warp] = total;
+        __syncthreads();
+        int base = excl;
+        for (int w = 0; w < warp; ++w) base += warp_tasks[w];
+        before[2 * tid] = base;
+        before[2 * tid + 1] = base + mine[0];
+        if (tid == kJoinThreads - 1) before[kMaxSms] = base + sum;
+        __syncthreads();
+    }
+    for (int task = blockIdx.x; task < before[kMaxSms]; task += gridDim.x) {
+        int lo = 0, hi = kMaxSms - 1;         // the last entry with before <= task that has tasks
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (before[mid] <= task) lo = mid; else hi = mid - 1;
+        }
+        const int cta = lo;
+        const Join j = a.joins[cta];
+        const int e0 = (task - before[cta]) * elements(j.parts), all = j.rows * (D / 4);
+        auto place = [&](int p) -> const float * { return a.parts + ((int64_t)(cta + p) * 2 + (p == 0 ? 1 : 0)) * S::kPartFloats; };
+        auto finish = [&](int e, float M, float L, const float (&o)[4]) {
+            const int r = e % j.rows, c = e / j.rows * 4;
+            const uint32_t g = (uint32_t)j.rt * S::kRows + r, tok = g / (uint32_t)a.group;
+            const int64_t orow = ((int64_t)j.first + tok) * a.heads_q + (int64_t)j.head * a.group + (g - tok * a.group);
+            const float iv = L > 0.f ? 1.f / L : 0.f;
+            *reinterpret_cast<uint2 *>(a.out + orow * D + c) = make_uint2(pack2<F16>(o[0] * iv, o[1] * iv), pack2<F16>(o[2] * iv, o[3] * iv));
+            if (c == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+        };
+        // add parts p0, p0 + step, ... of element e
+        auto gather = [&](int e, int p0, int step, float &M, float &L, float (&o)[4]) {
+            const int r = e % j.rows, c4 = e / j.rows, tile = r >> 7, rr = r & 127;   // r: over the item's row tiles
+#pragma unroll 4
+            for (int p = p0; p < j.parts; p += step) {
+                const float *q = place(p) + tile * 128 * (D + 2);
+                const float mp = __ldcg(q + 128 * D + rr), lp = __ldcg(q + 128 * D + 128 + rr);
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(q) + c4 * 128 + rr);
+                if (mp == -INFINITY) continue;
+                const float Mn = fmaxf(M, mp), fo = M == -INFINITY ? 0.f : exp2_fast(M - Mn), fp = exp2_fast(mp - Mn);
+                M = Mn;
+                L = L * fo + lp * fp;
+                o[0] = o[0] * fo + x.x * fp; o[1] = o[1] * fo + x.y * fp;
+                o[2] = o[2] * fo + x.z * fp; o[3] = o[3] * fo + x.w * fp;
+            }
+        };
+        if (j.parts <= kFew) {
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int e = e0 + k * kJoinThreads + tid;
+                if (e >= all) continue;
+                float M = -INFINITY, L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+                gather(e, 0, 1, M, L, o);
+                finish(e, M, L, o);
+            }
+        } else {
+            // warp w takes parts w, w + 8, ... of the task's 32 elements; warp 0 adds the eight up in order
+            const int e = e0 + lane;
+            float M = -INFINITY, L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+            if (e < all) gather(e, warp, 8, M, L, o);
+            float *mine = red[tid];
+            mine[0] = M; mine[1] = L; mine[2] = o[0]; mine[3] = o[1]; mine[4] = o[2]; mine[5] = o[3];
+            __syncthreads();
+            if (warp == 0 && e < all) {
+                for (int w = 1; w < 8; ++w) {
+                    const float *q = red[w * 32 + lane];
+                    if (q[0] == -INFINITY) continue;
+                    const float Mn = fmaxf(M, q[0]), fo = M == -INFINITY ? 0.f : exp2_fast(M - Mn), fp = exp2_fast(q[0] - Mn);
+                    M = Mn;
+                    L = L * fo + q[1] * fp;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[k] = o[k] * fo + q[2 + k] * fp;
+                }
+                finish(e, M, L, o);
+            }
+            __syncthreads();
+        }
     }
 }
 

@@ -110,8 +110,8 @@ constexpr int64_t kMaxStride = 1ll << 39;
 
 bool bad_stride(int64_t s) { return s < 0 || s >= kMaxStride || s % 8 != 0; }
 
-template <typename K, typename A>
-spec_status launch(K kernel, dim3 grid, unsigned block, size_t smem, const A &a)
+template <typename K, typename... A>
+spec_status launch(K kernel, dim3 grid, unsigned block, size_t smem, const A &...a)
 {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
@@ -124,7 +124,7 @@ spec_status launch(K kernel, dim3 grid, unsigned block, size_t smem, const A &a)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a...);
     if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
     host::count_launch();
     return SPEC_OK;
@@ -168,10 +168,14 @@ spec_status launch_attention(const Device &d, const attn::Args &a, bool f16)
 {
     using S = attn::Shape<D, QT>;
     static_assert(S::kPartFloats <= kPartFloats, "");
-    const dim3 grid((unsigned)attention_grid(d));
+    const int ctas = attention_grid(d);
     const size_t smem = (size_t)d.attn_smem[shape_index<D, QT>()][f16];
-    return f16 ? launch(attn::attention_kernel<D, QT, true>, grid, S::kThreads, smem, a)
-               : launch(attn::attention_kernel<D, QT, false>, grid, S::kThreads, smem, a);
+    const spec_status st = f16 ? launch(attn::attention_kernel<D, QT, true>, dim3((unsigned)ctas), S::kThreads, smem, a)
+                               : launch(attn::attention_kernel<D, QT, false>, dim3((unsigned)ctas), S::kThreads, smem, a);
+    if (st != SPEC_OK) return st;
+    const dim3 join((unsigned)(4 * d.sms));
+    return f16 ? launch(attn::join_kernel<D, QT, true>, join, attn::kJoinThreads, 0, a, ctas)
+               : launch(attn::join_kernel<D, QT, false>, join, attn::kJoinThreads, 0, a, ctas);
 }
 
 // The cache as TMA sees it: [page][head][block of 64][token][64], boxes of one
@@ -273,7 +277,7 @@ int64_t spec_paged_attention_workspace(void)
     Device *d = nullptr;
     const spec_status st = device(&d);
     if (st != SPEC_OK) return st;
-    return (int64_t)attn::kMaxSms * 4 + (int64_t)attention_grid(*d) * 2 * kPartFloats * 4;
+    return (int64_t)attn::kMaxSms * sizeof(attn::Join) + (int64_t)attention_grid(*d) * 2 * kPartFloats * 4;
 }
 
 spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
@@ -328,8 +332,8 @@ spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q,
     a.lanes = (int32_t)b.lanes; a.max_pages = b.max_pages;
     a.c = scale * attn::kLog2e; a.window = window;
     a.out = static_cast<uint16_t *>(out); a.lse = lse;
-    a.tickets = static_cast<unsigned int *>(workspace);
-    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + attn::kMaxSms * 4);
+    a.joins = static_cast<attn::Join *>(workspace);
+    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + attn::kMaxSms * sizeof(attn::Join));
     const int64_t chunk = max_new > 0 ? max_new : (tokens + b.lanes - 1) / b.lanes;
     const bool two = chunk * a.group > 128;   // more rows than one tile: two tiles share every K/V tile
     const bool f16 = c.dtype == SPEC_F16;
