@@ -27,9 +27,12 @@
 // one per CTA of a grid of one CTA per SM, from the lengths in device memory:
 // ragged batches balance by themselves and a single long lane is split over
 // the whole GPU.  A CTA whose run starts or ends inside an item leaves its part
-// (m, sum, O) in the workspace, and a second kernel joins the parts in order, spread
-// over the whole GPU (joined by the last part's CTA, an item in 152 parts of 128
-// rows took 250 us longer).  The loader warp works the items out and hands
+// (m, sum, O) in the workspace; when its run is done it waits for the item's
+// other parts and joins its share of the item's elements, in the parts' order.  (The
+// launch is cooperative, so all CTAs are there; runs are equal, so the wait is
+// short, and it is bounded.  One token of one head over 19,456 keys, 152 parts: 47 us
+// with the last part's CTA joining alone -- 927 us for 128 rows of 256 --, 24 and 28 us with a
+// second kernel, which costs every call 4 us.)  The loader warp works the items out and hands
 // them to the others through a ring in shared memory.
 #pragma once
 
@@ -42,7 +45,7 @@ namespace attn {
 constexpr float kLag = 8.f;      // log2 units the running maximum may lag
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMaxSms = 512;     // entries of the join table at the start of the workspace
+constexpr int kMaxSms = 512;     // counters at the start of the workspace: [2][kMaxSms]
 
 template <int D_, int QT_>
 struct Shape {
@@ -79,16 +82,17 @@ struct Args {
     int64_t window;
     uint16_t *out;
     float *lse;
-    struct Join *joins;    // [grid]
+    unsigned int *counters;   // [2][kMaxSms], zero between calls: parts published, and joiners done, of the item begun by a CTA
     float *parts;          // [grid][2][kPartFloats]
 };
 
-// An item in parts: those of CTA `cta` (its second slot) and of the CTAs after it
-// (their first slots).  Entry `cta` of a table with one entry a CTA.
+// An item in parts that this CTA has one of: the second slot's part of CTA
+// `first_cta` (which begins the item) and the first slots' of the n - 1 CTAs after it.
 struct Join {
-    int32_t parts;         // 0: the CTA begins no item that others finish
+    int32_t n;             // 0: none
+    int32_t first_cta;
     int32_t rows;          // of the item's row tiles, in use
-    int32_t first, head, rt, pad[3];
+    int32_t first, head, rt;
 };
 
 // mbar_wait without the long suspension hint: the waits of this kernel's pipeline
@@ -436,6 +440,12 @@ __device__ __forceinline__ bool named_barrier_any(int id, int threads, bool mine
                  : "memory");
     return any != 0;
 }
+__device__ __forceinline__ uint32_t ld_acquire(const unsigned int *p)
+{
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
 constexpr int kAllSoftmax = 9;   // barrier ids: 1 .. 8 a pair of warps with the same rows, 9 all softmax warps
 
 template <int D, int QT, bool F16>
@@ -445,6 +455,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars<S> bar;
     __shared__ Item items[kItems];
+    __shared__ Join joins[2];      // of the parts in this CTA's first and second slot
     __shared__ uint32_t tmem_slot;
     __shared__ Plan plan;
     __shared__ int64_t warp_units[S::kThreads / 32];
@@ -557,8 +568,8 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         const uint32_t box_bytes = (uint32_t)rows * D * 2;
         uint32_t idx = 0;                                        // stage uses so far
         bool ok = true;
-        Join join;
-        join.parts = 0;
+        if (lane < 2) joins[lane].n = 0;
+        __syncwarp();
         for (uint32_t n = 0; ok; ++n) {
             Segment s;
             const bool more = next_segment<S>(a, run, s);
@@ -572,11 +583,13 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     it.first = s.ln.first; it.n = s.ln.n; it.seq = s.ln.seq; it.head = s.head; it.rt = s.rt;
                     it.lo = s.r.lo; it.hi = s.r.hi; it.tile = s.tile; it.tiles = s.tiles;
                     it.slot = !split ? -1 : begins ? 1 : 0;
-                    if (split && begins) {
+                    if (split) {
                         const int64_t left = (int64_t)s.ln.n * a.group - (int64_t)s.rt * S::kRows;
-                        join.parts = (int32_t)(run_owner(s.item0 + s.item_tiles - 1, plan.total, plan.grid) - blockIdx.x) + 1;
-                        join.rows = (int32_t)(left < S::kRows ? left : S::kRows);
-                        join.first = s.ln.first; join.head = s.head; join.rt = s.rt;
+                        Join &jn = joins[it.slot];
+                        jn.first_cta = (int32_t)run_owner(s.item0, plan.total, plan.grid);
+                        jn.n = (int32_t)run_owner(s.item0 + s.item_tiles - 1, plan.total, plan.grid) - jn.first_cta + 1;
+                        jn.rows = (int32_t)(left < S::kRows ? left : S::kRows);
+                        jn.first = s.ln.first; jn.head = s.head; jn.rt = s.rt;
                     }
                 }
                 mbar_arrive(&bar.item_full[n % kItems]);
@@ -614,7 +627,6 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 }
             }
         }
-        if (lane == 0) a.joins[blockIdx.x] = join;
         if (!ok) {
             // given up: the copies in flight still have to land (each stage's
             // last use; bounded, whatever the other waits did)
@@ -735,10 +747,16 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         const int pair = 1 + st * 4 + quad;                       // barrier of the two warps with these rows
         uint32_t tile_n = 0, s_n[2] = {0, 0}, pv_n = 0;           // tiles so far, units per S buffer, PVs of this stream
+        int published = -1;                                       // slot of a part just written
         for (uint32_t n = 0;; ++n) {
             const bool ok = wait(&bar.item_full[n % kItems], (n / kItems) & 1);
             // all softmax warps go on or none does: the barriers below count on it
-            if (named_barrier_any(kAllSoftmax, S::kSoftmaxWarps * 32, !ok)) break;
+            const bool stop = named_barrier_any(kAllSoftmax, S::kSoftmaxWarps * 32, !ok);
+            if (published >= 0) {            // the last item's part is complete
+                if (tid == 0) atom_add_acq_rel(a.counters + joins[published].first_cta, 1u);
+                published = -1;
+            }
+            if (stop) break;
             const Item &it = items[n % kItems];
             const int tiles = it.tiles;
             if (tiles == 0) break;
@@ -949,129 +967,95 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 }
             }
             fence_before();
+            if (split) __threadfence();      // the part, before its count past the next barrier
+            published = slot;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.item_empty[n % kItems]);
             // (O, the swap area and the pair barriers are used again only past the
             // barrier at the next item's start)
+        }
+
+        // ---- the items in parts: wait for the others' and join this CTA's share.
+        // A thread takes four columns of a row; where there are threads to spare,
+        // 2, 4 or 8 of them share an element's parts, each with its own running
+        // maximum, and their sums are added up in order.
+        constexpr int kT = S::kSoftmaxWarps * 32;
+        float *red = reinterpret_cast<float *>(kv_smem);          // [kT][6]: nothing is on its way there any more
+        for (int sl = 0; sl < 2; ++sl) {
+            const Join j = joins[sl];
+            if (j.n == 0) continue;
+            if (tid == 0) {
+                const unsigned int *published_parts = a.counters + j.first_cta;
+                const uint64_t t0 = global_ns();
+                while (ld_acquire(published_parts) < (unsigned)j.n) {
+                    if (*reinterpret_cast<volatile unsigned int *>(&s_gave_up)) break;
+                    if (global_ns() - t0 > kWaitLimitNs) {
+                        s_gave_up = 1u;
+                        atomicOr(&g_wait_timeouts, 1u);
+                    }
+                }
+                __threadfence();
+                // the last joiner leaves the counters at zero for the next call
+                if (atom_add_acq_rel(a.counters + kMaxSms + j.first_cta, 1u) == (unsigned)j.n - 1) {
+                    a.counters[j.first_cta] = 0u;
+                    a.counters[kMaxSms + j.first_cta] = 0u;
+                }
+            }
+            named_barrier(kAllSoftmax, kT);
+            const int all = j.rows * (D / 4), mine = (int)blockIdx.x - j.first_cta;
+            const int e0 = (int)((int64_t)all * mine / j.n), e1 = (int)((int64_t)all * (mine + 1) / j.n);
+            int lg = 0;                                            // log2 of the threads of an element
+            while (lg < 3 && (2 << lg) <= j.n && (e1 - e0) << (lg + 1) <= kT) ++lg;
+            const int step = 1 << lg;
+            for (int base = e0; base < e1; base += kT >> lg) {
+                const int e = base + (tid >> lg), p0 = tid & (step - 1);
+                float M = -INFINITY, L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+                auto add = [&](float mp, float lp, float x, float y, float z, float w) {
+                    if (mp == -INFINITY) return;
+                    const float Mn = fmaxf(M, mp), fo = M == -INFINITY ? 0.f : exp2_fast(M - Mn), fp = exp2_fast(mp - Mn);
+                    M = Mn;
+                    L = L * fo + lp * fp;
+                    o[0] = o[0] * fo + x * fp;
+                    o[1] = o[1] * fo + y * fp;
+                    o[2] = o[2] * fo + z * fp;
+                    o[3] = o[3] * fo + w * fp;
+                };
+                const int r = e < e1 ? e % j.rows : 0, c4 = e < e1 ? e / j.rows : 0;   // r: over the item's row tiles
+                if (e < e1) {
+#pragma unroll 4
+                    for (int p = p0; p < j.n; p += step) {
+                        const float *q = a.parts + ((int64_t)(j.first_cta + p) * 2 + (p == 0 ? 1 : 0)) * S::kPartFloats + (r >> 7) * 128 * (D + 2);
+                        const float mp = __ldcg(q + 128 * D + (r & 127)), lp = __ldcg(q + 128 * D + 128 + (r & 127));
+                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(q) + c4 * 128 + (r & 127));
+                        add(mp, lp, x.x, x.y, x.z, x.w);
+                    }
+                }
+                if (lg > 0) {
+                    float *mine6 = red + tid * 6;
+                    mine6[0] = M; mine6[1] = L; mine6[2] = o[0]; mine6[3] = o[1]; mine6[4] = o[2]; mine6[5] = o[3];
+                    __syncwarp();                                  // an element's threads are in one warp
+                    if (p0 == 0)
+                        for (int k = 1; k < step; ++k) {
+                            const float *q = mine6 + k * 6;
+                            add(q[0], q[1], q[2], q[3], q[4], q[5]);
+                        }
+                    __syncwarp();
+                }
+                if (e < e1 && p0 == 0) {
+                    const uint32_t g = (uint32_t)j.rt * S::kRows + r, tok = g / (uint32_t)a.group;
+                    const int64_t orow = ((int64_t)j.first + tok) * a.heads_q + (int64_t)j.head * a.group + (g - tok * a.group);
+                    const float iv = L > 0.f ? 1.f / L : 0.f;
+                    *reinterpret_cast<uint2 *>(a.out + orow * D + c4 * 4) =
+                        make_uint2(pack2<F16>(o[0] * iv, o[1] * iv), pack2<F16>(o[2] * iv, o[3] * iv));
+                    if (c4 == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+                }
+            }
         }
     }
     __syncthreads();
     if (warp == kMma) {
         fence_after();
         tmem_free(tmem);
-    }
-}
-
-// ---- the join -----------------------------------------------------------------
-
-constexpr int kJoinThreads = 256;
-
-// Join the parts of every split item: out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p,
-// lse = M + log2 of the sum.  A thread takes four columns of a row; of an item in many parts,
-// eight threads share them, each with its own running maximum.  The parts lie in L2; the
-// kernel is bound by their latency.
-template <int D, int QT, bool F16>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a, int ctas)
-{
-    using S = Shape<D, QT>;
-    __shared__ int32_t before[kMaxSms + 1];   // tasks before each entry
-    __shared__ int32_t warp_tasks[kJoinThreads / 32];
-    __shared__ float red[kJoinThreads][6];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kFew = 8;                   // up to so many parts a thread takes them all
-    constexpr int kEach = 4;                  // elements (four columns of a row) of a thread then
-    auto elements = [](int parts) { return parts > kFew ? kJoinThreads / 8 : kJoinThreads * kEach; };   // of a task
-    pdl_launch_dependents();
-    pdl_wait();
-    {
-        static_assert(kMaxSms == 2 * kJoinThreads, "");
-        int32_t mine[2], sum = 0;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int c = 2 * tid + k;
-            mine[k] = 0;
-            if (c < ctas) {
-                const int parts = __ldcg(&a.joins[c].parts), rows = __ldcg(&a.joins[c].rows);
-                if (parts > 0) mine[k] = (rows * (D / 4) + elements(parts) - 1) / elements(parts);
-            }
-            sum += mine[k];
-        }
-        int total;
-        const int excl = warp_exclusive_sum(sum, lane, total);
-        if (lane == 0) warp_tasks[warp] = total;
-        __syncthreads();
-        int base = excl;
-        for (int w = 0; w < warp; ++w) base += warp_tasks[w];
-        before[2 * tid] = base;
-        before[2 * tid + 1] = base + mine[0];
-        if (tid == kJoinThreads - 1) before[kMaxSms] = base + sum;
-        __syncthreads();
-    }
-    for (int task = blockIdx.x; task < before[kMaxSms]; task += gridDim.x) {
-        int lo = 0, hi = kMaxSms - 1;         // the last entry with before <= task that has tasks
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (before[mid] <= task) lo = mid; else hi = mid - 1;
-        }
-        const int cta = lo;
-        const Join j = a.joins[cta];
-        const int e0 = (task - before[cta]) * elements(j.parts), all = j.rows * (D / 4);
-        auto place = [&](int p) -> const float * { return a.parts + ((int64_t)(cta + p) * 2 + (p == 0 ? 1 : 0)) * S::kPartFloats; };
-        auto finish = [&](int e, float M, float L, const float (&o)[4]) {
-            const int r = e % j.rows, c = e / j.rows * 4;
-            const uint32_t g = (uint32_t)j.rt * S::kRows + r, tok = g / (uint32_t)a.group;
-            const int64_t orow = ((int64_t)j.first + tok) * a.heads_q + (int64_t)j.head * a.group + (g - tok * a.group);
-            const float iv = L > 0.f ? 1.f / L : 0.f;
-            *reinterpret_cast<uint2 *>(a.out + orow * D + c) = make_uint2(pack2<F16>(o[0] * iv, o[1] * iv), pack2<F16>(o[2] * iv, o[3] * iv));
-            if (c == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
-        };
-        // add parts p0, p0 + step, ... of element e
-        auto gather = [&](int e, int p0, int step, float &M, float &L, float (&o)[4]) {
-            const int r = e % j.rows, c4 = e / j.rows, tile = r >> 7, rr = r & 127;   // r: over the item's row tiles
-#pragma unroll 4
-            for (int p = p0; p < j.parts; p += step) {
-                const float *q = place(p) + tile * 128 * (D + 2);
-                const float mp = __ldcg(q + 128 * D + rr), lp = __ldcg(q + 128 * D + 128 + rr);
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(q) + c4 * 128 + rr);
-                if (mp == -INFINITY) continue;
-                const float Mn = fmaxf(M, mp), fo = M == -INFINITY ? 0.f : exp2_fast(M - Mn), fp = exp2_fast(mp - Mn);
-                M = Mn;
-                L = L * fo + lp * fp;
-                o[0] = o[0] * fo + x.x * fp; o[1] = o[1] * fo + x.y * fp;
-                o[2] = o[2] * fo + x.z * fp; o[3] = o[3] * fo + x.w * fp;
-            }
-        };
-        if (j.parts <= kFew) {
-#pragma unroll
-            for (int k = 0; k < kEach; ++k) {
-                const int e = e0 + k * kJoinThreads + tid;
-                if (e >= all) continue;
-                float M = -INFINITY, L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-                gather(e, 0, 1, M, L, o);
-                finish(e, M, L, o);
-            }
-        } else {
-            // warp w takes parts w, w + 8, ... of the task's 32 elements; warp 0 adds the eight up in order
-            const int e = e0 + lane;
-            float M = -INFINITY, L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-            if (e < all) gather(e, warp, 8, M, L, o);
-            float *mine = red[tid];
-            mine[0] = M; mine[1] = L; mine[2] = o[0]; mine[3] = o[1]; mine[4] = o[2]; mine[5] = o[3];
-            __syncthreads();
-            if (warp == 0 && e < all) {
-                for (int w = 1; w < 8; ++w) {
-                    const float *q = red[w * 32 + lane];
-                    if (q[0] == -INFINITY) continue;
-                    const float Mn = fmaxf(M, q[0]), fo = M == -INFINITY ? 0.f : exp2_fast(M - Mn), fp = exp2_fast(q[0] - Mn);
-                    M = Mn;
-                    L = L * fo + q[1] * fp;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) o[k] = o[k] * fo + q[2 + k] * fp;
-                }
-                finish(e, M, L, o);
-            }
-            __syncthreads();
-        }
     }
 }
 

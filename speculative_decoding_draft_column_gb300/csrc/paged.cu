@@ -110,8 +110,8 @@ constexpr int64_t kMaxStride = 1ll << 39;
 
 bool bad_stride(int64_t s) { return s < 0 || s >= kMaxStride || s % 8 != 0; }
 
-template <typename K, typename... A>
-spec_status launch(K kernel, dim3 grid, unsigned block, size_t smem, const A &...a)
+template <bool kCooperative = false, typename K, typename A>
+spec_status launch(K kernel, dim3 grid, unsigned block, size_t smem, const A &a)
 {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
@@ -119,12 +119,14 @@ spec_status launch(K kernel, dim3 grid, unsigned block, size_t smem, const A &..
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = host::stream();
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeCooperative;
+    attr[1].val.cooperative = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a...);
+    cfg.numAttrs = kCooperative ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
     host::count_launch();
     return SPEC_OK;
@@ -168,14 +170,11 @@ spec_status launch_attention(const Device &d, const attn::Args &a, bool f16)
 {
     using S = attn::Shape<D, QT>;
     static_assert(S::kPartFloats <= kPartFloats, "");
-    const int ctas = attention_grid(d);
+    const dim3 grid((unsigned)attention_grid(d));
     const size_t smem = (size_t)d.attn_smem[shape_index<D, QT>()][f16];
-    const spec_status st = f16 ? launch(attn::attention_kernel<D, QT, true>, dim3((unsigned)ctas), S::kThreads, smem, a)
-                               : launch(attn::attention_kernel<D, QT, false>, dim3((unsigned)ctas), S::kThreads, smem, a);
-    if (st != SPEC_OK) return st;
-    const dim3 join((unsigned)(4 * d.sms));
-    return f16 ? launch(attn::join_kernel<D, QT, true>, join, attn::kJoinThreads, 0, a, ctas)
-               : launch(attn::join_kernel<D, QT, false>, join, attn::kJoinThreads, 0, a, ctas);
+    // cooperative: CTAs wait for the parts of items that they share
+    return f16 ? launch<true>(attn::attention_kernel<D, QT, true>, grid, S::kThreads, smem, a)
+               : launch<true>(attn::attention_kernel<D, QT, false>, grid, S::kThreads, smem, a);
 }
 
 // The cache as TMA sees it: [page][head][block of 64][token][64], boxes of one
@@ -277,7 +276,7 @@ int64_t spec_paged_attention_workspace(void)
     Device *d = nullptr;
     const spec_status st = device(&d);
     if (st != SPEC_OK) return st;
-    return (int64_t)attn::kMaxSms * sizeof(attn::Join) + (int64_t)attention_grid(*d) * 2 * kPartFloats * 4;
+    return 2 * (int64_t)attn::kMaxSms * 4 + (int64_t)attention_grid(*d) * 2 * kPartFloats * 4;
 }
 
 spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
@@ -332,8 +331,8 @@ spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q,
     a.lanes = (int32_t)b.lanes; a.max_pages = b.max_pages;
     a.c = scale * attn::kLog2e; a.window = window;
     a.out = static_cast<uint16_t *>(out); a.lse = lse;
-    a.joins = static_cast<attn::Join *>(workspace);
-    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + attn::kMaxSms * sizeof(attn::Join));
+    a.counters = static_cast<unsigned int *>(workspace);
+    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + 2 * attn::kMaxSms * 4);
     const int64_t chunk = max_new > 0 ? max_new : (tokens + b.lanes - 1) / b.lanes;
     const bool two = chunk * a.group > 128;   // more rows than one tile: two tiles share every K/V tile
     const bool f16 = c.dtype == SPEC_F16;
