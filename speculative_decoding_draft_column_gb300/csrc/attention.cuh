@@ -302,17 +302,20 @@ struct Reach {
     int32_t tiles;     // at least 1, so that rows with no key are still answered
 };
 
+// (Rows of all new tokens are below 2^31, checked by the host: 32-bit divides, which
+// these few threads wait for, cost a tenth of 64-bit ones.)
 template <typename S>
 __device__ __forceinline__ Reach reach_of(const Args &a, int n, int seq, int rt)
 {
-    const int64_t row0 = (int64_t)rt * S::kRows;
-    const int f = (int)(row0 / a.group);
-    const int64_t last = (row0 + S::kRows - 1) / a.group;
-    const int e = last < n - 1 ? (int)last : n - 1;
+    const uint32_t row0 = (uint32_t)rt * S::kRows, g = (uint32_t)a.group;
+    const int last = (int)((row0 + S::kRows - 1) / g), e = last < n - 1 ? last : n - 1;
     Reach r;
     r.hi = seq - n + e + 1;
-    const int64_t lo = a.window > 0 ? (int64_t)(seq - n + f) - a.window + 1 : 0;
-    r.lo = lo > 0 ? (int)lo : 0;
+    r.lo = 0;
+    if (a.window > 0) {
+        const int64_t lo = (int64_t)(seq - n + (int)(row0 / g)) - a.window + 1;
+        r.lo = lo > 0 ? (int)lo : 0;
+    }
     if (r.hi > r.lo) {
         r.tile0 = r.lo / S::BK;
         r.tiles = (r.hi + S::BK - 1) / S::BK - r.tile0;
@@ -343,7 +346,7 @@ __device__ __forceinline__ Lane lane_of(const Args &a, int l)
 }
 
 template <typename S>
-__device__ __forceinline__ int row_tiles(const Args &a, int n) { return (int)(((int64_t)n * a.group + S::kRows - 1) / S::kRows); }
+__device__ __forceinline__ int row_tiles(const Args &a, int n) { return (int)(((uint32_t)n * (uint32_t)a.group + S::kRows - 1) / S::kRows); }
 
 template <typename S>
 __device__ __forceinline__ int64_t head_units(const Args &a, const Lane &l)
@@ -400,12 +403,13 @@ __device__ __forceinline__ bool next_segment(const Args &a, Run &w, Segment &s)
 struct Plan {
     int64_t total;         // units of the step
     int64_t lane_u;        // units before the lane where this CTA's run starts
+    int64_t per_head;      // units of one head of that lane
     int32_t lane, grid;    // that lane; CTAs that have a run
 };
 
-__device__ __forceinline__ int64_t run_start(int64_t cta, int64_t total, int64_t grid) { return cta * total / grid; }
+__device__ __forceinline__ int64_t run_start(int64_t cta, int64_t total, int64_t grid) { return udiv(cta * total, grid); }
 // the CTA whose run holds unit u
-__device__ __forceinline__ int64_t run_owner(int64_t u, int64_t total, int64_t grid) { return ((u + 1) * grid + total - 1) / total - 1; }
+__device__ __forceinline__ int64_t run_owner(int64_t u, int64_t total, int64_t grid) { return udiv((u + 1) * grid + total - 1, total) - 1; }
 
 // ---- the kernel ---------------------------------------------------------------
 
@@ -490,25 +494,42 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
     if (warp == kMma) tmem_alloc(&tmem_slot);
     pdl_wait();
 
-    // Units of the step and the lane where this CTA's run starts: each thread
-    // sums a contiguous share of the lanes.
+    // Units of the step and the lane where this CTA's run starts.  Few lanes: a
+    // warp each, its threads sharing the row tiles; many: each thread sums a
+    // contiguous share of them.
     {
+        constexpr int kWarps = S::kThreads / 32;
+        const bool by_warp = a.lanes <= kWarps;
         const int per = (a.lanes + S::kThreads - 1) / S::kThreads;
-        const int l0 = min(tid * per, a.lanes), l1 = min(l0 + per, a.lanes);
-        int64_t mine = 0;
-        for (int l = l0; l < l1; ++l) mine += head_units<S>(a, lane_of(a, l)) * a.heads_kv;
-        int64_t incl = mine;
+        const int l0 = by_warp ? warp : min(tid * per, a.lanes), l1 = by_warp ? min(warp + 1, a.lanes) : min(l0 + per, a.lanes);
+        int64_t mine = 0, head = 0, incl;
+        if (by_warp) {
+            if (l0 < l1) {
+                const Lane ln = lane_of(a, l0);
+                const int rts = row_tiles<S>(a, ln.n);
+                for (int rt = lane; rt < rts; rt += 32) head += reach_of<S>(a, ln.n, ln.seq, rt).tiles;
+            }
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(kFull, incl, d);
-            if (lane >= d) incl += y;
+            for (int d = 16; d; d >>= 1) head += __shfl_xor_sync(kFull, head, d);
+            incl = mine = head * a.heads_kv;
+        } else {
+            for (int l = l0; l < l1; ++l) {
+                head = head_units<S>(a, lane_of(a, l));
+                mine += head * a.heads_kv;
+            }
+            incl = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t y = __shfl_up_sync(kFull, incl, d);
+                if (lane >= d) incl += y;
+            }
         }
         if (lane == 31) warp_units[warp] = incl;
         fence_before();
         __syncthreads();
         fence_after();
         int64_t before = incl - mine, total = 0;
-        for (int w = 0; w < S::kThreads / 32; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             if (w < warp) before += warp_units[w];
             total += warp_units[w];
         }
@@ -519,16 +540,18 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         }
         if ((int64_t)blockIdx.x < grid) {
             const int64_t u0 = run_start(blockIdx.x, total, grid);
-            if (u0 >= before && u0 < before + mine) {
+            if (u0 >= before && u0 < before + mine && (!by_warp || lane == 0)) {
                 int64_t at = before;
                 int l = l0;
-                for (;; ++l) {
-                    const int64_t u = head_units<S>(a, lane_of(a, l)) * a.heads_kv;
-                    if (u0 < at + u) break;
-                    at += u;
-                }
+                if (l1 - l0 > 1)
+                    for (;; ++l) {
+                        head = head_units<S>(a, lane_of(a, l));
+                        if (u0 < at + head * a.heads_kv) break;
+                        at += head * a.heads_kv;
+                    }
                 plan.lane = l;
                 plan.lane_u = at;
+                plan.per_head = head;
             }
         }
         __syncthreads();
@@ -551,15 +574,23 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             run.lane = plan.lane;
             run.ln = lane_of(a, run.lane);
             run.rts = row_tiles<S>(a, run.ln.n);
-            const int64_t per_head = head_units<S>(a, run.ln), off = run.u - plan.lane_u;
-            run.head = (int)udiv(off, per_head);
-            run.item0 = plan.lane_u + run.head * per_head;
-            run.rt = 0;
-            for (;;) {
-                const int t = reach_of<S>(a, run.ln.n, run.ln.seq, run.rt).tiles;
-                if (run.u < run.item0 + t) break;
-                run.item0 += t;
-                ++run.rt;
+            const int64_t off = run.u - plan.lane_u;
+            run.head = (int)udiv(off, plan.per_head);
+            run.item0 = plan.lane_u + run.head * plan.per_head;
+            // the row tile: 32 at a time
+            for (run.rt = 0;; run.rt += 32) {
+                const int rt = run.rt + lane;
+                int all;
+                const int tiles = rt < run.rts ? reach_of<S>(a, run.ln.n, run.ln.seq, rt).tiles : 0;
+                const int before = warp_exclusive_sum(tiles, lane, all);
+                if (run.u < run.item0 + all) {
+                    const uint32_t past = __ballot_sync(kFull, run.u < run.item0 + before + tiles);
+                    const int k = __ffs(past) - 1;
+                    run.rt += k;
+                    run.item0 += __shfl_sync(kFull, before, k);
+                    break;
+                }
+                run.item0 += all;
             }
         }
         const int rows = min(1 << a.log_page, S::BK);            // rows of a box
