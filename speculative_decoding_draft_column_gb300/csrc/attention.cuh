@@ -815,9 +815,10 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     const int from = valid ? klo - key0 - half * kW : 0, to = valid ? khi - key0 - half * kW : kW;
                     const bool edge = __any_sync(kFull, from > 0 || to < kW);
                     // two passes over S in TMEM (other warps hide the loads; the
-                    // half row in registers would not fit)
+                    // half row in registers would not fit), rolled: the kernel's
+                    // code is read from L2 once a launch, and its size counts
                     float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < kW; c += 32) {
                         uint32_t x[32];
                         tmem_ld32(x, sa + c);
@@ -859,7 +860,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     const float ref = m == -INFINITY ? 0.f : m;
                     const uint64_t cc = two(a.c, a.c), mm = two(-ref, -ref);
                     uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < kW; c += 32) {
                         // P of columns c .. c+31 covers columns c/2 .. c/2+15 of this half's S, read before
                         uint32_t x[32], pk[16];
