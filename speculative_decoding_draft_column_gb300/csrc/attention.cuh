@@ -63,6 +63,7 @@ struct Shape {
     static constexpr int kSwap = 512;                          // floats that softmax warps exchange through
     static constexpr int kPayload = QB * QT * kQBytes + kStages * kStageBytes + kSwap * 4;
     static constexpr int kRows = QT * 128;
+    static constexpr int kLeast = QT == 1 ? 2 : 1;             // units of a run that an item is cut into, at least
     // TMEM columns: S buffers, then O
     static constexpr int kO = 2 * BK;
     static constexpr int kPartFloats = kRows * (D + 2);        // O, then m and sum
@@ -400,16 +401,18 @@ __device__ __forceinline__ bool next_segment(const Args &a, Run &w, Segment &s)
     return true;
 }
 
+// Run c is units [floor(c * total / grid), floor((c + 1) * total / grid)).
 struct Plan {
     int64_t total;         // units of the step
+    int64_t each;          // total / grid
     int64_t lane_u;        // units before the lane where this CTA's run starts
     int64_t per_head;      // units of one head of that lane
-    int32_t lane, grid;    // that lane; CTAs that have a run
+    int32_t more, lane, grid;   // total % grid; that lane; CTAs that have a run
 };
 
-__device__ __forceinline__ int64_t run_start(int64_t cta, int64_t total, int64_t grid) { return udiv(cta * total, grid); }
+__device__ __forceinline__ int64_t run_start(int cta, int64_t each, int32_t more, int32_t grid) { return cta * each + (uint32_t)(cta * more) / (uint32_t)grid; }
 // the CTA whose run holds unit u
-__device__ __forceinline__ int64_t run_owner(int64_t u, int64_t total, int64_t grid) { return udiv((u + 1) * grid + total - 1, total) - 1; }
+__device__ __forceinline__ int run_owner(int64_t u, int64_t total, int32_t grid) { return (int)udiv((u + 1) * grid + total - 1, total) - 1; }
 
 // ---- the kernel ---------------------------------------------------------------
 
@@ -502,19 +505,23 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         const bool by_warp = a.lanes <= kWarps;
         const int per = (a.lanes + S::kThreads - 1) / S::kThreads;
         const int l0 = by_warp ? warp : min(tid * per, a.lanes), l1 = by_warp ? min(warp + 1, a.lanes) : min(l0 + per, a.lanes);
+        // units in the low bits, items (a CTA of its own each, if there are enough) above
+        constexpr int kItemBit = 40;
+        constexpr int64_t kUnits = (1ll << kItemBit) - 1;
         int64_t mine = 0, head = 0, incl;
         if (by_warp) {
             if (l0 < l1) {
                 const Lane ln = lane_of(a, l0);
                 const int rts = row_tiles<S>(a, ln.n);
-                for (int rt = lane; rt < rts; rt += 32) head += reach_of<S>(a, ln.n, ln.seq, rt).tiles;
+                for (int rt = lane; rt < rts; rt += 32) head += reach_of<S>(a, ln.n, ln.seq, rt).tiles + (1ll << kItemBit);
             }
 #pragma unroll
             for (int d = 16; d; d >>= 1) head += __shfl_xor_sync(kFull, head, d);
             incl = mine = head * a.heads_kv;
         } else {
             for (int l = l0; l < l1; ++l) {
-                head = head_units<S>(a, lane_of(a, l));
+                const Lane ln = lane_of(a, l);
+                head = head_units<S>(a, ln) + ((int64_t)row_tiles<S>(a, ln.n) << kItemBit);
                 mine += head * a.heads_kv;
             }
             incl = mine;
@@ -528,18 +535,34 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         fence_before();
         __syncthreads();
         fence_after();
-        int64_t before = incl - mine, total = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += warp_units[w];
-            total += warp_units[w];
+        static_assert(kWarps <= 32, "");
+        int64_t upto = lane < kWarps ? warp_units[lane] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(kFull, upto, d);
+            if (lane >= d) upto += y;
         }
-        const int64_t grid = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
+        const int64_t all = __shfl_sync(kFull, upto, 31), total = all & kUnits;
+        const int64_t before = (__shfl_sync(kFull, upto, warp) - warp_units[warp] + incl - mine) & kUnits;
+        mine &= kUnits;
+        head &= kUnits;
+        // As many runs as there are CTAs, but not so many that an item has to be
+        // cut into runs of less than kLeast units: the streams of a CTA work on two
+        // tiles at once, and parts have to be joined.
+        int64_t grid = all >> kItemBit;
+        const int64_t some = (total + S::kLeast - 1) / S::kLeast;
+        if (grid < some) grid = some;
+        if (grid > (int64_t)gridDim.x) grid = gridDim.x;
+        const int64_t each = grid > 0 ? udiv(total, grid) : 0;
+        const int32_t more = (int32_t)(total - each * grid);
         if (tid == 0) {
             plan.total = total;
+            plan.each = each;
+            plan.more = more;
             plan.grid = (int32_t)grid;
         }
         if ((int64_t)blockIdx.x < grid) {
-            const int64_t u0 = run_start(blockIdx.x, total, grid);
+            const int64_t u0 = run_start(blockIdx.x, each, more, (int32_t)grid);
             if (u0 >= before && u0 < before + mine && (!by_warp || lane == 0)) {
                 int64_t at = before;
                 int l = l0;
@@ -568,9 +591,8 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         Run run;
         run.u = run.end = 0;
         if ((int64_t)blockIdx.x < plan.grid) {
-            const int64_t total = plan.total;
-            run.u = run_start(blockIdx.x, total, plan.grid);
-            run.end = run_start(blockIdx.x + 1, total, plan.grid);
+            run.u = run_start(blockIdx.x, plan.each, plan.more, plan.grid);
+            run.end = run_start(blockIdx.x + 1, plan.each, plan.more, plan.grid);
             run.lane = plan.lane;
             run.ln = lane_of(a, run.lane);
             run.rts = row_tiles<S>(a, run.ln.n);
@@ -597,6 +619,11 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         const int boxes = S::BK / rows;
         const bool whole = rows == S::BK;                        // one box brings all blocks
         const uint32_t box_bytes = (uint32_t)rows * D * 2;
+        auto page_of = [&](const Segment &s, int t) -> int {     // of this lane's box of tile t
+            const int64_t k0 = (int64_t)(s.tile + t) * S::BK + lane * rows, pi = k0 >> a.log_page;
+            return lane < boxes && k0 < s.r.hi && k0 + rows > s.r.lo && pi < a.max_pages
+                       ? __ldg(a.block_table + s.lane * a.max_pages + pi) : -1;
+        };
         uint32_t idx = 0;                                        // stage uses so far
         bool ok = true;
         if (lane < 2) joins[lane].n = 0;
@@ -604,6 +631,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         for (uint32_t n = 0; ok; ++n) {
             Segment s;
             const bool more = next_segment<S>(a, run, s);
+            int page = more ? page_of(s, 0) : -1;                // on its way while the item is handed out
             ok = __all_sync(kFull, wait(&bar.item_empty[n % kItems], ((n / kItems) & 1) ^ 1));
             if (!ok) break;
             if (lane == 0) {
@@ -614,27 +642,15 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     it.first = s.ln.first; it.n = s.ln.n; it.seq = s.ln.seq; it.head = s.head; it.rt = s.rt;
                     it.lo = s.r.lo; it.hi = s.r.hi; it.tile = s.tile; it.tiles = s.tiles;
                     it.slot = !split ? -1 : begins ? 1 : 0;
-                    if (split) {
-                        const int64_t left = (int64_t)s.ln.n * a.group - (int64_t)s.rt * S::kRows;
-                        Join &jn = joins[it.slot];
-                        jn.first_cta = (int32_t)run_owner(s.item0, plan.total, plan.grid);
-                        jn.n = (int32_t)run_owner(s.item0 + s.item_tiles - 1, plan.total, plan.grid) - jn.first_cta + 1;
-                        jn.rows = (int32_t)(left < S::kRows ? left : S::kRows);
-                        jn.first = s.ln.first; jn.head = s.head; jn.rt = s.rt;
-                    }
                 }
                 mbar_arrive(&bar.item_full[n % kItems]);
             }
             __syncwarp();
             if (!more) break;
             for (int t = 0; t < s.tiles && ok; ++t) {
-                const int key0 = (s.tile + t) * S::BK, k0 = key0 + lane * rows;
+                const int k0 = (s.tile + t) * S::BK + lane * rows;
                 const bool mine = lane < boxes && k0 < s.r.hi && k0 + rows > s.r.lo;
-                int page = -1;
-                if (mine) {
-                    const int64_t pi = k0 >> a.log_page;
-                    if (pi < a.max_pages) page = __ldg(a.block_table + s.lane * a.max_pages + pi);
-                }
+                if (t > 0) page = page_of(s, t);
                 const uint32_t bytes = __popc(__ballot_sync(kFull, mine)) * box_bytes;
                 const int row = k0 & ((1 << a.log_page) - 1);
 #pragma unroll
@@ -656,6 +672,14 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     }
                     __syncwarp();
                 }
+            }
+            if (lane == 0 && s.tiles < s.item_tiles) {           // (seen with the next item, or with the end)
+                const int64_t left = (int64_t)s.ln.n * a.group - (int64_t)s.rt * S::kRows;
+                Join &jn = joins[s.tile == s.r.tile0 ? 1 : 0];
+                jn.first_cta = run_owner(s.item0, plan.total, plan.grid);
+                jn.n = run_owner(s.item0 + s.item_tiles - 1, plan.total, plan.grid) - jn.first_cta + 1;
+                jn.rows = (int32_t)(left < S::kRows ? left : S::kRows);
+                jn.first = s.ln.first; jn.head = s.head; jn.rt = s.rt;
             }
         }
         if (!ok) {
