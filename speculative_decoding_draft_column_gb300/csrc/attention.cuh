@@ -808,7 +808,10 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             // all softmax warps go on or none does: the barriers below count on it
             const bool stop = named_barrier_any(kAllSoftmax, S::kSoftmaxWarps * 32, !ok);
             if (published >= 0) {            // the last item's part is complete
-                if (tid == 0) atom_add_acq_rel(a.counters + joins[published].first_cta, 1u);
+                if (tid == 0) {              // (the barrier orders the other threads' writes before this fence)
+                    __threadfence();
+                    atom_add_acq_rel(a.counters + joins[published].first_cta, 1u);
+                }
                 published = -1;
             }
             if (stop) break;
@@ -1023,7 +1026,6 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 }
             }
             fence_before();
-            if (split) __threadfence();      // the part, before its count past the next barrier
             published = slot;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.item_empty[n % kItems]);
@@ -1037,27 +1039,27 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         // maximum, and their sums are added up in order.
         constexpr int kT = S::kSoftmaxWarps * 32;
         float *red = reinterpret_cast<float *>(kv_smem);          // [kT][6]: nothing is on its way there any more
+        if (lane == 0 && warp < 2 && joins[warp].n > 0) {         // a warp waits for each of the two items
+            const Join &j = joins[warp];
+            const uint64_t t0 = global_ns();
+            while (ld_acquire(a.counters + j.first_cta) < (unsigned)j.n) {
+                if (*reinterpret_cast<volatile unsigned int *>(&s_gave_up)) break;
+                if (global_ns() - t0 > kWaitLimitNs) {
+                    s_gave_up = 1u;
+                    atomicOr(&g_wait_timeouts, 1u);
+                }
+            }
+            __threadfence();
+            // the last joiner leaves the counters at zero for the next call
+            if (atom_add_acq_rel(a.counters + kMaxSms + j.first_cta, 1u) == (unsigned)j.n - 1) {
+                a.counters[j.first_cta] = 0u;
+                a.counters[kMaxSms + j.first_cta] = 0u;
+            }
+        }
+        if (joins[0].n + joins[1].n > 0) named_barrier(kAllSoftmax, kT);
         for (int sl = 0; sl < 2; ++sl) {
             const Join j = joins[sl];
             if (j.n == 0) continue;
-            if (tid == 0) {
-                const unsigned int *published_parts = a.counters + j.first_cta;
-                const uint64_t t0 = global_ns();
-                while (ld_acquire(published_parts) < (unsigned)j.n) {
-                    if (*reinterpret_cast<volatile unsigned int *>(&s_gave_up)) break;
-                    if (global_ns() - t0 > kWaitLimitNs) {
-                        s_gave_up = 1u;
-                        atomicOr(&g_wait_timeouts, 1u);
-                    }
-                }
-                __threadfence();
-                // the last joiner leaves the counters at zero for the next call
-                if (atom_add_acq_rel(a.counters + kMaxSms + j.first_cta, 1u) == (unsigned)j.n - 1) {
-                    a.counters[j.first_cta] = 0u;
-                    a.counters[kMaxSms + j.first_cta] = 0u;
-                }
-            }
-            named_barrier(kAllSoftmax, kT);
             const int all = j.rows * (D / 4), mine = (int)blockIdx.x - j.first_cta;
             const int e0 = (int)((int64_t)all * mine / j.n), e1 = (int)((int64_t)all * (mine + 1) / j.n);
             int lg = 0;                                            // log2 of the threads of an element
@@ -1067,8 +1069,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 const int e = base + (tid >> lg), p0 = tid & (step - 1);
                 float M = -INFINITY, L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
                 auto add = [&](float mp, float lp, float x, float y, float z, float w) {
-                    if (mp == -INFINITY) return;
-                    const float Mn = fmaxf(M, mp), fo = M == -INFINITY ? 0.f : exp2_fast(M - Mn), fp = exp2_fast(mp - Mn);
+                    const float Mn = fmaxf(M, mp), ref = Mn == -INFINITY ? 0.f : Mn, fo = exp2_fast(M - ref), fp = exp2_fast(mp - ref);
                     M = Mn;
                     L = L * fo + lp * fp;
                     o[0] = o[0] * fo + x * fp;
