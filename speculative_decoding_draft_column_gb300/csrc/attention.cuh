@@ -76,6 +76,7 @@ struct Args {
     const uint16_t *q;
     int64_t tokens, qs_t, qs_h;
     int32_t heads_q, heads_kv, group, log_page;
+    uint32_t group_magic, group_shift;   // n / group = (umulhi(n, magic) + n) >> shift for n below 2^31
     const int32_t *block_table, *cu_new, *seq_lens;
     int64_t max_pages;
     int32_t lanes;
@@ -296,6 +297,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 
 // ---- the step's items ---------------------------------------------------------
 
+// Rows of all new tokens are below 2^31 (checked by the host), and the divisor is
+// the same for all: a multiplication by its reciprocal, rounded up to 33 bits.  (The
+// plan of the runs and the loads of Q wait for these divides; the 64-bit ones of a
+// first version took 3 us of a call.)
+__device__ __forceinline__ uint32_t div_group(const Args &a, uint32_t n) { return (__umulhi(n, a.group_magic) + n) >> a.group_shift; }
+
 // A row-tile group of a lane: the keys any of its rows attends, and the K/V tiles.
 struct Reach {
     int32_t lo, hi;    // keys [lo, hi); hi <= lo: none
@@ -303,18 +310,16 @@ struct Reach {
     int32_t tiles;     // at least 1, so that rows with no key are still answered
 };
 
-// (Rows of all new tokens are below 2^31, checked by the host: 32-bit divides, which
-// these few threads wait for, cost a tenth of 64-bit ones.)
 template <typename S>
 __device__ __forceinline__ Reach reach_of(const Args &a, int n, int seq, int rt)
 {
-    const uint32_t row0 = (uint32_t)rt * S::kRows, g = (uint32_t)a.group;
-    const int last = (int)((row0 + S::kRows - 1) / g), e = last < n - 1 ? last : n - 1;
+    const uint32_t row0 = (uint32_t)rt * S::kRows;
+    const int last = (int)div_group(a, row0 + S::kRows - 1), e = last < n - 1 ? last : n - 1;
     Reach r;
     r.hi = seq - n + e + 1;
     r.lo = 0;
     if (a.window > 0) {
-        const int64_t lo = (int64_t)(seq - n + (int)(row0 / g)) - a.window + 1;
+        const int64_t lo = (int64_t)(seq - n + (int)div_group(a, row0)) - a.window + 1;
         r.lo = lo > 0 ? (int)lo : 0;
     }
     if (r.hi > r.lo) {
@@ -785,7 +790,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
 #pragma unroll 8
             for (int i = t0; i < valid * kPieces; i += 64) {
                 const int r = i / kPieces, p = i % kPieces;
-                const uint32_t gr = (uint32_t)row0 + r, tok = gr / (uint32_t)a.group;   // rows fit 31 bits (checked)
+                const uint32_t gr = (uint32_t)row0 + r, tok = div_group(a, gr);
                 const int h = it.head * a.group + (int)(gr - tok * a.group);
                 const uint4 x = __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)(it.first + (int)tok) * a.qs_t + h * a.qs_h) + p);
                 *reinterpret_cast<uint4 *>(dst + (r >> 7) * S::kQBytes + (p >> 3) * (128 * 128) + (r & 127) * 128 +
@@ -821,7 +826,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             const int lo = it.lo, hi = it.hi, tile0 = it.tile;
             const int64_t gr = (int64_t)it.rt * S::kRows + (QT == 2 ? st * 128 : 0) + row;
             const bool valid = gr < (int64_t)it.n * a.group;
-            const int tok = valid ? (int)((uint32_t)gr / (uint32_t)a.group) : 0;
+            const int tok = valid ? (int)div_group(a, (uint32_t)gr) : 0;
             const int pos = it.seq - it.n + tok;
             const int64_t klo64 = a.window > 0 ? (int64_t)pos - a.window + 1 : 0;
             const int klo = klo64 > 0 ? (int)klo64 : 0, khi = valid ? pos + 1 : klo;   // keys of this row
@@ -1065,46 +1070,69 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             int lg = 0;                                            // log2 of the threads of an element
             while (lg < 3 && (2 << lg) <= j.n && (e1 - e0) << (lg + 1) <= kT) ++lg;
             const int step = 1 << lg;
-            for (int base = e0; base < e1; base += kT >> lg) {
-                const int e = base + (tid >> lg), p0 = tid & (step - 1);
-                float M = -INFINITY, L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-                auto add = [&](float mp, float lp, float x, float y, float z, float w) {
-                    const float Mn = fmaxf(M, mp), ref = Mn == -INFINITY ? 0.f : Mn, fo = exp2_fast(M - ref), fp = exp2_fast(mp - ref);
-                    M = Mn;
-                    L = L * fo + lp * fp;
-                    o[0] = o[0] * fo + x * fp;
-                    o[1] = o[1] * fo + y * fp;
-                    o[2] = o[2] * fo + z * fp;
-                    o[3] = o[3] * fo + w * fp;
+            const float *first_part = a.parts + ((int64_t)j.first_cta * 2 + 1) * S::kPartFloats;   // the others: one slot on, then every second
+            constexpr int kTwo = 2;                                // elements of a thread in flight
+            for (int base = e0; base < e1; base += kTwo * (kT >> lg)) {
+                const int p0 = tid & (step - 1);
+                int r[kTwo], c4[kTwo];
+                bool on[kTwo];
+                float M[kTwo], L[kTwo], o[kTwo][4];
+                auto add = [&](int u, float mp, float lp, float x, float y, float z, float w) {
+                    const float Mn = fmaxf(M[u], mp), ref = Mn == -INFINITY ? 0.f : Mn, fo = exp2_fast(M[u] - ref), fp = exp2_fast(mp - ref);
+                    M[u] = Mn;
+                    L[u] = L[u] * fo + lp * fp;
+                    o[u][0] = o[u][0] * fo + x * fp;
+                    o[u][1] = o[u][1] * fo + y * fp;
+                    o[u][2] = o[u][2] * fo + z * fp;
+                    o[u][3] = o[u][3] * fo + w * fp;
                 };
-                const int r = e < e1 ? e % j.rows : 0, c4 = e < e1 ? e / j.rows : 0;   // r: over the item's row tiles
-                if (e < e1) {
-#pragma unroll 4
-                    for (int p = p0; p < j.n; p += step) {
-                        const float *q = a.parts + ((int64_t)(j.first_cta + p) * 2 + (p == 0 ? 1 : 0)) * S::kPartFloats + (r >> 7) * 128 * (D + 2);
-                        const float mp = __ldcg(q + 128 * D + (r & 127)), lp = __ldcg(q + 128 * D + 128 + (r & 127));
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(q) + c4 * 128 + (r & 127));
-                        add(mp, lp, x.x, x.y, x.z, x.w);
+#pragma unroll
+                for (int u = 0; u < kTwo; ++u) {
+                    const int e = base + u * (kT >> lg) + (tid >> lg);
+                    on[u] = e < e1;
+                    c4[u] = on[u] ? e / j.rows : 0;
+                    r[u] = on[u] ? e - c4[u] * j.rows : 0;         // over the item's row tiles
+                    M[u] = -INFINITY;
+                    L[u] = o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
+                }
+#pragma unroll 2
+                for (int p = p0; p < j.n; p += step) {
+                    const float *part = p == 0 ? first_part : first_part + (int64_t)(2 * p - 1) * S::kPartFloats;
+                    float mp[kTwo], lp[kTwo];
+                    float4 x[kTwo];
+#pragma unroll
+                    for (int u = 0; u < kTwo; ++u) {
+                        const float *q = part + (r[u] >> 7) * 128 * (D + 2);
+                        mp[u] = __ldcg(q + 128 * D + (r[u] & 127));
+                        lp[u] = __ldcg(q + 128 * D + 128 + (r[u] & 127));
+                        x[u] = __ldcg(reinterpret_cast<const float4 *>(q) + c4[u] * 128 + (r[u] & 127));
                     }
+#pragma unroll
+                    for (int u = 0; u < kTwo; ++u) add(u, mp[u], lp[u], x[u].x, x[u].y, x[u].z, x[u].w);
                 }
                 if (lg > 0) {
-                    float *mine6 = red + tid * 6;
-                    mine6[0] = M; mine6[1] = L; mine6[2] = o[0]; mine6[3] = o[1]; mine6[4] = o[2]; mine6[5] = o[3];
-                    __syncwarp();                                  // an element's threads are in one warp
-                    if (p0 == 0)
-                        for (int k = 1; k < step; ++k) {
-                            const float *q = mine6 + k * 6;
-                            add(q[0], q[1], q[2], q[3], q[4], q[5]);
-                        }
-                    __syncwarp();
+#pragma unroll
+                    for (int u = 0; u < kTwo; ++u) {
+                        float *mine6 = red + tid * 6;
+                        mine6[0] = M[u]; mine6[1] = L[u]; mine6[2] = o[u][0]; mine6[3] = o[u][1]; mine6[4] = o[u][2]; mine6[5] = o[u][3];
+                        __syncwarp();                              // an element's threads are in one warp
+                        if (p0 == 0)
+                            for (int k = 1; k < step; ++k) {
+                                const float *q = mine6 + k * 6;
+                                add(u, q[0], q[1], q[2], q[3], q[4], q[5]);
+                            }
+                        __syncwarp();
+                    }
                 }
-                if (e < e1 && p0 == 0) {
-                    const uint32_t g = (uint32_t)j.rt * S::kRows + r, tok = g / (uint32_t)a.group;
+#pragma unroll
+                for (int u = 0; u < kTwo; ++u) {
+                    if (!on[u] || p0 != 0) continue;
+                    const uint32_t g = (uint32_t)j.rt * S::kRows + r[u], tok = div_group(a, g);
                     const int64_t orow = ((int64_t)j.first + tok) * a.heads_q + (int64_t)j.head * a.group + (g - tok * a.group);
-                    const float iv = L > 0.f ? 1.f / L : 0.f;
-                    *reinterpret_cast<uint2 *>(a.out + orow * D + c4 * 4) =
-                        make_uint2(pack2<F16>(o[0] * iv, o[1] * iv), pack2<F16>(o[2] * iv, o[3] * iv));
-                    if (c4 == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+                    const float iv = L[u] > 0.f ? 1.f / L[u] : 0.f;
+                    *reinterpret_cast<uint2 *>(a.out + orow * D + c4[u] * 4) =
+                        make_uint2(pack2<F16>(o[u][0] * iv, o[u][1] * iv), pack2<F16>(o[u][2] * iv, o[u][3] * iv));
+                    if (c4[u] == 0 && a.lse) a.lse[orow] = L[u] > 0.f ? (M[u] + log2f(L[u])) * kLn2 : -INFINITY;
                 }
             }
         }

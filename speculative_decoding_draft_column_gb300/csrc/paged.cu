@@ -327,6 +327,8 @@ spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q,
     a.tokens = tokens; a.qs_t = q_token_stride; a.qs_h = q_head_stride;
     a.heads_q = heads_q; a.heads_kv = c.heads; a.group = heads_q / c.heads;
     while ((1 << a.log_page) < c.page_size) ++a.log_page;
+    while ((1u << a.group_shift) < (uint32_t)a.group) ++a.group_shift;
+    a.group_magic = (uint32_t)((((1ull << a.group_shift) - a.group) << 32) / a.group + 1);
     a.block_table = b.block_table; a.cu_new = b.cu_new; a.seq_lens = b.seq_lens;
     a.lanes = (int32_t)b.lanes; a.max_pages = b.max_pages;
     a.c = scale * attn::kLog2e; a.window = window;
