@@ -32,7 +32,9 @@
 // launch is cooperative, so all CTAs are there; runs are equal, so the wait is
 // short, and it is bounded.  One token of one head over 19,456 keys, 152 parts: 47 us
 // with the last part's CTA joining alone -- 927 us for 128 rows of 256 --, 24 and 28 us with a
-// second kernel, which costs every call 4 us.)  The loader warp works the items out and hands
+// second kernel, which costs every call 4 us.)  Where the table's width bounds all
+// parts of an item to little, the last part's CTA does join alone, and the launch
+// is an ordinary one: 2 us less outside of graphs.  The loader warp works the items out and hands
 // them to the others through a ring in shared memory.
 #pragma once
 
@@ -80,6 +82,7 @@ struct Args {
     const int32_t *block_table, *cu_new, *seq_lens;
     int64_t max_pages;
     int32_t lanes;
+    int32_t share_joins;   // the CTAs of an item share its join (a cooperative launch); else its last part's CTA does it
     float c;               // scale * log2(e)
     int64_t window;
     uint16_t *out;
@@ -468,6 +471,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
     __shared__ Bars<S> bar;
     __shared__ Item items[kItems];
     __shared__ Join joins[2];      // of the parts in this CTA's first and second slot
+    __shared__ int32_t came_last[2];   // this CTA's part was the item's last (where joins are not shared)
     __shared__ uint32_t tmem_slot;
     __shared__ Plan plan;
     __shared__ int64_t warp_units[S::kThreads / 32];
@@ -631,7 +635,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         };
         uint32_t idx = 0;                                        // stage uses so far
         bool ok = true;
-        if (lane < 2) joins[lane].n = 0;
+        if (lane < 2) joins[lane].n = came_last[lane] = 0;
         __syncwarp();
         for (uint32_t n = 0; ok; ++n) {
             Segment s;
@@ -815,7 +819,12 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             if (published >= 0) {            // the last item's part is complete
                 if (tid == 0) {              // (the barrier orders the other threads' writes before this fence)
                     __threadfence();
-                    atom_add_acq_rel(a.counters + joins[published].first_cta, 1u);
+                    const Join &j = joins[published];
+                    const uint32_t before = atom_add_acq_rel(a.counters + j.first_cta, 1u);
+                    if (!a.share_joins && before == (uint32_t)j.n - 1) {
+                        came_last[published] = 1;
+                        a.counters[j.first_cta] = 0u;
+                    }
                 }
                 published = -1;
             }
@@ -1044,7 +1053,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         // maximum, and their sums are added up in order.
         constexpr int kT = S::kSoftmaxWarps * 32;
         float *red = reinterpret_cast<float *>(kv_smem);          // [kT][6]: nothing is on its way there any more
-        if (lane == 0 && warp < 2 && joins[warp].n > 0) {         // a warp waits for each of the two items
+        if (a.share_joins && lane == 0 && warp < 2 && joins[warp].n > 0) {   // a warp waits for each of the two items
             const Join &j = joins[warp];
             const uint64_t t0 = global_ns();
             while (ld_acquire(a.counters + j.first_cta) < (unsigned)j.n) {
@@ -1064,9 +1073,9 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         if (joins[0].n + joins[1].n > 0) named_barrier(kAllSoftmax, kT);
         for (int sl = 0; sl < 2; ++sl) {
             const Join j = joins[sl];
-            if (j.n == 0) continue;
-            const int all = j.rows * (D / 4), mine = (int)blockIdx.x - j.first_cta;
-            const int e0 = (int)((int64_t)all * mine / j.n), e1 = (int)((int64_t)all * (mine + 1) / j.n);
+            if (j.n == 0 || !(a.share_joins || came_last[sl])) continue;
+            const int all = j.rows * (D / 4), sharers = a.share_joins ? j.n : 1, mine = a.share_joins ? (int)blockIdx.x - j.first_cta : 0;
+            const int e0 = (int)((uint32_t)(all * mine) / (uint32_t)sharers), e1 = (int)((uint32_t)(all * (mine + 1)) / (uint32_t)sharers);
             int lg = 0;                                            // log2 of the threads of an element
             while (lg < 3 && (2 << lg) <= j.n && (e1 - e0) << (lg + 1) <= kT) ++lg;
             const int step = 1 << lg;

@@ -172,9 +172,20 @@ spec_status launch_attention(const Device &d, const attn::Args &a, bool f16)
     static_assert(S::kPartFloats <= kPartFloats, "");
     const dim3 grid((unsigned)attention_grid(d));
     const size_t smem = (size_t)d.attn_smem[shape_index<D, QT>()][f16];
-    // cooperative: CTAs wait for the parts of items that they share
-    return f16 ? launch<true>(attn::attention_kernel<D, QT, true>, grid, S::kThreads, smem, a)
-               : launch<true>(attn::attention_kernel<D, QT, false>, grid, S::kThreads, smem, a);
+    // What the parts of one item can come to at most: as many as its tiles (the
+    // table's width) make runs of kLeast, of the rows that the tokens fill.  A CTA
+    // joins 128 KB alone in about the 2 us that a cooperative launch costs a
+    // stream (8.7 against 10.6 us a call of one tile), and more than that slower
+    // than the CTAs that share it do.
+    attn::Args b = a;
+    const int64_t tiles = (a.max_pages << a.log_page) / S::BK + 2, runs = tiles / S::kLeast + 2;
+    const int64_t rows = a.tokens * a.group < S::kRows ? a.tokens * a.group : S::kRows;
+    b.share_joins = (runs < (int64_t)grid.x ? runs : (int64_t)grid.x) * rows * D * 4 > (128 << 10);
+    if (b.share_joins)   // CTAs wait for one another's parts
+        return f16 ? launch<true>(attn::attention_kernel<D, QT, true>, grid, S::kThreads, smem, b)
+                   : launch<true>(attn::attention_kernel<D, QT, false>, grid, S::kThreads, smem, b);
+    return f16 ? launch(attn::attention_kernel<D, QT, true>, grid, S::kThreads, smem, b)
+               : launch(attn::attention_kernel<D, QT, false>, grid, S::kThreads, smem, b);
 }
 
 // The cache as TMA sees it: [page][head][block of 64][token][64], boxes of one
