@@ -348,9 +348,10 @@ __device__ __forceinline__ Lane lane_of(const Args &a, int l)
     r.first = c0 < 0 ? 0 : c0 > t ? t : c0;
     const int32_t end = c1 < r.first ? r.first : c1 > t ? t : c1;
     r.n = end - r.first;
-    // a lane cut by the buffer keeps its tokens' positions
-    const int32_t seq = __ldg(a.seq_lens + l);
-    r.seq = (seq < 0 ? 0 : seq) - (c1 > end && r.n > 0 ? c1 - end : 0);
+    // a lane cut by the buffer keeps its tokens' positions; a length that is no
+    // length (near 2^31) must not overflow the tiles' arithmetic
+    const int32_t seq = __ldg(a.seq_lens + l), most = 0x7FFF0000;
+    r.seq = (seq < 0 ? 0 : seq > most ? most : seq) - (c1 > end && r.n > 0 ? c1 - end : 0);
     return r;
 }
 
@@ -1085,7 +1086,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 const int p0 = tid & (step - 1);
                 int r[kTwo], c4[kTwo];
                 bool on[kTwo];
-                float M[kTwo], L[kTwo], o[kTwo][4];
+                float M[kTwo] = {-INFINITY, -INFINITY}, L[kTwo] = {0.f, 0.f}, o[kTwo][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
                 auto add = [&](int u, float mp, float lp, float x, float y, float z, float w) {
                     const float Mn = fmaxf(M[u], mp), ref = Mn == -INFINITY ? 0.f : Mn, fo = exp2_fast(M[u] - ref), fp = exp2_fast(mp - ref);
                     M[u] = Mn;
@@ -1101,8 +1102,6 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     on[u] = e < e1;
                     c4[u] = on[u] ? e / j.rows : 0;
                     r[u] = on[u] ? e - c4[u] * j.rows : 0;         // over the item's row tiles
-                    M[u] = -INFINITY;
-                    L[u] = o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
                 }
 #pragma unroll 2
                 for (int p = p0; p < j.n; p += step) {

@@ -410,3 +410,130 @@ def test_plan_store_attend(sd):
         b.held.copy_(b.held_out)
         cursor.copy_(b.info[1:2])
     assert b.info.cpu().tolist()[2:] == [0, 0]
+
+
+# ---- further shapes, refusals with tensors, and an example -----------------------
+
+def test_large_group_and_cut_queries(sd):
+    """A group of more heads than a tile has rows; a query buffer shorter than
+    the step, whose tokens keep their positions."""
+    c = _case([2, 1], [30, 300], 1, 150, 64, 16, "bf16")
+    out, lse = _attend(sd, c)
+    _check(c, out, lse)
+    c = _case([5, 8, 3], [30, 300, 10], 2, 2, 128, 16, "bf16")
+    out, lse = _attend(sd, c, q=c["q"][:9].contiguous())
+    whole_out, whole_lse = _attend(sd, c)
+    f = lambda x: x.double().cpu().numpy()  # noqa: E731
+    o, ls, ob, lb = ref.attention(f(c["q"]), f(c["k"]), f(c["v"]), c["table"], c["cu"], c["seq"], 128 ** -0.5, 0, "bf16")
+    assert (np.abs(f(out) - o[:9]) <= ob[:9]).all() and (np.abs(f(lse) - ls[:9]) <= lb[:9]).all()
+
+
+def test_lengths_that_are_none(sd):
+    """Negative chunk boundaries and lengths past the table end the call all
+    the same; other lanes are answered."""
+    import torch
+    c = _case([2, 3, 1], [30, 20, 40], 1, 2, 64, 16, "bf16")
+    cache = sd.PagedCache(c["k"], c["v"])
+    out, lse = torch.zeros_like(c["q"]), torch.zeros(c["q"].shape[:2], device="cuda")
+    ws = sd.new_attention_workspace()
+    b = sd.PagedBatch(_i32(c["table"].tolist()), _i32([0, 2, 1, 6]), _i32(c["seq"]), page_size=16)
+    sd.spec_paged_attention(c["q"], cache, b, 0.125, out, lse, ws)
+    seq = [c["seq"][0], 200, c["seq"][2]]      # past the lane's pages and the table: zero keys there
+    b = sd.PagedBatch(_i32(c["table"].tolist()), _i32(c["cu"]), _i32(seq), page_size=16)
+    sd.spec_paged_attention(c["q"], cache, b, 0.125, out, lse, ws)
+    torch.cuda.synchronize()
+    sd.spec_device_status()
+    good, glse = _attend(sd, c)
+    # (lane 1 attends what its last page holds past its keys: no promise is made for it)
+    assert torch.equal(out[:2], good[:2]) and torch.equal(out[5:6], good[5:6])
+
+
+def test_two_streams_at_once(sd):
+    """Calls that overlap, each with a workspace of its own."""
+    import torch
+    cases = [_case([3, 1], [9_000, 12_000], 2, 2, 128, 64, "bf16", seed=s) for s in (1, 2)]
+    want = [_attend(sd, c) for c in cases]
+    streams, got = [torch.cuda.Stream() for _ in cases], []
+    for s, c in zip(streams, cases):
+        s.wait_stream(torch.cuda.current_stream())
+        cache = sd.PagedCache(c["k"], c["v"])
+        b = sd.PagedBatch(_i32(c["table"].tolist()), _i32(c["cu"]), _i32(c["seq"]), page_size=64)
+        got.append((cache, b, torch.full_like(c["q"], 7.5), torch.full(c["q"].shape[:2], 7.5, device="cuda"), sd.new_attention_workspace()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, c, (cache, b, out, lse, ws) in zip(streams, cases, got):
+            with torch.cuda.stream(s):
+                sd.spec_paged_attention(c["q"], cache, b, 128 ** -0.5, out, lse, ws)
+    torch.cuda.synchronize()
+    sd.spec_device_status()
+    for (wo, wl), (_, _, out, lse, _) in zip(want, got):
+        assert torch.equal(out, wo) and torch.equal(lse, wl)
+
+
+def test_binding_refuses(sd):
+    import torch
+    c = _case([2], [20], 2, 2, 64, 16, "bf16")
+    cache = sd.PagedCache(c["k"], c["v"])
+    b = sd.PagedBatch(_i32(c["table"].tolist()), _i32(c["cu"]), _i32(c["seq"]), page_size=16)
+    q, ws = c["q"], sd.new_attention_workspace()
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+
+    def refused(text, f, *a, **k):
+        with pytest.raises(sd.SpecError) as ei:
+            f(*a, **k)
+        assert ei.value.status == sd.SPEC_ERR_ARG and text in str(ei.value), str(ei.value)
+    at = sd.spec_paged_attention
+    refused("dtype", at, q.half(), cache, b, 0.1, out, lse, ws)
+    refused("shape", at, q[:, :, :32], cache, b, 0.1, out, lse, ws)
+    refused("contiguous", at, q.transpose(1, 2).contiguous().transpose(1, 2), cache, b, 0.1, out, lse, ws)
+    refused("out", at, q, cache, b, 0.1, out[:1], lse, ws)
+    refused("lse", at, q, cache, b, 0.1, out, lse.half(), ws)
+    refused("workspace", at, q, cache, b, 0.1, out, lse, ws[:100])
+    refused("heads_q", at, q[:, :3], cache, b, 0.1, torch.empty_like(q[:, :3]).contiguous(), lse, ws)
+    refused("k:", sd.spec_paged_store, q[:, :1], q[:, :2], torch.zeros(9, dtype=torch.int64, device="cuda"), cache)
+    refused("slots", sd.spec_paged_store, q[:, :2], q[:, 2:], torch.zeros(q.shape[0], dtype=torch.int32, device="cuda"), cache)
+    refused("plan's buffers", sd.spec_paged_plan, b, _i32([1]))
+    refused("last dimension", sd.PagedCache, c["k"].transpose(2, 3), c["v"].transpose(2, 3))
+    refused("one shape", sd.PagedCache, c["k"], c["v"][:1])
+    refused("go together", sd.PagedBatch, _i32(c["table"].tolist()), _i32(c["cu"]), _i32(c["seq"]), page_size=16, held=_i32([1]))
+    x = torch.zeros((2, 50), dtype=torch.bfloat16, device="cuda")
+    refused("dtype", sd.process_logits, x.float(), 2, 1)
+    refused("penalties", sd.process_logits, x, 2, 1, penalties=torch.zeros((1, 3), device="cuda"))
+    refused("mask", sd.process_logits, x, 2, 1, mask=_i32([[1]]), mask_rows=_i32([0, 0]))
+    refused("go together", sd.process_logits, x, 2, 1, history=_i32([[1], [2]]))
+
+
+def test_example_round(sd):
+    """The example loop: every committed token is the argmax of its processed
+    column, allowed by the grammar and said once; the cache holds the keys and
+    values of exactly the tokens committed before the last anchor."""
+    import importlib.util
+    import os
+    import torch
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "paged_round.py")
+    spec = importlib.util.spec_from_file_location("paged_round", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    r = m.generate(lanes=3, rounds=6, seed=4)
+    torch.cuda.synchronize()
+    sd.spec_device_status()
+    toy, cache, batch = r["toy"], r["cache"], r["batch"]
+    assert r["accepted"].shape == (6, 3) and int(r["accepted"].min()) >= 0 and int(r["accepted"].max()) <= 7
+    assert int(r["accepted"].sum()) > 0, "the drafter is meant to be right sometimes"
+    assert batch.info.cpu().tolist()[2:] == [0, 0]
+    top = r["last_target"].float().argmax(1).view(3, 8)
+    for lane in range(3):
+        p, s = int(r["prompt"][lane]), int(r["said"][lane])
+        said = r["history"][lane, p:s].long()
+        assert s - p == int(r["accepted"][:, lane].sum()) + 6
+        assert bool(toy.allowed[said].all()) and len(set(said.tolist())) == s - p
+        a = int(r["accepted"][-1, lane])
+        best = r["last_target"][lane * 8:lane * 8 + 8].float()
+        committed = r["last_commits"][lane, :a + 1].long()
+        assert torch.equal(best[torch.arange(a + 1), committed], best[torch.arange(a + 1), top[lane, :a + 1]])
+        n = int(batch.context_lens[lane])
+        assert n == s - 1                      # the last commit is the next anchor
+        j = torch.arange(n, device="cuda")
+        page = batch.block_table[lane].long()[j // cache.page_size]
+        ids = r["history"][lane, :n].long()
+        assert torch.equal(cache.k[page, j % cache.page_size], toy.k[ids]) and torch.equal(cache.v[page, j % cache.page_size], toy.v[ids])
