@@ -841,6 +841,11 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             const int64_t klo64 = a.window > 0 ? (int64_t)pos - a.window + 1 : 0;
             const int klo = klo64 > 0 ? (int)klo64 : 0, khi = valid ? pos + 1 : klo;   // keys of this row
             const bool live = __any_sync(kFull, khi > klo);
+            // the quads of rows in use, and this thread's place among those who clear V rows
+            const int64_t rows_left = (int64_t)it.n * a.group - (int64_t)it.rt * S::kRows - (QT == 2 ? st * 128 : 0);
+            const int quads = rows_left >= 97 ? 4 : rows_left <= 0 ? 0 : (int)(rows_left + 31) >> 5, idle = quads < 4 ? quads : 0;
+            const bool clears = quad >= idle;
+            const int clear_id = ((quad - idle) * 2 + half) * 32 + lane, clear_of = (4 - idle) * 64;
 
             float m = -INFINITY, l = 0.f;                          // l: of this half's columns
             const int U = QT == 2 || S::NS == 1 ? tiles : (tiles - st + 1) >> 1;
@@ -924,19 +929,17 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     l += s0 + s1;
                 }
                 // V rows that no row of the item may see hold anything, NaN
-                // included: 0 * NaN must not reach O
-                if (key0 < lo || key0 + S::BK > hi) {
+                // included: 0 * NaN must not reach O.  Warps without rows clear
+                // them while the others compute, or all do.
+                if ((key0 < lo || key0 + S::BK > hi) && clears) {
                     const uint32_t idx = 2 * (tile_n + t) + 1, vs = idx % S::kStages;
                     wait(&bar.full[vs], (idx / S::kStages) & 1);
                     uint8_t *v = kv_smem + vs * S::kStageBytes;
-                    constexpr int kPer = 256 / S::BK;               // threads of a key row
-                    const int kr = (half * 128 + row) / kPer, part = row % kPer;
-                    if (key0 + kr < lo || key0 + kr >= hi) {
-#pragma unroll
-                        for (int blk = 0; blk < S::NB; ++blk)
-#pragma unroll
-                            for (int p = part; p < 8; p += kPer)
-                                *reinterpret_cast<uint4 *>(v + blk * (S::BK * 128) + kr * 128 + p * 16) = make_uint4(0, 0, 0, 0);
+                    const int below = lo > key0 ? min(lo - key0, S::BK) : 0, above = hi < key0 + S::BK ? max(hi - key0, below) : S::BK;
+                    const int gone = below + S::BK - above;         // rows [0, below) and [above, BK)
+                    for (int k = clear_id; k < gone * (D / 8); k += clear_of) {
+                        const int g = k / (D / 8), p = k % (D / 8), kr = g < below ? g : g - below + above;
+                        *reinterpret_cast<uint4 *>(v + (p >> 3) * (S::BK * 128) + kr * 128 + (p & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async();
                 }
@@ -959,8 +962,9 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             float f0 = 1.f, f1 = 0.f;                              // weights of the streams' O
             int c0 = half * (D / 2);
             constexpr bool kStreams = QT == 1 && S::NS == 2;
-            constexpr int kCols = kStreams ? D / 4 : D / 2;
-            if (kStreams) {
+            const bool streams = kStreams && tiles > 1;            // (an item of one tile has the first stream's only)
+            const int cols = streams ? D / 4 : kStreams && st == 1 ? 0 : D / 2;
+            if (streams) {
                 swap[st * 256 + half * 128 + row] = l;
                 fence_before();
                 named_barrier(kAllSoftmax, S::kSoftmaxWarps * 32);
@@ -974,7 +978,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 f0 = m0 == -INFINITY ? 0.f : exp2_fast(m0 - m);
                 f1 = m1 == -INFINITY ? 0.f : exp2_fast(m1 - m);
                 l = l0 * f0 + l1 * f1;
-                c0 = (st * 2 + half) * kCols;
+                c0 = (st * 2 + half) * (D / 4);
             } else if (live) {
                 float *mx = swap + st * 256 + row;
                 mx[half * 128] = l;
@@ -992,10 +996,10 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             if (live) {
                 const uint32_t oa = tmem + lane_base + S::kO + (QT == 2 ? st * D : 0);
 #pragma unroll 1
-                for (int c = c0; c < c0 + kCols; c += 16) {
+                for (int c = c0; c < c0 + cols; c += 16) {
                     uint32_t o[16];
                     tmem_ld16(o, oa + c);
-                    if (kStreams && tiles > 1) {
+                    if (streams) {
                         uint32_t o1[16];
                         tmem_ld16(o1, oa + D + c);
 #pragma unroll
@@ -1029,9 +1033,9 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     }
                 }
             } else if (valid && !split) {                          // a warp of rows without keys
-                for (int c = c0; c < c0 + kCols; c += 8) *reinterpret_cast<uint4 *>(a.out + out_row * D + c) = make_uint4(0, 0, 0, 0);
+                for (int c = c0; c < c0 + cols; c += 8) *reinterpret_cast<uint4 *>(a.out + out_row * D + c) = make_uint4(0, 0, 0, 0);
             }
-            if (valid && c0 == 0) {
+            if (valid && c0 == 0 && cols > 0) {
                 if (split) {
                     float *ml = part + 128 * D;
                     ml[row] = live ? m : -INFINITY;
@@ -1072,76 +1076,91 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             }
         }
         if (joins[0].n + joins[1].n > 0) named_barrier(kAllSoftmax, kT);
+        // this CTA's elements of both items, one after the other
+        int from[2], count[2];
+#pragma unroll
         for (int sl = 0; sl < 2; ++sl) {
-            const Join j = joins[sl];
+            const Join &j = joins[sl];
+            from[sl] = count[sl] = 0;
             if (j.n == 0 || !(a.share_joins || came_last[sl])) continue;
             const int all = j.rows * (D / 4), sharers = a.share_joins ? j.n : 1, mine = a.share_joins ? (int)blockIdx.x - j.first_cta : 0;
-            const int e0 = (int)((uint32_t)(all * mine) / (uint32_t)sharers), e1 = (int)((uint32_t)(all * (mine + 1)) / (uint32_t)sharers);
-            int lg = 0;                                            // log2 of the threads of an element
-            while (lg < 3 && (2 << lg) <= j.n && (e1 - e0) << (lg + 1) <= kT) ++lg;
-            const int step = 1 << lg;
-            const float *first_part = a.parts + ((int64_t)j.first_cta * 2 + 1) * S::kPartFloats;   // the others: one slot on, then every second
-            constexpr int kTwo = 2;                                // elements of a thread in flight
-            for (int base = e0; base < e1; base += kTwo * (kT >> lg)) {
-                const int p0 = tid & (step - 1);
-                int r[kTwo], c4[kTwo];
-                bool on[kTwo];
-                float M[kTwo] = {-INFINITY, -INFINITY}, L[kTwo] = {0.f, 0.f}, o[kTwo][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                auto add = [&](int u, float mp, float lp, float x, float y, float z, float w) {
-                    const float Mn = fmaxf(M[u], mp), ref = Mn == -INFINITY ? 0.f : Mn, fo = exp2_fast(M[u] - ref), fp = exp2_fast(mp - ref);
-                    M[u] = Mn;
-                    L[u] = L[u] * fo + lp * fp;
-                    o[u][0] = o[u][0] * fo + x * fp;
-                    o[u][1] = o[u][1] * fo + y * fp;
-                    o[u][2] = o[u][2] * fo + z * fp;
-                    o[u][3] = o[u][3] * fo + w * fp;
-                };
+            from[sl] = (int)((uint32_t)(all * mine) / (uint32_t)sharers);
+            count[sl] = (int)((uint32_t)(all * (mine + 1)) / (uint32_t)sharers) - from[sl];
+        }
+        const int work = count[0] + count[1], most = max(joins[0].n, joins[1].n);
+        int lg = 0;                                                // log2 of the threads of an element
+        while (lg < 3 && (2 << lg) <= most && work << (lg + 1) <= kT) ++lg;
+        const int step = 1 << lg;
+        constexpr int kTwo = 2;                                    // elements of a thread in flight
+        for (int base = 0; base < work; base += kTwo * (kT >> lg)) {
+            const int p0 = tid & (step - 1);
+            int sl[kTwo], r[kTwo], c4[kTwo], n[kTwo];
+            float M[kTwo] = {-INFINITY, -INFINITY}, L[kTwo] = {0.f, 0.f}, o[kTwo][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            const float *first_part[kTwo];                         // the others: one slot on, then every second
+            auto add = [&](int u, float mp, float lp, float x, float y, float z, float w) {
+                const float Mn = fmaxf(M[u], mp), ref = Mn == -INFINITY ? 0.f : Mn, fo = exp2_fast(M[u] - ref), fp = exp2_fast(mp - ref);
+                M[u] = Mn;
+                L[u] = L[u] * fo + lp * fp;
+                o[u][0] = o[u][0] * fo + x * fp;
+                o[u][1] = o[u][1] * fo + y * fp;
+                o[u][2] = o[u][2] * fo + z * fp;
+                o[u][3] = o[u][3] * fo + w * fp;
+            };
+            int longest = 0;
 #pragma unroll
-                for (int u = 0; u < kTwo; ++u) {
-                    const int e = base + u * (kT >> lg) + (tid >> lg);
-                    on[u] = e < e1;
-                    c4[u] = on[u] ? e / j.rows : 0;
-                    r[u] = on[u] ? e - c4[u] * j.rows : 0;         // over the item's row tiles
-                }
+            for (int u = 0; u < kTwo; ++u) {
+                const int k = base + u * (kT >> lg) + (tid >> lg);
+                sl[u] = k < count[0] ? 0 : 1;
+                const Join &j = joins[sl[u]];
+                const int e = k < count[0] ? from[0] + k : from[1] + k - count[0];
+                n[u] = k < work ? j.n : 0;
+                c4[u] = k < work ? (int)((uint32_t)e / (uint32_t)j.rows) : 0;
+                r[u] = k < work ? e - c4[u] * j.rows : 0;          // over the item's row tiles
+                first_part[u] = a.parts + ((int64_t)j.first_cta * 2 + 1) * S::kPartFloats + (r[u] >> 7) * 128 * (D + 2);
+                longest = max(longest, n[u]);
+            }
 #pragma unroll 2
-                for (int p = p0; p < j.n; p += step) {
-                    const float *part = p == 0 ? first_part : first_part + (int64_t)(2 * p - 1) * S::kPartFloats;
-                    float mp[kTwo], lp[kTwo];
-                    float4 x[kTwo];
-#pragma unroll
-                    for (int u = 0; u < kTwo; ++u) {
-                        const float *q = part + (r[u] >> 7) * 128 * (D + 2);
-                        mp[u] = __ldcg(q + 128 * D + (r[u] & 127));
-                        lp[u] = __ldcg(q + 128 * D + 128 + (r[u] & 127));
-                        x[u] = __ldcg(reinterpret_cast<const float4 *>(q) + c4[u] * 128 + (r[u] & 127));
-                    }
-#pragma unroll
-                    for (int u = 0; u < kTwo; ++u) add(u, mp[u], lp[u], x[u].x, x[u].y, x[u].z, x[u].w);
-                }
-                if (lg > 0) {
-#pragma unroll
-                    for (int u = 0; u < kTwo; ++u) {
-                        float *mine6 = red + tid * 6;
-                        mine6[0] = M[u]; mine6[1] = L[u]; mine6[2] = o[u][0]; mine6[3] = o[u][1]; mine6[4] = o[u][2]; mine6[5] = o[u][3];
-                        __syncwarp();                              // an element's threads are in one warp
-                        if (p0 == 0)
-                            for (int k = 1; k < step; ++k) {
-                                const float *q = mine6 + k * 6;
-                                add(u, q[0], q[1], q[2], q[3], q[4], q[5]);
-                            }
-                        __syncwarp();
-                    }
-                }
+            for (int p = p0; p < longest; p += step) {
+                float mp[kTwo], lp[kTwo];
+                float4 x[kTwo];
 #pragma unroll
                 for (int u = 0; u < kTwo; ++u) {
-                    if (!on[u] || p0 != 0) continue;
-                    const uint32_t g = (uint32_t)j.rt * S::kRows + r[u], tok = div_group(a, g);
-                    const int64_t orow = ((int64_t)j.first + tok) * a.heads_q + (int64_t)j.head * a.group + (g - tok * a.group);
-                    const float iv = L[u] > 0.f ? 1.f / L[u] : 0.f;
-                    *reinterpret_cast<uint2 *>(a.out + orow * D + c4[u] * 4) =
-                        make_uint2(pack2<F16>(o[u][0] * iv, o[u][1] * iv), pack2<F16>(o[u][2] * iv, o[u][3] * iv));
-                    if (c4[u] == 0 && a.lse) a.lse[orow] = L[u] > 0.f ? (M[u] + log2f(L[u])) * kLn2 : -INFINITY;
+                    const float *q = p == 0 ? first_part[u] : first_part[u] + (int64_t)(2 * p - 1) * S::kPartFloats;
+                    mp[u] = -INFINITY;
+                    lp[u] = 0.f;
+                    x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (p >= n[u]) continue;
+                    mp[u] = __ldcg(q + 128 * D + (r[u] & 127));
+                    lp[u] = __ldcg(q + 128 * D + 128 + (r[u] & 127));
+                    x[u] = __ldcg(reinterpret_cast<const float4 *>(q) + c4[u] * 128 + (r[u] & 127));
                 }
+#pragma unroll
+                for (int u = 0; u < kTwo; ++u) add(u, mp[u], lp[u], x[u].x, x[u].y, x[u].z, x[u].w);
+            }
+            if (lg > 0) {
+#pragma unroll
+                for (int u = 0; u < kTwo; ++u) {
+                    float *mine6 = red + tid * 6;
+                    mine6[0] = M[u]; mine6[1] = L[u]; mine6[2] = o[u][0]; mine6[3] = o[u][1]; mine6[4] = o[u][2]; mine6[5] = o[u][3];
+                    __syncwarp();                                  // an element's threads are in one warp
+                    if (p0 == 0)
+                        for (int k = 1; k < step; ++k) {
+                            const float *q = mine6 + k * 6;
+                            add(u, q[0], q[1], q[2], q[3], q[4], q[5]);
+                        }
+                    __syncwarp();
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kTwo; ++u) {
+                if (n[u] == 0 || p0 != 0) continue;
+                const Join &j = joins[sl[u]];
+                const uint32_t g = (uint32_t)j.rt * S::kRows + r[u], tok = div_group(a, g);
+                const int64_t orow = ((int64_t)j.first + tok) * a.heads_q + (int64_t)j.head * a.group + (g - tok * a.group);
+                const float iv = L[u] > 0.f ? 1.f / L[u] : 0.f;
+                *reinterpret_cast<uint2 *>(a.out + orow * D + c4[u] * 4) =
+                    make_uint2(pack2<F16>(o[u][0] * iv, o[u][1] * iv), pack2<F16>(o[u][2] * iv, o[u][3] * iv));
+                if (c4[u] == 0 && a.lse) a.lse[orow] = L[u] > 0.f ? (M[u] + log2f(L[u])) * kLn2 : -INFINITY;
             }
         }
     }
