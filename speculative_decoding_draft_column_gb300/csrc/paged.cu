@@ -79,7 +79,7 @@ spec_status device(Device **out)
         e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
         e = cudaFuncSetAttribute(paged::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 2 * (SPEC_PAGED_MAX_LANES + 1) * 8);
+                                 (int)paged::plan_smem(SPEC_PAGED_MAX_LANES));
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
         e = cudaFuncSetAttribute(rules::process_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, rules::smem_bytes(true));
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
@@ -252,7 +252,7 @@ spec_status spec_paged_plan(const spec_paged_batch *batch, const int32_t *free_p
     if (grid < by_lanes) grid = by_lanes;
     if (grid < 1) grid = 1;
     if (grid > d->sms) grid = d->sms;
-    return launch(paged::plan_kernel, dim3((unsigned)grid), paged::kPlanThreads, 2 * (size_t)(b.lanes + 1) * 8, a);
+    return launch(paged::plan_kernel, dim3((unsigned)grid), paged::kPlanThreads, paged::plan_smem(b.lanes), a);
 }
 
 spec_status spec_paged_store(const void *k, const void *v, int64_t tokens, int64_t k_token_stride,

@@ -10,6 +10,8 @@ namespace paged {
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
+inline size_t plan_smem(int64_t lanes) { return (size_t)(2 * (lanes + 1) * 8 + 3 * lanes * 4); }
+
 struct PlanArgs {
     spec_paged_batch b;
     const int32_t *free_pages;
@@ -49,17 +51,21 @@ __device__ __forceinline__ int64_t warp_inclusive_sum64(int64_t v, int lane)
 // Every CTA scans all lanes' lengths (a few KB, from L2) into shared memory and
 // then writes its share of the lanes' and the tokens' outputs: one launch, no
 // exchange between CTAs.  The step is bound by that chain of dependent reads
-// (lengths, scan, table), not by its bytes.
+// (lengths, scan, table), not by its bytes; 1,024 lanes with 262,144 new tokens
+// write 3.4 MB.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs a)
 {
     pdl_launch_dependents();
     pdl_wait();
-    extern __shared__ int64_t sums[];   // [lanes + 1] new tokens, then [lanes + 1] wanted pages, before each lane
+    // [lanes + 1] new tokens, then [lanes + 1] wanted pages, before each lane;
+    // [lanes] each: cached tokens, pages held before, pages held after
+    extern __shared__ int64_t sums[];
     __shared__ int64_t warp_n[kPlanWarps], warp_w[kPlanWarps];
     __shared__ int over_lanes;
     const spec_paged_batch &b = a.b;
     const int lanes = (int)b.lanes, tid = threadIdx.x, wl = tid & 31, wid = tid >> 5;
     int64_t *cu = sums, *cw = sums + lanes + 1;
+    int32_t *ctx = reinterpret_cast<int32_t *>(cw + lanes + 1), *had = ctx + lanes, *has = had + lanes;
     if (tid == 0) over_lanes = 0;
     __syncthreads();
 
@@ -71,6 +77,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         const LaneNeed r = lane_need(b, l);
         cu[l] = sn;
         cw[l] = sw;
+        ctx[l] = (int32_t)r.ctx;
+        had[l] = (int32_t)r.held;
+        has[l] = (int32_t)r.want;       // until the free pages are shared out
         sn += r.n;
         sw += r.want;
         over += r.need > b.max_pages;
@@ -94,18 +103,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     int64_t cursor = a.cursor ? __ldg(a.cursor) : 0;
     cursor = cursor < 0 ? 0 : cursor > a.num_free ? a.num_free : cursor;
     const int64_t avail = a.num_free - cursor;
+    for (int l = tid; l < lanes; l += kPlanThreads) {
+        const int64_t left = avail - cw[l], want = has[l];
+        has[l] = had[l] + (int32_t)(left < 0 ? 0 : left < want ? left : want);
+    }
+    __syncthreads();
 
     // lanes: one warp each, in turn
     for (int l = blockIdx.x * kPlanWarps + wid; l < lanes; l += gridDim.x * kPlanWarps) {
-        const LaneNeed r = lane_need(b, l);
-        const int64_t left = avail - cw[l], got = left < 0 ? 0 : left < r.want ? left : r.want;
-        int32_t *row = b.block_table + (int64_t)l * b.max_pages + r.held;
+        const int held = had[l], got = has[l] - held;
+        int32_t *row = b.block_table + (int64_t)l * b.max_pages + held;
         const int32_t *src = a.free_pages + cursor + cw[l];
-        for (int64_t i = wl; i < got; i += 32) row[i] = __ldg(src + i);
+        for (int i = wl; i < got; i += 32) row[i] = __ldg(src + i);
         if (wl == 0) {
             b.cu_new[l] = (int32_t)cu[l];
-            b.seq_lens[l] = (int32_t)(r.ctx + r.n);
-            b.held_out[l] = (int32_t)(r.held + got);
+            b.seq_lens[l] = (int32_t)(ctx[l] + (cu[l + 1] - cu[l]));
+            b.held_out[l] = held + got;
         }
     }
     if (blockIdx.x == 0 && tid == 0) {
@@ -117,29 +130,36 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
 
     // tokens: the lane by bisection, the page from the table or, if the step
-    // adds it, from the free list (another CTA may be writing the table entry)
-    for (int64_t t = (int64_t)blockIdx.x * kPlanThreads + tid; t < b.tokens; t += (int64_t)gridDim.x * kPlanThreads) {
-        int32_t pos = 0;
-        int64_t slot = -1;
-        if (t < total) {
+    // adds it, from the free list (another CTA may be writing the table entry);
+    // kAhead tokens of a thread on their way together
+    constexpr int kAhead = 4;
+    const int64_t stride = (int64_t)gridDim.x * kPlanThreads;
+    for (int64_t t0 = (int64_t)blockIdx.x * kPlanThreads + tid; t0 < b.tokens; t0 += kAhead * stride) {
+        int32_t pos[kAhead], in[kAhead], id[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t t = t0 + u * stride;
+            pos[u] = in[u] = 0;
+            id[u] = -1;
+            if (t >= total || t >= b.tokens) continue;
             int lo = 0, hi = lanes - 1;   // the last lane with cu <= t
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
                 if (cu[mid] <= t) lo = mid; else hi = mid - 1;
             }
-            const LaneNeed r = lane_need(b, lo);
-            const int64_t p = r.ctx + (t - cu[lo]), page = udiv(p, b.page_size);
-            pos = (int32_t)p;
-            const int64_t left = avail - cw[lo], got = left < 0 ? 0 : left < r.want ? left : r.want;
-            if (page < r.held + got) {
-                const int32_t id = page < r.held ? b.block_table[(int64_t)lo * b.max_pages + page]
-                                                 : __ldg(a.free_pages + cursor + cw[lo] + (page - r.held));
-                slot = (int64_t)id * b.page_size + (p - page * b.page_size);
-                if (id < 0) slot = -1;
-            }
+            const int64_t p = ctx[lo] + (t - cu[lo]), page = udiv(p, b.page_size);
+            pos[u] = (int32_t)p;
+            in[u] = (int32_t)(p - page * b.page_size);
+            if (page < had[lo]) id[u] = b.block_table[(int64_t)lo * b.max_pages + page];
+            else if (page < has[lo]) id[u] = __ldg(a.free_pages + cursor + cw[lo] + (page - had[lo]));
         }
-        b.positions[t] = pos;
-        b.slots[t] = slot;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t t = t0 + u * stride;
+            if (t >= b.tokens) continue;
+            b.positions[t] = pos[u];
+            b.slots[t] = id[u] < 0 ? -1 : (int64_t)id[u] * b.page_size + in[u];
+        }
     }
 }
 
