@@ -42,6 +42,7 @@ FALLBACK_HBM_GBS = 6800.0
 NOMINAL_HBM_GBS = 8000.0      # GB300 HBM3e, the peak the targets are stated against
 KERNEL_DIR = os.path.join(ROOT, "speculative_decoding_draft_column_gb300", "csrc")
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
+OTHER_SOURCES = ("paged.cu", "paged.cuh", "attention.cuh", "logits_rules.cuh")
 
 WORKLOADS = {
     "C1": "1 lane x 7 drafts: 7 draft columns x V=248,046 bf16 ~N(0,3) + 3 planted peaks, k=8; "
@@ -99,10 +100,11 @@ def hbm_peak():
 
 
 def source_hash() -> str:
-    """sha256 (first 16 hex digits) over the kernel sources, in name order."""
+    """sha256 (first 16 hex digits) over the round's kernel sources, in name
+    order (not those of the paged cache and the logits rules, which no round runs)."""
     h = hashlib.sha256()
     for name in sorted(os.listdir(KERNEL_DIR)):
-        if name.endswith((".cu", ".cuh")):
+        if name.endswith((".cu", ".cuh")) and name not in OTHER_SOURCES:
             with open(os.path.join(KERNEL_DIR, name), "rb") as f:
                 h.update(name.encode() + b"\0" + f.read())
     return h.hexdigest()[:16]
