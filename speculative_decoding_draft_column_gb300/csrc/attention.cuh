@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
     __shared__ int32_t came_last[2];   // this CTA's part was the item's last (where joins are not shared)
     __shared__ uint32_t tmem_slot;
     __shared__ Plan plan;
-    __shared__ int64_t warp_units[S::kThreads / 32];
+    __shared__ __align__(16) int64_t warp_units[S::kThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kLoader = S::kSoftmaxWarps, kMma = kLoader + 1, kQLoader = kLoader + 2;
 
@@ -545,15 +545,14 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         fence_before();
         __syncthreads();
         fence_after();
-        static_assert(kWarps <= 32, "");
-        int64_t upto = lane < kWarps ? warp_units[lane] : 0;
+        int64_t all = 0, below = 0;                              // of all warps, of those before this one
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(kFull, upto, d);
-            if (lane >= d) upto += y;
+        for (int w = 0; w < kWarps; ++w) {
+            const int64_t x = warp_units[w];
+            all += x;
+            below += w < warp ? x : 0;
         }
-        const int64_t all = __shfl_sync(kFull, upto, 31), total = all & kUnits;
-        const int64_t before = (__shfl_sync(kFull, upto, warp) - warp_units[warp] + incl - mine) & kUnits;
+        const int64_t total = all & kUnits, before = (below + incl - mine) & kUnits;
         mine &= kUnits;
         head &= kUnits;
         // As many runs as there are CTAs, but not so many that an item has to be
@@ -610,7 +609,8 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             run.head = (int)udiv(off, plan.per_head);
             run.item0 = plan.lane_u + run.head * plan.per_head;
             // the row tile: 32 at a time
-            for (run.rt = 0;; run.rt += 32) {
+            run.rt = 0;
+            for (; run.rts > 1; run.rt += 32) {
                 const int rt = run.rt + lane;
                 int all;
                 const int tiles = rt < run.rts ? reach_of<S>(a, run.ln.n, run.ln.seq, rt).tiles : 0;
