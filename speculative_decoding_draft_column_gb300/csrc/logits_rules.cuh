@@ -56,6 +56,9 @@ __device__ __forceinline__ uint16_t to_bf16(float f)
     return h;
 }
 
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
+
 // bytes of the sign bits that the selector's nibbles (8 + byte) name
 __device__ __forceinline__ uint32_t copies(uint32_t v, uint32_t selector)
 {
@@ -124,32 +127,44 @@ __global__ void __launch_bounds__(kThreads, 2) process_kernel(const __grid_const
     const int end = left > kSlice ? kSlice : (int)left, begin = t0 > 0 ? -8 : 0;   // tokens [begin, end) are the column's
     const int piece = warp % kPieces, col_step = kWarps / kPieces, first_col = warp / kPieces;
     struct Part {
-        int mis, lo, hi;   // elements [lo, hi) are the column's
+        int lo, hi;        // elements [lo, hi) are the column's
         int v0, v1;        // vectors wholly inside: by bulk copy (the rest token by token)
     };
-    auto part = [&](int j) -> Part {
+    auto part = [&](int mis) -> Part {
         Part p;
-        p.mis = (mis0 + j * v7) & 7;
-        p.lo = begin + p.mis - piece * kPiece;
-        p.hi = end + p.mis - piece * kPiece;
+        p.lo = begin + mis - piece * kPiece;
+        p.hi = end + mis - piece * kPiece;
         p.v0 = p.lo > 0 ? 1 : 0;                          // lo is at most 7
         const int n = p.hi >> 3;
         p.v1 = n > kPiece / 8 ? kPiece / 8 : n < p.v0 ? p.v0 : n;
         return p;
     };
+    // the slice lies inside its columns, in whatever phase: every piece is whole
+    const bool inner = t0 >= 8 && t0 + kSlice <= a.V;
     uint16_t *ring = reinterpret_cast<uint16_t *>(smem) + warp * kRing * kPiece;
-    auto offset = [&](int j, const Part &p) -> int64_t { return (col0 + j) * a.V + t0 - p.mis + piece * kPiece; };
-    auto fetch = [&](int k) {                              // the warp's k-th piece; one thread
-        const int j = first_col + k * col_step;
-        const Part p = part(j);
+    // one thread: the piece at element `at` of the logits (its phase taken off) into a place of the ring
+    auto fetch = [&](int place, int64_t at, int mis) {
+        uint64_t *bar = &full[warp][place];
+        uint16_t *to = ring + place * kPiece;
+        if (inner) {
+            mbar_arrive_expect_tx(bar, kPiece * 2);
+            bulk_g2s(to, a.logits + at, kPiece * 2, bar);
+            return;
+        }
+        const Part p = part(mis);
         const uint32_t bytes = (uint32_t)(p.v1 - p.v0) * 16;
-        uint64_t *bar = &full[warp][k % kRing];
         mbar_arrive_expect_tx(bar, bytes);
-        if (bytes) bulk_g2s(ring + (k % kRing) * kPiece + 8 * p.v0, a.logits + offset(j, p) + 8 * p.v0, bytes, bar);
+        if (bytes) bulk_g2s(to + 8 * p.v0, a.logits + at + 8 * p.v0, bytes, bar);
     };
+    // from one of the warp's columns to the next
+    const int64_t col_stride = (int64_t)col_step * a.V, at_first = (col0 + first_col) * a.V + t0 + piece * kPiece;
+    const int mis_first = (mis0 + first_col * v7) & 7, mis_stride = (col_step * v7) & 7;
     const int mine = a.cols > first_col ? (a.cols - first_col + col_step - 1) / col_step : 0;   // pieces of this warp
     if (wl == 0)
-        for (int k = 0; k < kRing && k < mine; ++k) fetch(k);
+        for (int k = 0; k < kRing && k < mine; ++k) {
+            const int mis = (mis_first + k * mis_stride) & 7;
+            fetch(k, at_first + k * col_stride - mis, mis);
+        }
 
     // Window entry of an id, or at least `limit`: one unsigned comparison keeps ids
     // outside the window and the vocabulary out (where the window starts below
@@ -260,98 +275,112 @@ __global__ void __launch_bounds__(kThreads, 2) process_kernel(const __grid_const
     __syncthreads();
     const int n = n_listed[piece];
 
-    // The mask words of a lane's vectors, a piece ahead of their use (a column's
-    // mask lies in memory of its own, read once).
-    auto mask_words = [&](int k, uint2 (&m)[kPer]) {
-        const int j = first_col + k * col_step, row = k < mine ? mask_row[j] : -1;
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) m[u] = make_uint2(~0u, ~0u);
-        if (row < 0) return;
-        const int rel = piece * kPiece + 8 * wl - ((mis0 + j * v7) & 7), w = rel >> 5;   // w: floor, also below 0
-        const uint32_t *q = mask0 + row * words + w;
-        const bool both = (rel & 31) > 24;                // a vector's bits lie in two words
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            if (rel + 256 * u >= end) break;
-            if (u > 0 || t0 > 0 || w >= 0) m[u].x = __ldg(q + 8 * u);
-            if (both && 32 * (w + 8 * u + 1) < end) m[u].y = __ldg(q + 8 * u + 1);
-        }
-    };
-    uint2 words_now[kPer], words_next[kPer];
-    mask_words(0, words_now);
-    for (int k = 0; k < mine; ++k) {
-        const int j = first_col + k * col_step, row = mask_row[j];
-        const Part pt = part(j);
-        const int64_t at0 = offset(j, pt);
-        uint16_t *x = ring + (k % kRing) * kPiece;
-        mask_words(k + 1, words_next);
-        mbar_wait(&full[warp][k % kRing], (k / kRing) & 1);
-        if (pt.v0 > 0 || pt.v1 < kPiece / 8) {             // the ends of the column
-            const int e = wl < 8 ? 8 * (pt.v0 - 1) + wl : 8 * pt.v1 + wl - 8;
-            if (wl < 16 && e >= 0 && e < kPiece && e >= pt.lo && e < pt.hi) x[e] = a.logits[at0 + e];
-            __syncwarp();
-        }
-        const int first = pt.lo > 0 ? pt.lo : 0, many = (pt.hi < kPiece ? pt.hi : kPiece) - first;
-#pragma unroll 1
-        for (int i = wl; i < n; i += 32) {
-            const int e = list[i], at = e - 8 + pt.mis - piece * kPiece;
-            if ((uint32_t)(at - first) >= (uint32_t)many || many <= 0) continue;
-            const uint32_t c = count[e];
-            uint32_t m = c & ~(kSeen | kDraft);
-            if (c & kDraft)                                // its count grows along the columns
-                for (int d = 1; d <= j; ++d) m += draft_entry[d] == e;
-            const float v = bf16_as_float(x[at]);
-            const float factor = (c & kSeen) || m ? (v > 0.f ? over_r : r) : 1.f;
-            const float take = __fadd_rn(__fmul_rn(f, (float)m), m ? p : 0.f);
-            const float z = __fsub_rn(__fmul_rn(v, factor), take);
-            x[at] = to_bf16(a.bias_ids ? __fadd_rn(z, bias[e]) : z);
-        }
-        if (row >= 0) {
-            __syncwarp();
+    auto stream = [&](auto inner_tag) {
+        constexpr bool kInner = decltype(inner_tag)::value;
+        // The mask words of a lane's vectors, a piece ahead of their use (a column's
+        // mask lies in memory of its own, read once).
+        auto mask_words = [&](int row, int mis, uint2 (&m)[kPer]) {
+            if (row < 0) return;
+            const int rel = piece * kPiece + 8 * wl - mis, w = rel >> 5;   // w: floor, also below 0
+            const uint32_t *q = mask0 + row * words + w;
+            const bool both = (rel & 31) > 24;            // a vector's bits lie in two words
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
-                const uint32_t allowed = __funnelshift_r(words_now[u].x, words_now[u].y, (uint32_t)(8 * wl - pt.mis) & 31u) & 0xFFu;
-                if (allowed == 0xFFu || 8 * (wl + 32 * u) >= pt.hi) continue;
-                uint4 *at = reinterpret_cast<uint4 *>(x) + wl + 32 * u;
-                uint4 q = make_uint4(kMasked, kMasked, kMasked, kMasked);
-                if (allowed != 0u) {
-                    q = *at;
-                    // bit k of four to the top of byte k, then 16 copies of each top bit: the words' masks
-                    const uint32_t l = (allowed & 15u) * 0x10204080u, h = (allowed >> 4) * 0x10204080u;
-                    auto keep = [](uint32_t w, uint32_t m) { return (w & m) | (kMasked & ~m); };
-                    q.x = keep(q.x, copies(l, 0x9988));
-                    q.y = keep(q.y, copies(l, 0xBBAA));
-                    q.z = keep(q.z, copies(h, 0x9988));
-                    q.w = keep(q.w, copies(h, 0xBBAA));
-                }
-                *at = q;
+                m[u] = make_uint2(0u, 0u);
+                if (!kInner && rel + 256 * u >= end) break;
+                if (kInner || u > 0 || t0 > 0 || w >= 0) m[u].x = __ldg(q + 8 * u);
+                if (both && (kInner || 32 * (w + 8 * u + 1) < end)) m[u].y = __ldg(q + 8 * u + 1);
             }
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (same_phase) {
-            if (pt.v0 > 0 || pt.v1 < kPiece / 8) {
+        };
+        uint2 words_now[kPer], words_next[kPer];
+        int mis = mis_first, row = mine > 0 ? mask_row[first_col] : -1;
+        int64_t at = at_first;
+        mask_words(row, mis, words_now);
+#pragma unroll 1
+        for (int k = 0, j = first_col; k < mine; ++k, j += col_step) {
+            const Part pt = kInner ? Part{0, kPiece, 0, kPiece / 8} : part(mis);
+            const int64_t at0 = at - mis;
+            const int place = k % kRing, mis_next = (mis + mis_stride) & 7, row_next = k + 1 < mine ? mask_row[j + col_step] : -1;
+            uint16_t *x = ring + place * kPiece;
+            mask_words(row_next, mis_next, words_next);
+            mbar_wait(&full[warp][place], (k / kRing) & 1);
+            if (!kInner && (pt.v0 > 0 || pt.v1 < kPiece / 8)) {   // the ends of the column
                 const int e = wl < 8 ? 8 * (pt.v0 - 1) + wl : 8 * pt.v1 + wl - 8;
-                if (wl < 16 && e >= 0 && e < kPiece && e >= pt.lo && e < pt.hi) a.out[at0 + e] = x[e];
+                if (wl < 16 && e >= 0 && e < kPiece && e >= pt.lo && e < pt.hi) x[e] = a.logits[at0 + e];
+                __syncwarp();
             }
-            if (wl == 0) {
-                if (pt.v1 > pt.v0) bulk_s2g(a.out + at0 + 8 * pt.v0, x + 8 * pt.v0, (uint32_t)(pt.v1 - pt.v0) * 16);
-                bulk_commit();                             // a group a piece, empty or not
+            const int first = pt.lo > 0 ? pt.lo : 0, many = (pt.hi < kPiece ? pt.hi : kPiece) - first;
+            const int shift = 8 + piece * kPiece - mis + first;   // from an entry to its place past `first`
+#pragma unroll 1
+            for (int i = wl; i < n; i += 32) {
+                const int e = list[i], at = e - shift;
+                if ((uint32_t)at >= (uint32_t)many || (!kInner && many <= 0)) continue;
+                const uint32_t c = count[e];
+                uint32_t m = c & ~(kSeen | kDraft);
+                if (c & kDraft)                            // its count grows along the columns
+                    for (int d = 1; d <= j; ++d) m += draft_entry[d] == e;
+                const float v = bf16_as_float(x[at + first]);
+                const float factor = (c & kSeen) || m ? (v > 0.f ? over_r : r) : 1.f;
+                const float take = __fadd_rn(__fmul_rn(f, (float)m), m ? p : 0.f);
+                const float z = __fsub_rn(__fmul_rn(v, factor), take);
+                x[at + first] = to_bf16(a.bias_ids ? __fadd_rn(z, bias[e]) : z);
             }
-        } else {
-            for (int e = wl; e < kPiece; e += 32)
-                if (e >= pt.lo && e < pt.hi) a.out[at0 + e] = x[e];
-        }
+            if (row >= 0) {
+                __syncwarp();
+                uint4 *vec = reinterpret_cast<uint4 *>(x) + wl;
+                const uint32_t bit = (uint32_t)(8 * wl - mis) & 31u;
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) words_now[u] = words_next[u];
-        // The place of the piece before this one takes the next load: its store has
-        // had this piece's time to read it, and the warp's own reads are past a
-        // barrier (and a proxy fence).
-        if (wl == 0 && k > 0 && k - 1 + kRing < mine) {
-            bulk_wait_read<1>();
-            fetch(k - 1 + kRing);
+                for (int u = 0; u < kPer; ++u) {
+                    const uint32_t allowed = __funnelshift_r(words_now[u].x, words_now[u].y, bit) & 0xFFu;
+                    if (allowed == 0xFFu || (!kInner && 8 * (wl + 32 * u) >= pt.hi)) continue;
+                    uint4 q = make_uint4(kMasked, kMasked, kMasked, kMasked);
+                    if (allowed != 0u) {
+                        q = vec[32 * u];
+                        // bit k of four to the top of byte k, then 16 copies of each top bit: the words' masks
+                        const uint32_t l = (allowed & 15u) * 0x10204080u, h = (allowed >> 4) * 0x10204080u;
+                        auto keep = [](uint32_t w, uint32_t m) { return (w & m) | (kMasked & ~m); };
+                        q.x = keep(q.x, copies(l, 0x9988));
+                        q.y = keep(q.y, copies(l, 0xBBAA));
+                        q.z = keep(q.z, copies(h, 0x9988));
+                        q.w = keep(q.w, copies(h, 0xBBAA));
+                    }
+                    vec[32 * u] = q;
+                }
+            }
+            if (n > 0 || row >= 0 || !kInner) fence_proxy_async();
+            __syncwarp();
+            if (same_phase) {
+                if (!kInner && (pt.v0 > 0 || pt.v1 < kPiece / 8)) {
+                    const int e = wl < 8 ? 8 * (pt.v0 - 1) + wl : 8 * pt.v1 + wl - 8;
+                    if (wl < 16 && e >= 0 && e < kPiece && e >= pt.lo && e < pt.hi) a.out[at0 + e] = x[e];
+                }
+                if (wl == 0) {
+                    if (kInner || pt.v1 > pt.v0) bulk_s2g(a.out + at0 + 8 * pt.v0, x + 8 * pt.v0, (uint32_t)(pt.v1 - pt.v0) * 16);
+                    bulk_commit();                         // a group a piece, empty or not
+                }
+            } else {
+                for (int e = wl; e < kPiece; e += 32)
+                    if (e >= pt.lo && e < pt.hi) a.out[at0 + e] = x[e];
+                fence_proxy_async();                       // (the next copy comes over what was read)
+                __syncwarp();
+            }
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) words_now[u] = words_next[u];
+            // The place of the piece before this one takes the next load: its store has
+            // had this piece's time to read it, and the warp's own reads are past a
+            // barrier (and a proxy fence).
+            if (wl == 0 && k > 0 && k - 1 + kRing < mine) {
+                bulk_wait_read<1>();
+                const int steps = kRing - 1, mis_then = (mis + steps * mis_stride) & 7;
+                fetch((k - 1) % kRing, at + steps * col_stride - mis_then, mis_then);
+            }
+            mis = mis_next;
+            row = row_next;
+            at += col_stride;
         }
-    }
+    };
+    if (inner) stream(Yes());
+    else stream(No());
     if (wl == 0) {
         bulk_wait_all();
         // given up on a load: it may still be on its way into this CTA's memory (bounded)
