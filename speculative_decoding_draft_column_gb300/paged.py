@@ -68,7 +68,10 @@ def _set_stream(dev):
 def _array(x, dtype, count, dev, name):
     """Pointer of a contiguous CUDA tensor of `dtype` on device `dev` with at
     least `count` elements; these calls take no raw pointers."""
-    if not hasattr(x, "get_device"):
+    try:
+        if x.dtype is dtype and x.get_device() == dev and x.numel() >= count and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
         _bad(f"{name}: need a CUDA tensor")
     if x.get_device() != dev:
         _bad(f"{name}: on {x.device}, need cuda:{dev}")
@@ -76,23 +79,26 @@ def _array(x, dtype, count, dev, name):
         _bad(f"{name}: dtype {x.dtype}, need {dtype}")
     if not x.is_contiguous():
         _bad(f"{name}: tensor must be contiguous")
-    if x.numel() < count:
-        _bad(f"{name}: {x.numel()} elements, the call needs {count}")
-    return x.data_ptr()
+    _bad(f"{name}: {x.numel()} elements, the call needs {count}")
 
 
 def _rows(x, shape, cache, name):
     """Strides of a [tokens, heads, head_dim] tensor of the cache's type and
     device whose rows are contiguous."""
-    if not hasattr(x, "get_device") or x.get_device() != cache.device:
+    try:
+        have, strides = x.shape, x.stride()
+        if x.dtype is cache.torch_dtype and x.get_device() == cache.device and len(have) == 3 and strides[2] == 1 \
+                and have[2] == cache.head_dim and (shape is None or have == shape):
+            return strides
+    except AttributeError:
         _bad(f"{name}: need a CUDA tensor on cuda:{cache.device}, where the cache is")
+    if x.get_device() != cache.device:
+        _bad(f"{name}: on {x.device}, the cache is on cuda:{cache.device}")
     if x.dtype is not cache.torch_dtype:
         _bad(f"{name}: dtype {x.dtype}, the cache's is {cache.torch_dtype}")
-    have = x.shape
     if len(have) != 3 or have[2] != cache.head_dim or (shape is not None and have != shape):
         _bad(f"{name}: shape {tuple(have)}, need {shape or ('tokens', 'heads', cache.head_dim)}")
-    strides = x.stride()
-    if strides[2] != 1 and x.numel():
+    if x.numel():
         _bad(f"{name}: the last dimension must be contiguous")
     return strides
 
