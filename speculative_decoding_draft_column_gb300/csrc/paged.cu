@@ -166,21 +166,27 @@ constexpr int64_t kPartFloats = max2(attn::Shape<128, 2>::kPartFloats, attn::Sha
 int attention_grid(const Device &d) { return d.sms < attn::kMaxSms ? d.sms : attn::kMaxSms; }
 
 template <int D, int QT>
-spec_status launch_attention(const Device &d, const attn::Args &a, bool f16)
+spec_status launch_attention(const Device &d, const attn::Args &a, int64_t chunk, bool f16)
 {
     using S = attn::Shape<D, QT>;
     static_assert(S::kPartFloats <= kPartFloats, "");
     const dim3 grid((unsigned)attention_grid(d));
     const size_t smem = (size_t)d.attn_smem[shape_index<D, QT>()][f16];
-    // What the parts of one item can come to at most: as many as its tiles (the
-    // table's width) make runs of kLeast, of the rows that the tokens fill.  A CTA
-    // joins 128 KB alone in about the 2 us that a cooperative launch costs a
-    // stream (8.7 against 10.6 us a call of one tile), and more than that slower
-    // than the CTAs that share it do.
+    // Whether an item's parts are joined by all its CTAs (a cooperative launch) or
+    // by the last part's CTA alone (an ordinary one: 2 us less a call in a
+    // stream; one token at 1,013 keys 13.2 against 16.4 us, 64 lanes of up to 16
+    // tokens at 6,000 keys 36.6 against 39.7).  Alone, a CTA joins 128 KB in about
+    // those 2 us.  The lengths are on the device, so the number of parts is
+    // estimated from the items that the lanes and heads make, and bounded by the
+    // table's width; where lengths are so uneven that it comes to far more, kAlone
+    // bytes a part keep the loss small.
+    constexpr int64_t kAlone = 32 << 10, kAloneAll = 128 << 10;
     attn::Args b = a;
-    const int64_t tiles = (a.max_pages << a.log_page) / S::BK + 2, runs = tiles / S::kLeast + 2;
-    const int64_t rows = a.tokens * a.group < S::kRows ? a.tokens * a.group : S::kRows;
-    b.share_joins = (runs < (int64_t)grid.x ? runs : (int64_t)grid.x) * rows * D * 4 > (128 << 10);
+    const int64_t ctas = grid.x, rows = chunk * a.group < S::kRows ? chunk * a.group : S::kRows;
+    const int64_t widest = ((a.max_pages << a.log_page) / S::BK + 2) / S::kLeast + 2;
+    const int64_t items = (int64_t)a.lanes * a.heads_kv, likely = ctas / items + 2;
+    const int64_t parts = widest < likely ? widest : likely, part = rows * D * 4;
+    b.share_joins = part > kAlone || parts * part > kAloneAll;
     if (b.share_joins)   // CTAs wait for one another's parts
         return f16 ? launch<true>(attn::attention_kernel<D, QT, true>, grid, S::kThreads, smem, b)
                    : launch<true>(attn::attention_kernel<D, QT, false>, grid, S::kThreads, smem, b);
@@ -346,12 +352,12 @@ spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q,
     a.out = static_cast<uint16_t *>(out); a.lse = lse;
     a.counters = static_cast<unsigned int *>(workspace);
     a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + 2 * attn::kMaxSms * 4);
-    const int64_t chunk = max_new > 0 ? max_new : (tokens + b.lanes - 1) / b.lanes;
+    const int64_t hint = max_new < tokens ? max_new : tokens, chunk = hint > 0 ? hint : (tokens + b.lanes - 1) / b.lanes;
     const bool two = chunk * a.group > 128;   // more rows than one tile: two tiles share every K/V tile
     const bool f16 = c.dtype == SPEC_F16;
-    if (c.head_dim == 256) return launch_attention<256, 1>(*d, a, f16);
-    if (c.head_dim == 128) return two ? launch_attention<128, 2>(*d, a, f16) : launch_attention<128, 1>(*d, a, f16);
-    return two ? launch_attention<64, 2>(*d, a, f16) : launch_attention<64, 1>(*d, a, f16);
+    if (c.head_dim == 256) return launch_attention<256, 1>(*d, a, chunk, f16);
+    if (c.head_dim == 128) return two ? launch_attention<128, 2>(*d, a, chunk, f16) : launch_attention<128, 1>(*d, a, chunk, f16);
+    return two ? launch_attention<64, 2>(*d, a, chunk, f16) : launch_attention<64, 1>(*d, a, chunk, f16);
 }
 
 spec_status spec_logits_process(const uint16_t *logits, int64_t lanes, int32_t cols, int64_t V,
