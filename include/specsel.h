@@ -365,19 +365,23 @@ spec_status spec_paged_store(const void *k, const void *v, int64_t tokens, int64
  *   batch     block_table, cu_new, seq_lens, lanes, max_pages, page_size; row t of q belongs
  *             to the lane with cu_new[lane] <= t < cu_new[lane+1];
  *   scale     positive and finite, usually 1 / sqrt(head_dim);
- *   max_new   the longest chunk to expect: a hint for the choice of tiles, results do not
- *             depend on it;
+ *   max_new   the longest chunk to expect (0: not known): a hint for the choice of tiles and
+ *             of the launch; any value gives a right answer;
  *   out       cache->dtype, contiguous [tokens][heads_q][head_dim], 16-byte aligned;
  *   lse       fp32 [tokens][heads_q], or NULL;
  *   workspace device, 16-byte aligned, spec_paged_attention_workspace() bytes, zeroed once before
- *             its first use; calls that may overlap on the GPU need one each.
+ *             its first use (and after a wait that gave up, which spec_device_status reports);
+ *             calls that may overlap on the GPU need one each.
  * Rows of q past cu_new[lanes] are left alone.  A row with no key in reach (a
  * seq_len below the chunk) gets out = 0 and lse = -inf.  What the cache holds
  * past a lane's last position or before its window, NaN included, does not
  * matter; values at positions inside seq_len must be finite.  Table entries outside
  * [0, pages) read as zero keys and values.
  * The scores and their sums are fp32; the weights w enter the second product
- * rounded to dtype, unnormalised; out is rounded once. */
+ * rounded to dtype, unnormalised; out is rounded once.  The sums' order follows
+ * from the lengths and the device alone: equal calls give equal bits.
+ * One launch: a grid of one CTA per SM, cooperative where items are shared by
+ * several CTAs and their parts are not small.  Its waits are bounded. */
 spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
                                  int64_t q_head_stride, const spec_paged_cache *cache, const spec_paged_batch *batch,
                                  float scale, int64_t window, int64_t max_new, void *out, float *lse,

@@ -32,10 +32,22 @@
 // launch is cooperative, so all CTAs are there; runs are equal, so the wait is
 // short, and it is bounded.  One token of one head over 19,456 keys, 152 parts: 47 us
 // with the last part's CTA joining alone -- 927 us for 128 rows of 256 --, 24 and 28 us with a
-// second kernel, which costs every call 4 us.)  Where the table's width bounds all
-// parts of an item to little, the last part's CTA does join alone, and the launch
-// is an ordinary one: 2 us less outside of graphs.  The loader warp works the items out and hands
-// them to the others through a ring in shared memory.
+// second kernel, which costs every call 4 us.)  Where the parts of an item are small,
+// the last part's CTA does join alone, and the launch is an ordinary one (the
+// host's rule is at the launch).  The loader warp works the items out and hands them
+// to the others through a ring in shared memory.
+//
+// What bounds it, on GB300 (graph-replayed; fractions of a measured copy, 6,788 GB/s, and
+// of a cuBLAS bf16 product, 1,886 TFLOP/s).  Many cached keys for few rows: the cache's bytes --
+// 16 lanes of 8 tokens over 16,000 keys, 32 query on 8 key/value heads of 128, 168 us, 0.92; 16
+// tokens over 262,144 keys 167 us, 0.95.  Chunks: the chain of a stream from one S to
+// the next (product, softmax, product) with the tensor pipe 50-60% busy -- 2,048 tokens over
+// 30,000 keys 735 us, 1,410 TFLOP/s, 0.75; heads of 64 855 TFLOP/s (the same softmax for half
+// the products), heads of 256 1,120 (K and V tiles of 64 keys from L2 for one row tile).  Little
+// work: the chain of one tile, 8 us (lengths 1.0, runs 1.5, first tile 1.5, scores 0.4, softmax
+// 1-2, product 0.4, output 1), and 3 us more where parts are joined.  Neither the exponentials (a polynomial for a
+// quarter of them: 748 -> 804 us) nor the second pass over S (held back in registers: 745 -> 769 us)
+// is what a chunk waits for.
 #pragma once
 
 #include <cuda.h>
