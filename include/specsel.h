@@ -405,7 +405,7 @@ int64_t spec_paged_attention_workspace(void);
  *   drafts       int32 [lanes][cols-1], or NULL: no drafts counted;
  *   penalties    fp32 [lanes][3]: r > 0 (1: none), f, p; or NULL: none;
  *   bias_ids, bias_vals   int32, fp32 [lanes][max_bias], the first bias_lens[l] in use; or all NULL;
- *                equal ids of a lane add up (in no fixed order);
+ *                equal ids of a lane add up, in their order, in fp32;
  *   mask         uint32 [mask_count][(V+31)/32]: bit t%32 of word t/32 set: t is allowed; mask_rows int32
  *                [lanes*cols]: the column's row of mask, outside [0, mask_count): no mask; or both NULL.
  * Ids outside [0, V) are ignored.  out may be logits itself (in place), and

@@ -20,7 +20,8 @@ constexpr int kRing = 2;                 // pieces a warp has in shared memory
 constexpr int kList = kPiece + 8;        // listed tokens of a piece, in any phase
 constexpr int kMaxCols = SPEC_MAX_GAMMA + 1;
 constexpr uint32_t kSeen = 0x80000000u;  // the token is in the prompt
-constexpr uint32_t kDraft = 0x40000000u; // the token is one of the drafts; the other bits count the output
+constexpr uint32_t kDraft = 0x40000000u; // the token is one of the drafts
+constexpr uint32_t kBiased = 0x20000000u; // the token has a bias; the other bits count the output
 constexpr int32_t kNoId = INT32_MIN;        // an id of no window
 constexpr uint32_t kMasked = 0xFF80FF80u;   // two bf16 -inf
 static_assert(kWindow % 4 == 0, "");
@@ -105,6 +106,7 @@ __global__ void __launch_bounds__(kThreads, 2) process_kernel(const __grid_const
     __shared__ int n_listed[kPieces];
     __shared__ int32_t draft_entry[kMaxCols], mask_row[kMaxCols];
     __shared__ uint64_t full[kWarps][kRing];
+    __shared__ int bias_again;
     const int tid = threadIdx.x, warp = tid >> 5, wl = tid & 31;
     const int64_t lane = blockIdx.y, t0 = (int64_t)blockIdx.x * kSlice;
     const int64_t w0 = t0 - 8;   // the token of window entry 0
@@ -118,7 +120,10 @@ __global__ void __launch_bounds__(kThreads, 2) process_kernel(const __grid_const
     }
     for (int i = tid; i < kWindow / 32 + 1; i += kThreads) touched[i] = 0u;
     if (tid < kWarps * kRing) mbar_init(&full[0][0] + tid, 1);
-    if (tid == 0) s_gave_up = 0u;
+    if (tid == 0) {
+        s_gave_up = 0u;
+        bias_again = 0;
+    }
     fence_mbar_init();
     pdl_wait();
     __syncthreads();
@@ -238,12 +243,15 @@ __global__ void __launch_bounds__(kThreads, 2) process_kernel(const __grid_const
         const int64_t tail = head + 4 * quads, i = tid < head ? tid : tail + tid - head;
         if (i < whole && (tid < head || i >= tail)) met(__ldg(h + i), i);
     }
-    if (a.bias_ids) {
-        const int64_t nb = clamp_len(__ldg(a.bias_lens + lane), a.max_bias);
-        for (int64_t i = tid; i < nb; i += kThreads) {
-            const uint32_t e = entry(__ldg(a.bias_ids + lane * a.max_bias + i));
+    const int32_t *bias_ids = a.bias_ids + lane * a.max_bias;
+    const float *bias_vals = a.bias_vals + lane * a.max_bias;
+    const int64_t biases = a.bias_ids ? clamp_len(__ldg(a.bias_lens + lane), a.max_bias) : 0;
+    if (biases > 0) {
+        for (int64_t i = tid; i < biases; i += kThreads) {
+            const uint32_t e = entry(__ldg(bias_ids + i));
             if (e < limit) {
-                atomicAdd(&bias[e], __ldg(a.bias_vals + lane * a.max_bias + i));
+                if (atomicOr(&count[e], kBiased) & kBiased) bias_again = 1;
+                else bias[e] = __ldg(bias_vals + i);
                 touch(e);
             }
         }
@@ -258,6 +266,20 @@ __global__ void __launch_bounds__(kThreads, 2) process_kernel(const __grid_const
     const int64_t words = (a.V + 31) / 32;
     const uint32_t *mask0 = a.mask ? a.mask + (t0 >> 5) : nullptr;
     __syncthreads();
+
+    // An id given twice: the first of its places adds them all up, in their order.
+    if (bias_again)
+        for (int64_t i = tid; i < biases; i += kThreads) {
+            const int32_t id = __ldg(bias_ids + i);
+            if (entry(id) >= limit) continue;
+            int64_t j = 0;
+            while (j < i && __ldg(bias_ids + j) != id) ++j;
+            if (j < i) continue;
+            float sum = __ldg(bias_vals + i);
+            for (j = i + 1; j < biases; ++j)
+                if (__ldg(bias_ids + j) == id) sum = __fadd_rn(sum, __ldg(bias_vals + j));
+            bias[entry(id)] = sum;
+        }
 
     // The pieces' lists, in order, from the bits.  Entry e is element e - 8 + mis
     // of the slice: a piece's list has the first eight entries of the next piece too.
@@ -321,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2) process_kernel(const __grid_const
                 const int e = list[i], at = e - shift;
                 if ((uint32_t)at >= (uint32_t)many || (!kInner && many <= 0)) continue;
                 const uint32_t c = count[e];
-                uint32_t m = c & ~(kSeen | kDraft);
+                uint32_t m = c & ~(kSeen | kDraft | kBiased);
                 if (c & kDraft)                            // its count grows along the columns
                     for (int d = 1; d <= j; ++d) m += draft_entry[d] == e;
                 const float v = bf16_as_float(x[at + first]);

@@ -126,6 +126,26 @@ def test_each_rule_alone(sd):
         _run(sd, 2, 4, 9_001, 300, seed=11, **kw)
 
 
+def test_repeated_biases_add_up_in_order(sd):
+    """Sums whose value depends on the order: those of fp32 additions from the first to the last, in every call."""
+    import torch
+    V, nb = 9_000, 700
+    rng = np.random.default_rng(5)
+    ids = rng.choice([3, 17, 4_095, 4_096, 8_999], size=(2, nb)).astype(np.int32)
+    ids[1, :3] = -1, V, 5_000                 # two of no token, one given once
+    vals = (rng.standard_normal((2, nb)) * 10.0 ** rng.integers(-3, 8, (2, nb))).astype(np.float32)
+    lens = [nb, nb - 1]
+    want = np.zeros((2, V), dtype=np.float32)
+    for l in range(2):
+        for t, v in zip(ids[l, :lens[l]], vals[l, :lens[l]]):
+            if 0 <= t < V:
+                want[l, t] = np.float32(want[l, t] + v)
+    x = torch.zeros((2, V), dtype=torch.bfloat16, device="cuda")
+    for _ in range(3):
+        y = sd.process_logits(x, 2, 1, bias_ids=_i32(ids), bias_vals=torch.from_numpy(vals).cuda(), bias_lens=_i32(lens))
+        assert torch.equal(y, torch.from_numpy(want).to(torch.bfloat16).cuda())
+
+
 def test_largest_block(sd):
     _run(sd, 5, 16, 20_011, 5_000, seed=3, nb=300, mask=True)
 
