@@ -368,12 +368,13 @@ spec_status spec_paged_store(const void *k, const void *v, int64_t tokens, int64
  *   max_new   the longest chunk to expect (0: not known): a hint for the choice of tiles and
  *             of the launch; any value gives a right answer;
  *   out       cache->dtype, contiguous [tokens][heads_q][head_dim], 16-byte aligned;
- *   lse       fp32 [tokens][heads_q], or NULL;
+ *   lse       fp32 [tokens][heads_q], or NULL; out and lse must not overlap what the call reads;
  *   workspace device, 16-byte aligned, spec_paged_attention_workspace() bytes, zeroed once before
  *             its first use (and after a wait that gave up, which spec_device_status reports);
  *             calls that may overlap on the GPU need one each.
  * Rows of q past cu_new[lanes] are left alone.  A row with no key in reach (a
- * seq_len below the chunk) gets out = 0 and lse = -inf.  What the cache holds
+ * seq_len below the chunk) gets out = 0 and lse = -inf; a row whose scores are
+ * NaN gets NaN, and no other row does.  What the cache holds
  * past a lane's last position or before its window, NaN included, does not
  * matter; values at positions inside seq_len must be finite.  Table entries outside
  * [0, pages) read as zero keys and values.

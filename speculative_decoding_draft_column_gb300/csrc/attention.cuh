@@ -825,10 +825,12 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         const int pair = 1 + st * 4 + quad;                       // barrier of the two warps with these rows
         uint32_t tile_n = 0, s_n[2] = {0, 0}, pv_n = 0;           // tiles so far, units per S buffer, PVs of this stream
         int published = -1;                                       // slot of a part just written
+        bool stop = false;                                        // a wait gave up: no parts, no joins
         for (uint32_t n = 0;; ++n) {
             const bool ok = wait(&bar.item_full[n % kItems], (n / kItems) & 1);
             // all softmax warps go on or none does: the barriers below count on it
-            const bool stop = named_barrier_any(kAllSoftmax, S::kSoftmaxWarps * 32, !ok);
+            stop = named_barrier_any(kAllSoftmax, S::kSoftmaxWarps * 32, !ok);
+            if (stop) break;                 // (what the joins hold is not known to be there)
             if (published >= 0) {            // the last item's part is complete
                 if (tid == 0) {              // (the barrier orders the other threads' writes before this fence)
                     __threadfence();
@@ -841,7 +843,6 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 }
                 published = -1;
             }
-            if (stop) break;
             const Item &it = items[n % kItems];
             const int tiles = it.tiles;
             if (tiles == 0) break;
@@ -1002,7 +1003,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             const int slot = it.slot;
             const bool split = slot >= 0;
             float *part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * S::kPartFloats + (QT == 2 ? st * 128 * (D + 2) : 0);
-            const float inv = split ? 1.f : l > 0.f ? 1.f / l : 0.f;
+            const float inv = split ? 1.f : l == 0.f ? 0.f : 1.f / l;   // (NaN scores: NaN)
             const int h = it.head * a.group + (int)(valid ? gr - (int64_t)tok * a.group : 0);
             const int64_t out_row = ((int64_t)it.first + tok) * a.heads_q + h;
             if (live) {
@@ -1021,7 +1022,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                             o[e] = __float_as_uint(v0 + v1);
                         }
                     }
-                    if (l <= 0.f) {
+                    if (l == 0.f) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) o[e] = 0u;
                     }
@@ -1053,7 +1054,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     ml[row] = live ? m : -INFINITY;
                     ml[128 + row] = live ? l : 0.f;
                 } else if (a.lse) {
-                    a.lse[out_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                    a.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                 }
             }
             fence_before();
@@ -1070,7 +1071,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         // maximum, and their sums are added up in order.
         constexpr int kT = S::kSoftmaxWarps * 32;
         float *red = reinterpret_cast<float *>(kv_smem);          // [kT][6]: nothing is on its way there any more
-        if (a.share_joins && lane == 0 && warp < 2 && joins[warp].n > 0) {   // a warp waits for each of the two items
+        if (!stop && a.share_joins && lane == 0 && warp < 2 && joins[warp].n > 0) {   // a warp waits for each of the two items
             const Join &j = joins[warp];
             const uint64_t t0 = global_ns();
             while (ld_acquire(a.counters + j.first_cta) < (unsigned)j.n) {
@@ -1087,14 +1088,14 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 a.counters[kMaxSms + j.first_cta] = 0u;
             }
         }
-        if (joins[0].n + joins[1].n > 0) named_barrier(kAllSoftmax, kT);
+        if (!stop && joins[0].n + joins[1].n > 0) named_barrier(kAllSoftmax, kT);
         // this CTA's elements of both items, one after the other
         int from[2], count[2];
 #pragma unroll
         for (int sl = 0; sl < 2; ++sl) {
             const Join &j = joins[sl];
             from[sl] = count[sl] = 0;
-            if (j.n == 0 || !(a.share_joins || came_last[sl])) continue;
+            if (stop || j.n == 0 || !(a.share_joins || came_last[sl])) continue;
             const int all = j.rows * (D / 4), sharers = a.share_joins ? j.n : 1, mine = a.share_joins ? (int)blockIdx.x - j.first_cta : 0;
             from[sl] = (int)((uint32_t)(all * mine) / (uint32_t)sharers);
             count[sl] = (int)((uint32_t)(all * (mine + 1)) / (uint32_t)sharers) - from[sl];
@@ -1169,10 +1170,10 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 const Join &j = joins[sl[u]];
                 const uint32_t g = (uint32_t)j.rt * S::kRows + r[u], tok = div_group(a, g);
                 const int64_t orow = ((int64_t)j.first + tok) * a.heads_q + (int64_t)j.head * a.group + (g - tok * a.group);
-                const float iv = L[u] > 0.f ? 1.f / L[u] : 0.f;
+                const float iv = L[u] == 0.f ? 0.f : 1.f / L[u];
                 *reinterpret_cast<uint2 *>(a.out + orow * D + c4[u] * 4) =
                     make_uint2(pack2<F16>(o[u][0] * iv, o[u][1] * iv), pack2<F16>(o[u][2] * iv, o[u][3] * iv));
-                if (c4[u] == 0 && a.lse) a.lse[orow] = L[u] > 0.f ? (M[u] + log2f(L[u])) * kLn2 : -INFINITY;
+                if (c4[u] == 0 && a.lse) a.lse[orow] = L[u] == 0.f ? -INFINITY : (M[u] + log2f(L[u])) * kLn2;
             }
         }
     }

@@ -327,6 +327,8 @@ spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q,
     if (misaligned(q, 16) || misaligned(out, 16) || misaligned(workspace, 16) || misaligned(lse, 4) ||
         misaligned(b.block_table, 4) || misaligned(b.cu_new, 4) || misaligned(b.seq_lens, 4))
         return fail(SPEC_ERR_ARG, "misaligned pointer (q, out and workspace need 16 bytes, int32 and lse 4)");
+    const char *q0 = static_cast<const char *>(q), *out0 = static_cast<const char *>(out);
+    if (q0 >= out0 && q0 < out0 + tokens * heads_q * c.head_dim * 2) return fail(SPEC_ERR_ARG, "out overlaps q");
     const int64_t need = spec_paged_attention_workspace();
     if (need < 0) return (spec_status)need;
     if (workspace_bytes < need)

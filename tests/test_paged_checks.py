@@ -108,6 +108,14 @@ def test_attention_refusals(sd):
     assert call(batch=_batch(sd, lanes=0)) == sd.SPEC_OK
 
 
+def test_attention_in_place_is_refused(sd):
+    def call(q, out):
+        return sd.lib.spec_paged_attention(q, 4, 4, 256, 64, ctypes.byref(_cache(sd)), ctypes.byref(_batch(sd)), 0.1, 0, 0, out,
+                                           None, P, 1 << 40)
+    _refused(sd, call(P, P), "overlaps")
+    _refused(sd, call(P + 4 * 256 * 2 - 16, P), "overlaps")
+
+
 def test_logits_refusals(sd):
     def call(lg=P, lanes=2, cols=3, V=100, h=None, hs=0, pl=None, hl=None, d=None, pen=None, bi=None, bv=None, nb=0, bl=None,
              m=None, mc=0, mr=None, out=P + (1 << 20)):

@@ -242,6 +242,24 @@ def test_large_scores(sd, dim):
         _check(c, out, lse)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,ctx", [([1], [40]), ([5, 3], [300, 90]), ([2], [9_000]), ([200], [700])])
+def test_nan_queries_stay_in_their_rows(sd, dim, new, ctx):
+    """A head of a token that is NaN gives NaN for itself and leaves the other rows' bits alone."""
+    import torch
+    c = _case(new, ctx, 2, 4, dim, 16, "bf16", seed=9)
+    out, lse = _attend(sd, c, max_new=max(new))
+    _check(c, out, lse)
+    q = c["q"].clone()
+    gone = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    for t in range(0, c["cu"][-1], 3):
+        gone[t, t % 8] = gone[t, (t + 5) % 8] = True
+    q[gone] = float("nan")
+    out2, lse2 = _attend(sd, c, q=q, max_new=max(new))
+    assert torch.isnan(out2[gone]).all() and torch.isnan(lse2[gone]).all()
+    assert torch.equal(out2[~gone].view(torch.int16), out[~gone].view(torch.int16)) and torch.equal(lse2[~gone], lse[~gone])
+
+
 def test_strided_queries_and_scale(sd):
     import torch
     c = _case([8, 1], [200, 31], 2, 4, 128, 16, "bf16")
