@@ -295,6 +295,13 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, i
                  : "memory");
 }
 
+// 16 bytes global -> shared, and the wait for all of the thread's
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
@@ -790,9 +797,13 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         __syncwarp();
     } else if (warp >= kQLoader) {
         // ---- Q: 16-byte pieces of the item's rows, consecutive lanes on
-        // consecutive pieces; rows past the item's keep what is there
-        const int t0 = tid - kQLoader * 32;
-        constexpr int kPieces = D / 8;
+        // consecutive pieces, all of them on their way together; rows past the item's
+        // keep what is there.  (Through registers, 8 at a time, 256 rows took 4 us.)
+        constexpr int kPieces = D / 8, kStep = 64 / kPieces;       // kStep rows a pass
+        const int p = (tid - kQLoader * 32) % kPieces, r0 = (tid - kQLoader * 32) / kPieces;
+        // kStep rows on: step_t tokens and step_h heads, less a token's heads for one more token
+        const int step_t = (int)div_group(a, kStep), step_h = kStep - step_t * a.group;
+        const int64_t step = step_t * a.qs_t + step_h * a.qs_h, carry = a.qs_t - a.group * a.qs_h;
         for (uint32_t n = 0;; ++n) {
             if (!__all_sync(kFull, wait(&bar.item_full[n % kItems], (n / kItems) & 1))) break;
             const Item it = items[n % kItems];
@@ -803,16 +814,21 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             if (!__all_sync(kFull, wait(&bar.q_empty[qb], ((n / S::QB) & 1) ^ 1))) break;
             const int64_t row0 = (int64_t)it.rt * S::kRows, have = (int64_t)it.n * a.group - row0;
             const int valid = have < S::kRows ? (int)have : S::kRows;
-            uint8_t *dst = q_smem + qb * QT * S::kQBytes;
-#pragma unroll 8
-            for (int i = t0; i < valid * kPieces; i += 64) {
-                const int r = i / kPieces, p = i % kPieces;
-                const uint32_t gr = (uint32_t)row0 + r, tok = div_group(a, gr);
-                const int h = it.head * a.group + (int)(gr - tok * a.group);
-                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)(it.first + (int)tok) * a.qs_t + h * a.qs_h) + p);
-                *reinterpret_cast<uint4 *>(dst + (r >> 7) * S::kQBytes + (p >> 3) * (128 * 128) + (r & 127) * 128 +
-                                           (((p & 7) ^ (r & 7)) << 4)) = x;
+            const uint32_t dst = smem_u32(q_smem) + qb * QT * S::kQBytes + (p >> 3) * (128 * 128);
+            const uint32_t gr = (uint32_t)row0 + r0, tok = div_group(a, gr);
+            int h = (int)(gr - tok * a.group);
+            const uint16_t *src = a.q + (int64_t)(it.first + (int)tok) * a.qs_t + (int64_t)(it.head * a.group + h) * a.qs_h + p * 8;
+#pragma unroll 4
+            for (int r = r0; r < valid; r += kStep) {
+                copy16(dst + (r >> 7) * S::kQBytes + (r & 127) * 128 + (((p & 7) ^ (r & 7)) << 4), src);
+                h += step_h;
+                src += step;
+                if (h >= a.group) {
+                    h -= a.group;
+                    src += carry;
+                }
             }
+            copies_landed();
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.q_full[qb]);
