@@ -458,6 +458,7 @@ struct Bars {
     uint64_t full[S::kStages], empty[S::kStages];
     uint64_t s_full[2], p_full[2], o_done[2];
     uint64_t q_full[2], q_empty[2], item_full[kItems], item_empty[kItems], drain;
+    uint64_t part_full[2], part_known[2];   // the part in a slot is written; the others know
 };
 
 __device__ __forceinline__ void named_barrier(int id, int threads)
@@ -511,6 +512,8 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             mbar_init(&bar.o_done[i], 1);
             mbar_init(&bar.q_full[i], 2);
             mbar_init(&bar.q_empty[i], 1);
+            mbar_init(&bar.part_full[i], S::kSoftmaxWarps);
+            mbar_init(&bar.part_known[i], 1);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&bar.item_full[i], 1);
@@ -804,11 +807,33 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         // kStep rows on: step_t tokens and step_h heads, less a token's heads for one more token
         const int step_t = (int)div_group(a, kStep), step_h = kStep - step_t * a.group;
         const int64_t step = step_t * a.qs_t + step_h * a.qs_h, carry = a.qs_t - a.group * a.qs_h;
+        // The last of these warps also tells the other CTAs of this CTA's parts, an item
+        // late: a fence waits for the part's writes, 1-2 us in which the softmax warps go on.
+        int part = -1;                                             // slot of the last item's part
+        auto tell = [&]() -> bool {
+            if (part < 0 || warp == kQLoader) return true;
+            if (!__all_sync(kFull, wait(&bar.part_full[part], 0))) return false;
+            if (lane == 0) {
+                __threadfence();
+                const Join &j = joins[part];
+                const uint32_t before = atom_add_acq_rel(a.counters + j.first_cta, 1u);
+                if (!a.share_joins && before == (uint32_t)j.n - 1) {
+                    came_last[part] = 1;
+                    a.counters[j.first_cta] = 0u;
+                }
+                mbar_arrive(&bar.part_known[part]);
+            }
+            __syncwarp();
+            return true;
+        };
         for (uint32_t n = 0;; ++n) {
             if (!__all_sync(kFull, wait(&bar.item_full[n % kItems], (n / kItems) & 1))) break;
             const Item it = items[n % kItems];
             __syncwarp();
-            if (it.tiles == 0) break;
+            if (it.tiles == 0) {
+                tell();
+                break;
+            }
             if (lane == 0) mbar_arrive(&bar.item_empty[n % kItems]);
             const uint32_t qb = n % S::QB;
             if (!__all_sync(kFull, wait(&bar.q_empty[qb], ((n / S::QB) & 1) ^ 1))) break;
@@ -832,6 +857,8 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.q_full[qb]);
+            if (!tell()) break;
+            part = it.slot;
         }
     } else {
         // ---- softmax, correction and epilogue: stream `st`, columns [half * kW, half * kW + kW) of its tiles
@@ -840,25 +867,12 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         const int pair = 1 + st * 4 + quad;                       // barrier of the two warps with these rows
         uint32_t tile_n = 0, s_n[2] = {0, 0}, pv_n = 0;           // tiles so far, units per S buffer, PVs of this stream
-        int published = -1;                                       // slot of a part just written
         bool stop = false;                                        // a wait gave up: no parts, no joins
         for (uint32_t n = 0;; ++n) {
             const bool ok = wait(&bar.item_full[n % kItems], (n / kItems) & 1);
             // all softmax warps go on or none does: the barriers below count on it
             stop = named_barrier_any(kAllSoftmax, S::kSoftmaxWarps * 32, !ok);
-            if (stop) break;                 // (what the joins hold is not known to be there)
-            if (published >= 0) {            // the last item's part is complete
-                if (tid == 0) {              // (the barrier orders the other threads' writes before this fence)
-                    __threadfence();
-                    const Join &j = joins[published];
-                    const uint32_t before = atom_add_acq_rel(a.counters + j.first_cta, 1u);
-                    if (!a.share_joins && before == (uint32_t)j.n - 1) {
-                        came_last[published] = 1;
-                        a.counters[j.first_cta] = 0u;
-                    }
-                }
-                published = -1;
-            }
+            if (stop) break;
             const Item &it = items[n % kItems];
             const int tiles = it.tiles;
             if (tiles == 0) break;
@@ -1074,9 +1088,11 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 }
             }
             fence_before();
-            published = slot;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.item_empty[n % kItems]);
+            if (lane == 0) {
+                if (split) mbar_arrive(&bar.part_full[slot]);
+                mbar_arrive(&bar.item_empty[n % kItems]);
+            }
             // (O, the swap area and the pair barriers are used again only past the
             // barrier at the next item's start)
         }
@@ -1087,11 +1103,13 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         // maximum, and their sums are added up in order.
         constexpr int kT = S::kSoftmaxWarps * 32;
         float *red = reinterpret_cast<float *>(kv_smem);          // [kT][6]: nothing is on its way there any more
+        bool failed = false;
         if (!stop && a.share_joins && lane == 0 && warp < 2 && joins[warp].n > 0) {   // a warp waits for each of the two items
             const Join &j = joins[warp];
             const uint64_t t0 = global_ns();
             while (ld_acquire(a.counters + j.first_cta) < (unsigned)j.n) {
-                if (*reinterpret_cast<volatile unsigned int *>(&s_gave_up)) break;
+                failed = *reinterpret_cast<volatile unsigned int *>(&s_gave_up) != 0u;
+                if (failed) break;
                 if (global_ns() - t0 > kWaitLimitNs) {
                     s_gave_up = 1u;
                     atomicOr(&g_wait_timeouts, 1u);
@@ -1104,7 +1122,8 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 a.counters[kMaxSms + j.first_cta] = 0u;
             }
         }
-        if (!stop && joins[0].n + joins[1].n > 0) named_barrier(kAllSoftmax, kT);
+        if (!stop && !a.share_joins && lane == 0 && warp < 2 && joins[warp].n > 0) failed = !wait(&bar.part_known[warp], 0);
+        if (!stop && joins[0].n + joins[1].n > 0) stop = named_barrier_any(kAllSoftmax, kT, failed);
         // this CTA's elements of both items, one after the other
         int from[2], count[2];
 #pragma unroll
