@@ -77,6 +77,7 @@ struct Shape {
     static constexpr int kSwap = 512;                          // floats that softmax warps exchange through
     static constexpr int kPayload = QB * QT * kQBytes + kStages * kStageBytes + kSwap * 4;
     static constexpr int kRows = QT * 128;
+    static constexpr int kExtra = QT == 2 ? 4 : 3;             // tiles that an item's other work costs
     static constexpr int kLeast = QT == 1 ? 2 : 1;             // units of a run that an item is cut into, at least
     // TMEM columns: S buffers, then O
     static constexpr int kO = 2 * BK;
@@ -390,6 +391,7 @@ __device__ __forceinline__ int64_t head_units(const Args &a, const Lane &l)
 struct Run {
     int64_t u, end;        // next unit, end of the run
     int64_t item0;         // first unit of the current item
+    int32_t extra;         // units of an item before its tiles'
     int32_t lane, head, rt;
     Lane ln;
     int32_t rts;
@@ -398,7 +400,7 @@ struct Run {
 struct Segment {           // the part of an item that this CTA computes
     Reach r;
     int32_t tile, tiles;   // first tile, number of tiles
-    int64_t item0;
+    int64_t item0;         // unit of the item's first tile
     int32_t item_tiles;
     int32_t lane, head, rt;
     Lane ln;
@@ -417,25 +419,27 @@ __device__ __forceinline__ bool next_segment(const Args &a, Run &w, Segment &s)
         w.rts = row_tiles<S>(a, w.ln.n);
     }
     s.r = reach_of<S>(a, w.ln.n, w.ln.seq, w.rt);
-    s.item0 = w.item0;
+    s.item0 = w.item0 + w.extra;
     s.item_tiles = s.r.tiles;
-    const int64_t skip = w.u - w.item0, left = s.r.tiles - skip, room = w.end - w.u;
-    s.tile = s.r.tile0 + (int)skip;
-    s.tiles = (int)(left < room ? left : room);
+    const int64_t left = s.r.tiles - (w.u - s.item0), room = w.end - w.u, to = w.u + (left < room ? left : room);
+    const int from = w.u > s.item0 ? (int)(w.u - s.item0) : 0;
+    s.tile = s.r.tile0 + from;
+    s.tiles = (int)(to - s.item0) - from;
     s.lane = w.lane; s.head = w.head; s.rt = w.rt; s.ln = w.ln;
-    w.u += s.tiles;
-    w.item0 += s.r.tiles;
+    w.u = to;
+    w.item0 = s.item0 + s.r.tiles;
     ++w.rt;
-    return true;
+    return s.tiles > 0;    // (a run that ends before an item's first tile leaves it to the next)
 }
 
 // Run c is units [floor(c * total / grid), floor((c + 1) * total / grid)).
 struct Plan {
-    int64_t total;         // units of the step
+    int64_t total;         // units of the step: the tiles, and `extra` for every item
     int64_t each;          // total / grid
     int64_t lane_u;        // units before the lane where this CTA's run starts
     int64_t per_head;      // units of one head of that lane
     int32_t more, lane, grid;   // total % grid; that lane; CTAs that have a run
+    int32_t extra;
 };
 
 __device__ __forceinline__ int64_t run_start(int cta, int64_t each, int32_t more, int32_t grid) { return cta * each + (uint32_t)(cta * more) / (uint32_t)grid; }
@@ -574,9 +578,18 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             all += x;
             below += w < warp ? x : 0;
         }
-        const int64_t total = all & kUnits, before = (below + incl - mine) & kUnits;
-        mine &= kUnits;
-        head &= kUnits;
+        // An item costs more than its tiles: its rows of Q, its first scores and its output
+        // take the time of kExtra tiles, and a run is cut by that too (a prompt of 2,048 at 0
+        // keys 84.3 us without, 72.3 with 1, 63.0 with 2, 59.1 with 3, 58.5 with 4; 8 lanes of
+        // 8 tokens 57.5, 55.0, 54.4, 54.0, 54.5).  Not where there are too few tiles for
+        // runs of kTwo each: there the cuts are even ones of the tiles (one token at 1,000
+        // keys 12.9 us, with extra units its first part would be shorter than the others).
+        constexpr int kTwo = 2;
+        const int32_t extra = (all & kUnits) >= (int64_t)kTwo * gridDim.x ? S::kExtra : 0;
+        auto units_of = [&](int64_t x) { return (x & kUnits) + extra * (x >> kItemBit); };
+        const int64_t total = units_of(all), before = units_of(below + incl - mine);
+        mine = units_of(mine);
+        head = units_of(head);
         // As many runs as there are CTAs, but not so many that an item has to be
         // cut into runs of less than kLeast units: the streams of a CTA work on two
         // tiles at once, and parts have to be joined.
@@ -591,6 +604,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             plan.each = each;
             plan.more = more;
             plan.grid = (int32_t)grid;
+            plan.extra = extra;
         }
         if ((int64_t)blockIdx.x < grid) {
             const int64_t u0 = run_start(blockIdx.x, each, more, (int32_t)grid);
@@ -599,7 +613,8 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 int l = l0;
                 if (l1 - l0 > 1)
                     for (;; ++l) {
-                        head = head_units<S>(a, lane_of(a, l));
+                        const Lane ln = lane_of(a, l);
+                        head = head_units<S>(a, ln) + extra * row_tiles<S>(a, ln.n);
                         if (u0 < at + head * a.heads_kv) break;
                         at += head * a.heads_kv;
                     }
@@ -624,6 +639,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         if ((int64_t)blockIdx.x < plan.grid) {
             run.u = run_start(blockIdx.x, plan.each, plan.more, plan.grid);
             run.end = run_start(blockIdx.x + 1, plan.each, plan.more, plan.grid);
+            run.extra = plan.extra;
             run.lane = plan.lane;
             run.ln = lane_of(a, run.lane);
             run.rts = row_tiles<S>(a, run.ln.n);
@@ -635,7 +651,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             for (; run.rts > 1; run.rt += 32) {
                 const int rt = run.rt + lane;
                 int all;
-                const int tiles = rt < run.rts ? reach_of<S>(a, run.ln.n, run.ln.seq, rt).tiles : 0;
+                const int tiles = rt < run.rts ? reach_of<S>(a, run.ln.n, run.ln.seq, rt).tiles + run.extra : 0;
                 const int before = warp_exclusive_sum(tiles, lane, all);
                 if (run.u < run.item0 + all) {
                     const uint32_t past = __ballot_sync(kFull, run.u < run.item0 + before + tiles);

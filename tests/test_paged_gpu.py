@@ -303,6 +303,20 @@ def test_many_tiles_per_cta(sd, dim):
     _check(c, out, lse)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_runs_cut_between_items(sd, dim):
+    """Enough tiles for every CTA, in items of one to a dozen: runs that begin and end inside items, between them,
+    and before an item's first tile."""
+    rng = np.random.default_rng(dim + 1)
+    step = 64 if dim == 256 else 128
+    for lanes, new, most, hk, group in ((40, 2, 9, 2, 4), (24, 1, 12, 3, 1), (9, 200, 5, 2, 4), (150, 3, 4, 1, 2)):
+        ctx = (step * most * rng.random(lanes)).astype(int).tolist()
+        c = _case([new] * lanes, ctx, hk, group, dim, 32, "bf16", seed=lanes)
+        for max_new in (new, 0):
+            out, lse = _attend(sd, c, max_new=max_new)
+            _check(c, out, lse)
+
+
 def test_many_lanes(sd):
     rng = np.random.default_rng(3)
     new, ctx = rng.integers(0, 3, 700).tolist(), rng.integers(0, 40, 700).tolist()
