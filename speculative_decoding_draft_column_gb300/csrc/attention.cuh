@@ -1194,8 +1194,8 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     lp[u] = 0.f;
                     x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (p >= n[u]) continue;
-                    mp[u] = __ldcg(q + 128 * D + (r[u] & 127));
-                    lp[u] = __ldcg(q + 128 * D + 128 + (r[u] & 127));
+                    mp[u] = q[128 * D + (r[u] & 127)];             // (read for every four columns: from L1)
+                    lp[u] = q[128 * D + 128 + (r[u] & 127)];
                     x[u] = __ldcg(reinterpret_cast<const float4 *>(q) + c4[u] * 128 + (r[u] & 127));
                 }
 #pragma unroll
