@@ -23,8 +23,8 @@
 // scores, and the pair agrees on the maximum through shared memory.
 //
 // Work.  An item is (lane, key/value head, row tiles); its units are the K/V
-// tiles in reach.  All units of the step, in item order, are cut into equal runs,
-// one per CTA of a grid of one CTA per SM, from the lengths in device memory:
+// tiles in reach, and kExtra for what it costs beside them.  All units of the step,
+// in item order, are cut into equal runs, one per CTA of a grid of one CTA per SM, from the lengths in device memory:
 // ragged batches balance by themselves and a single long lane is split over
 // the whole GPU.  A CTA whose run starts or ends inside an item leaves its part
 // (m, sum, O) in the workspace; when its run is done it waits for the item's
@@ -40,14 +40,15 @@
 // What bounds it, on GB300 (graph-replayed; fractions of a measured copy, 6,788 GB/s, and
 // of a cuBLAS bf16 product, 1,886 TFLOP/s).  Many cached keys for few rows: the cache's bytes --
 // 16 lanes of 8 tokens over 16,000 keys, 32 query on 8 key/value heads of 128, 168 us, 0.92; 16
-// tokens over 262,144 keys 167 us, 0.95.  Chunks: the chain of a stream from one S to
+// tokens over 262,144 keys 165 us, 0.96.  Chunks: the chain of a stream from one S to
 // the next (product, softmax, product) with the tensor pipe 50-60% busy -- 2,048 tokens over
-// 30,000 keys 735 us, 1,410 TFLOP/s, 0.75; heads of 64 855 TFLOP/s (the same softmax for half
-// the products), heads of 256 1,120 (K and V tiles of 64 keys from L2 for one row tile).  Little
+// 30,000 keys 715 us, 1,455 TFLOP/s, 0.77; heads of 64 865 TFLOP/s (the same softmax for half
+// the products), heads of 256 1,125 (K and V tiles of 64 keys from L2 for one row tile).  A prompt of
+// 2,048 at 0 keys 59 us, 585 TFLOP/s: rows of Q, edges, outputs and joins as much as tiles.  Little
 // work: the chain of one tile, 8 us (lengths 1.0, runs 1.5, first tile 1.5, scores 0.4, softmax
 // 1-2, product 0.4, output 1), and 3 us more where parts are joined.  Neither the exponentials (a polynomial for a
 // quarter of them: 748 -> 804 us) nor the second pass over S (held back in registers: 745 -> 769 us)
-// is what a chunk waits for.
+// nor the weights' last columns (their product in two lots: 733 -> 742 us) is what a chunk waits for.
 #pragma once
 
 #include <cuda.h>
@@ -582,10 +583,9 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         // take the time of kExtra tiles, and a run is cut by that too (a prompt of 2,048 at 0
         // keys 84.3 us without, 72.3 with 1, 63.0 with 2, 59.1 with 3, 58.5 with 4; 8 lanes of
         // 8 tokens 57.5, 55.0, 54.4, 54.0, 54.5).  Not where there are too few tiles for
-        // runs of kTwo each: there the cuts are even ones of the tiles (one token at 1,000
+        // runs of two each: there the cuts are even ones of the tiles (one token at 1,000
         // keys 12.9 us, with extra units its first part would be shorter than the others).
-        constexpr int kTwo = 2;
-        const int32_t extra = (all & kUnits) >= (int64_t)kTwo * gridDim.x ? S::kExtra : 0;
+        const int32_t extra = (all & kUnits) >= 2 * (int64_t)gridDim.x ? S::kExtra : 0;
         auto units_of = [&](int64_t x) { return (x & kUnits) + extra * (x >> kItemBit); };
         const int64_t total = units_of(all), before = units_of(below + incl - mine);
         mine = units_of(mine);
