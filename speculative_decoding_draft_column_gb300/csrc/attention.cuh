@@ -1091,8 +1091,12 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                         }
                     }
                 }
-            } else if (valid && !split) {                          // a warp of rows without keys
-                for (int c = c0; c < c0 + cols; c += 8) *reinterpret_cast<uint4 *>(a.out + out_row * D + c) = make_uint4(0, 0, 0, 0);
+            } else if (valid) {                                    // a warp of rows without keys
+                for (int c = c0; c < c0 + cols; c += 8)
+                    if (!split) *reinterpret_cast<uint4 *>(a.out + out_row * D + c) = make_uint4(0, 0, 0, 0);
+                    else
+                        for (int e = 0; e < 2; ++e)                // (what was there, a NaN perhaps, times 0 is not 0)
+                            *(reinterpret_cast<float4 *>(part) + (c / 4 + e) * 128 + row) = make_float4(0.f, 0.f, 0.f, 0.f);
             }
             if (valid && c0 == 0 && cols > 0) {
                 if (split) {
@@ -1114,11 +1118,11 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         }
 
         // ---- the items in parts: wait for the others' and join this CTA's share.
-        // A thread takes four columns of a row; where there are threads to spare,
-        // 2, 4 or 8 of them share an element's parts, each with its own running
-        // maximum, and their sums are added up in order.
+        // A thread takes sixteen columns of a row (four cost a chunk of 2,048 at 0 keys 5 us
+        // more: the maxima and scales of a part are worked out for every element); where
+        // there are threads to spare, up to 32 of them share an element's parts, each with
+        // its own running maximum, and their sums are added up in pairs.
         constexpr int kT = S::kSoftmaxWarps * 32;
-        float *red = reinterpret_cast<float *>(kv_smem);          // [kT][6]: nothing is on its way there any more
         bool failed = false;
         if (!stop && a.share_joins && lane == 0 && warp < 2 && joins[warp].n > 0) {   // a warp waits for each of the two items
             const Join &j = joins[warp];
@@ -1147,85 +1151,65 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             const Join &j = joins[sl];
             from[sl] = count[sl] = 0;
             if (stop || j.n == 0 || !(a.share_joins || came_last[sl])) continue;
-            const int all = j.rows * (D / 4), sharers = a.share_joins ? j.n : 1, mine = a.share_joins ? (int)blockIdx.x - j.first_cta : 0;
+            const int all = j.rows * (D / 16), sharers = a.share_joins ? j.n : 1, mine = a.share_joins ? (int)blockIdx.x - j.first_cta : 0;
             from[sl] = (int)((uint32_t)(all * mine) / (uint32_t)sharers);
             count[sl] = (int)((uint32_t)(all * (mine + 1)) / (uint32_t)sharers) - from[sl];
         }
         const int work = count[0] + count[1], most = max(joins[0].n, joins[1].n);
         int lg = 0;                                                // log2 of the threads of an element
-        while (lg < 3 && (2 << lg) <= most && work << (lg + 1) <= kT) ++lg;
-        const int step = 1 << lg;
-        constexpr int kTwo = 2;                                    // elements of a thread in flight
-        for (int base = 0; base < work; base += kTwo * (kT >> lg)) {
-            const int p0 = tid & (step - 1);
-            int sl[kTwo], r[kTwo], c4[kTwo], n[kTwo];
-            float M[kTwo] = {-INFINITY, -INFINITY}, L[kTwo] = {0.f, 0.f}, o[kTwo][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            const float *first_part[kTwo];                         // the others: one slot on, then every second
-            auto add = [&](int u, float mp, float lp, float x, float y, float z, float w) {
-                const float Mn = fmaxf(M[u], mp), ref = Mn == -INFINITY ? 0.f : Mn, fo = exp2_fast(M[u] - ref), fp = exp2_fast(mp - ref);
-                M[u] = Mn;
-                L[u] = L[u] * fo + lp * fp;
-                o[u][0] = o[u][0] * fo + x * fp;
-                o[u][1] = o[u][1] * fo + y * fp;
-                o[u][2] = o[u][2] * fo + z * fp;
-                o[u][3] = o[u][3] * fo + w * fp;
+        while (lg < 5 && (2 << lg) <= most && work << (lg + 1) <= kT) ++lg;
+        const int step = 1 << lg, p0 = tid & (step - 1);
+        for (int base = 0; base < work; base += kT >> lg) {
+            const int k = base + (tid >> lg), sl = k < count[0] ? 0 : 1;
+            const Join &j = joins[sl];
+            const int e = k < count[0] ? from[0] + k : from[1] + k - count[0], n = k < work ? j.n : 0;
+            const int g = k < work ? (int)((uint32_t)e / (uint32_t)j.rows) : 0, r = k < work ? e - g * j.rows : 0;   // columns 16 g on; over the item's row tiles
+            // the first part; the others are one slot on, then every second
+            const float *first_part = a.parts + ((int64_t)j.first_cta * 2 + 1) * S::kPartFloats + (r >> 7) * 128 * (D + 2);
+            float M = -INFINITY, L = 0.f, o[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = 0.f;
+            auto scales = [&](float mp, float lp, float &fo, float &fp) {
+                const float Mn = fmaxf(M, mp), ref = Mn == -INFINITY ? 0.f : Mn;
+                fo = exp2_fast(M - ref);
+                fp = exp2_fast(mp - ref);
+                M = Mn;
+                L = L * fo + lp * fp;
             };
-            int longest = 0;
-#pragma unroll
-            for (int u = 0; u < kTwo; ++u) {
-                const int k = base + u * (kT >> lg) + (tid >> lg);
-                sl[u] = k < count[0] ? 0 : 1;
-                const Join &j = joins[sl[u]];
-                const int e = k < count[0] ? from[0] + k : from[1] + k - count[0];
-                n[u] = k < work ? j.n : 0;
-                c4[u] = k < work ? (int)((uint32_t)e / (uint32_t)j.rows) : 0;
-                r[u] = k < work ? e - c4[u] * j.rows : 0;          // over the item's row tiles
-                first_part[u] = a.parts + ((int64_t)j.first_cta * 2 + 1) * S::kPartFloats + (r[u] >> 7) * 128 * (D + 2);
-                longest = max(longest, n[u]);
-            }
 #pragma unroll 2
-            for (int p = p0; p < longest; p += step) {
-                float mp[kTwo], lp[kTwo];
-                float4 x[kTwo];
+            for (int p = p0; p < n; p += step) {
+                const float *q = p == 0 ? first_part : first_part + (int64_t)(2 * p - 1) * S::kPartFloats;
+                const float mp = q[128 * D + (r & 127)], lp = q[128 * D + 128 + (r & 127)];
+                float4 x[4];
 #pragma unroll
-                for (int u = 0; u < kTwo; ++u) {
-                    const float *q = p == 0 ? first_part[u] : first_part[u] + (int64_t)(2 * p - 1) * S::kPartFloats;
-                    mp[u] = -INFINITY;
-                    lp[u] = 0.f;
-                    x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (p >= n[u]) continue;
-                    mp[u] = q[128 * D + (r[u] & 127)];             // (read for every four columns: from L1)
-                    lp[u] = q[128 * D + 128 + (r[u] & 127)];
-                    x[u] = __ldcg(reinterpret_cast<const float4 *>(q) + c4[u] * 128 + (r[u] & 127));
-                }
+                for (int i = 0; i < 4; ++i) x[i] = __ldcg(reinterpret_cast<const float4 *>(q) + (4 * g + i) * 128 + (r & 127));
+                float fo, fp;
+                scales(mp, lp, fo, fp);
 #pragma unroll
-                for (int u = 0; u < kTwo; ++u) add(u, mp[u], lp[u], x[u].x, x[u].y, x[u].z, x[u].w);
-            }
-            if (lg > 0) {
-#pragma unroll
-                for (int u = 0; u < kTwo; ++u) {
-                    float *mine6 = red + tid * 6;
-                    mine6[0] = M[u]; mine6[1] = L[u]; mine6[2] = o[u][0]; mine6[3] = o[u][1]; mine6[4] = o[u][2]; mine6[5] = o[u][3];
-                    __syncwarp();                                  // an element's threads are in one warp
-                    if (p0 == 0)
-                        for (int k = 1; k < step; ++k) {
-                            const float *q = mine6 + k * 6;
-                            add(u, q[0], q[1], q[2], q[3], q[4], q[5]);
-                        }
-                    __syncwarp();
+                for (int i = 0; i < 4; ++i) {
+                    o[4 * i] = o[4 * i] * fo + x[i].x * fp;
+                    o[4 * i + 1] = o[4 * i + 1] * fo + x[i].y * fp;
+                    o[4 * i + 2] = o[4 * i + 2] * fo + x[i].z * fp;
+                    o[4 * i + 3] = o[4 * i + 3] * fo + x[i].w * fp;
                 }
             }
+#pragma unroll 1
+            for (int d = 1; d < step; d <<= 1) {                   // (an element's threads are neighbours in a warp; the first's result counts)
+                float fo, fp;
+                scales(__shfl_xor_sync(kFull, M, d), __shfl_xor_sync(kFull, L, d), fo, fp);
 #pragma unroll
-            for (int u = 0; u < kTwo; ++u) {
-                if (n[u] == 0 || p0 != 0) continue;
-                const Join &j = joins[sl[u]];
-                const uint32_t g = (uint32_t)j.rt * S::kRows + r[u], tok = div_group(a, g);
-                const int64_t orow = ((int64_t)j.first + tok) * a.heads_q + (int64_t)j.head * a.group + (g - tok * a.group);
-                const float iv = L[u] == 0.f ? 0.f : 1.f / L[u];
-                *reinterpret_cast<uint2 *>(a.out + orow * D + c4[u] * 4) =
-                    make_uint2(pack2<F16>(o[u][0] * iv, o[u][1] * iv), pack2<F16>(o[u][2] * iv, o[u][3] * iv));
-                if (c4[u] == 0 && a.lse) a.lse[orow] = L[u] == 0.f ? -INFINITY : (M[u] + log2f(L[u])) * kLn2;
+                for (int i = 0; i < 16; ++i) o[i] = o[i] * fo + __shfl_xor_sync(kFull, o[i], d) * fp;
             }
+            if (n == 0 || p0 != 0) continue;
+            const uint32_t gr = (uint32_t)j.rt * S::kRows + r, tok = div_group(a, gr);
+            const int64_t orow = ((int64_t)j.first + tok) * a.heads_q + (int64_t)j.head * a.group + (gr - tok * a.group);
+            const float iv = L == 0.f ? 0.f : 1.f / L;
+            uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + g * 16);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                dst[i] = make_uint4(pack2<F16>(o[8 * i] * iv, o[8 * i + 1] * iv), pack2<F16>(o[8 * i + 2] * iv, o[8 * i + 3] * iv),
+                                    pack2<F16>(o[8 * i + 4] * iv, o[8 * i + 5] * iv), pack2<F16>(o[8 * i + 6] * iv, o[8 * i + 7] * iv));
+            if (g == 0 && a.lse) a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
         }
     }
     __syncthreads();

@@ -260,6 +260,19 @@ def test_nan_queries_stay_in_their_rows(sd, dim, new, ctx):
     assert torch.equal(out2[~gone].view(torch.int16), out[~gone].view(torch.int16)) and torch.equal(lse2[~gone], lse[~gone])
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_rows_with_no_key_after_nan_parts(sd, dim):
+    """An item in parts whose first rows attend nothing, in a workspace where another call's parts were NaN."""
+    ws = sd.new_attention_workspace()
+    c = _case([300], [40_000], 1, 1, dim, 64, "bf16")
+    out, _ = _attend(sd, c, q=c["q"] * float("nan"), max_new=300, ws=ws)
+    assert out[:300].isnan().all()
+    for seq in (200, 160, 250):
+        c = _case([300], [0], 1, 1, dim, 16, "bf16")
+        out, lse = _attend(sd, c, seq=[seq], max_new=300, ws=ws)
+        _check(c, out, lse, seq=[seq])
+
+
 def test_strided_queries_and_scale(sd):
     import torch
     c = _case([8, 1], [200, 31], 2, 4, 128, 16, "bf16")
