@@ -30,8 +30,8 @@
 // (m, sum, O) in the workspace; when its run is done it waits for the item's
 // other parts and joins its share of the item's elements, in the parts' order.  (The
 // launch is cooperative, so all CTAs are there; runs are equal, so the wait is
-// short, and it is bounded.  One token of one head over 19,456 keys, 152 parts: 47 us
-// with the last part's CTA joining alone -- 927 us for 128 rows of 256 --, 24 and 28 us with a
+// short, and it is bounded.  One token of one head over 19,456 keys, 152 parts: 17 us;
+// 47 us with the last part's CTA joining alone -- 927 us for 128 rows of 256 --, 28 us with a
 // second kernel, which costs every call 4 us.)  Where the parts of an item are small,
 // the last part's CTA does join alone, and the launch is an ordinary one (the
 // host's rule is at the launch).  The loader warp works the items out and hands them
@@ -39,12 +39,12 @@
 //
 // What bounds it, on GB300 (graph-replayed; fractions of a measured copy, 6,788 GB/s, and
 // of a cuBLAS bf16 product, 1,886 TFLOP/s).  Many cached keys for few rows: the cache's bytes --
-// 16 lanes of 8 tokens over 16,000 keys, 32 query on 8 key/value heads of 128, 168 us, 0.92; 16
-// tokens over 262,144 keys 165 us, 0.96.  Chunks: the chain of a stream from one S to
+// 16 lanes of 8 tokens over 16,000 keys, 32 query on 8 key/value heads of 128, 166 us, 0.93; 16
+// tokens over 262,144 keys 162 us, 0.98.  Chunks: the chain of a stream from one S to
 // the next (product, softmax, product) with the tensor pipe 50-60% busy -- 2,048 tokens over
-// 30,000 keys 715 us, 1,455 TFLOP/s, 0.77; heads of 64 865 TFLOP/s (the same softmax for half
+// 30,000 keys 709 us, 1,467 TFLOP/s, 0.78; heads of 64 867 TFLOP/s (the same softmax for half
 // the products), heads of 256 1,125 (K and V tiles of 64 keys from L2 for one row tile).  A prompt of
-// 2,048 at 0 keys 59 us, 585 TFLOP/s: rows of Q, edges, outputs and joins as much as tiles.  Little
+// 2,048 at 0 keys 52 us, 659 TFLOP/s: rows of Q, edges, outputs and joins as much as tiles.  Little
 // work: the chain of one tile, 8 us (lengths 1.0, runs 1.5, first tile 1.5, scores 0.4, softmax
 // 1-2, product 0.4, output 1), and 3 us more where parts are joined.  Neither the exponentials (a polynomial for a
 // quarter of them: 748 -> 804 us) nor the second pass over S (held back in registers: 745 -> 769 us)
@@ -1156,8 +1156,8 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             count[sl] = (int)((uint32_t)(all * (mine + 1)) / (uint32_t)sharers) - from[sl];
         }
         const int work = count[0] + count[1], most = max(joins[0].n, joins[1].n);
-        int lg = 0;                                                // log2 of the threads of an element
-        while (lg < 5 && (2 << lg) <= most && work << (lg + 1) <= kT) ++lg;
+        int lg = 0;                                                // log2 of the threads of an element, two parts each at least
+        while (lg < 5 && (4 << lg) <= most && work << (lg + 1) <= kT) ++lg;
         const int step = 1 << lg, p0 = tid & (step - 1);
         for (int base = 0; base < work; base += kT >> lg) {
             const int k = base + (tid >> lg), sl = k < count[0] ? 0 : 1;

@@ -174,9 +174,9 @@ spec_status launch_attention(const Device &d, const attn::Args &a, int64_t chunk
     const size_t smem = (size_t)d.attn_smem[shape_index<D, QT>()][f16];
     // Whether an item's parts are joined by all its CTAs (a cooperative launch) or
     // by the last part's CTA alone (an ordinary one: 3 us less a call in a
-    // stream; one token at 1,013 keys 13.3 against 16.4 us, 64 lanes of up to 16
-    // tokens at 6,000 keys 28.6 against 32.7, 8 lanes of 8 at 500-16,000 keys 66.0
-    // against 69.6).  Alone, a CTA joins 128 KB in 2 us.  The lengths are on the device, so the number of parts is
+    // stream; one token at 1,013 keys 12.7 against 16.4 us, 64 lanes of up to 16
+    // tokens at 6,000 keys 27.0 against 30.8, 8 lanes of 8 at 500-16,000 keys 65.7
+    // against 68.8).  Alone, a CTA joins 128 KB in 2 us.  The lengths are on the device, so the number of parts is
     // estimated from the items that the lanes and heads make, and bounded by the
     // table's width; where lengths are so uneven that it comes to far more, kAlone
     // bytes a part keep the loss small.
