@@ -380,7 +380,7 @@ spec_status spec_paged_store(const void *k, const void *v, int64_t tokens, int64
  * [0, pages) read as zero keys and values.
  * The scores and their sums are fp32; the weights w enter the second product
  * rounded to dtype, unnormalised; out is rounded once.  The sums' order follows
- * from the lengths and the device alone: equal calls give equal bits.
+ * from the lengths, the arguments and the device alone: equal calls give equal bits.
  * One launch: a grid of one CTA per SM, cooperative where items are shared by
  * several CTAs and their parts are not small.  Its waits are bounded. */
 spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,

@@ -28,7 +28,8 @@
 // ragged batches balance by themselves and a single long lane is split over
 // the whole GPU.  A CTA whose run starts or ends inside an item leaves its part
 // (m, sum, O) in the workspace; when its run is done it waits for the item's
-// other parts and joins its share of the item's elements, in the parts' order.  (The
+// other parts and joins its share of the item's elements, in an order of sums that
+// follows from the item and the CTA's place in it, not from timing.  (The
 // launch is cooperative, so all CTAs are there; runs are equal, so the wait is
 // short, and it is bounded.  One token of one head over 19,456 keys, 152 parts: 17 us;
 // 47 us with the last part's CTA joining alone -- 927 us for 128 rows of 256 --, 28 us with a
@@ -112,6 +113,8 @@ struct Join {
     int32_t first_cta;
     int32_t rows;          // of the item's row tiles, in use
     int32_t first, head, rt;
+    int32_t from, count;   // elements (16 columns of a row) this CTA joins: its share, or all if its part comes last
+    int32_t lg;            // log2 of the threads that share an element's parts, two of them each at least
 };
 
 // mbar_wait without the long suspension hint: the waits of this kernel's pipeline
@@ -674,7 +677,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         };
         uint32_t idx = 0;                                        // stage uses so far
         bool ok = true;
-        if (lane < 2) joins[lane].n = came_last[lane] = 0;
+        if (lane < 2) joins[lane].n = joins[lane].count = joins[lane].lg = came_last[lane] = 0;
         __syncwarp();
         for (uint32_t n = 0; ok; ++n) {
             Segment s;
@@ -728,6 +731,18 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 jn.n = run_owner(s.item0 + s.item_tiles - 1, plan.total, plan.grid) - jn.first_cta + 1;
                 jn.rows = (int32_t)(left < S::kRows ? left : S::kRows);
                 jn.first = s.ln.first; jn.head = s.head; jn.rt = s.rt;
+                const int all = jn.rows * (D / 16), sharers = a.share_joins ? jn.n : 1, mine = a.share_joins ? (int)blockIdx.x - jn.first_cta : 0;
+                jn.from = (int32_t)((uint32_t)(all * mine) / (uint32_t)sharers);
+                jn.count = (int32_t)((uint32_t)(all * (mine + 1)) / (uint32_t)sharers) - jn.from;
+                // The threads of an element order its sums, and so follow from the item
+                // alone -- whether this CTA comes last at an item, or at two, is timing -- or, in
+                // a shared join, from the two items that the CTA joins at once.
+                const bool both = a.share_joins && joins[0].n > 0 && joins[1].n > 0;
+                const int work = both ? joins[0].count + joins[1].count : jn.count, most = both ? max(joins[0].n, joins[1].n) : jn.n;
+                int lg = 0;
+                while (lg < 5 && (4 << lg) <= most && work << (lg + 1) <= S::kSoftmaxWarps * 32) ++lg;
+                jn.lg = lg;
+                if (both) joins[0].lg = lg;
             }
         }
         if (!ok) {
@@ -1144,26 +1159,17 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         }
         if (!stop && !a.share_joins && lane == 0 && warp < 2 && joins[warp].n > 0) failed = !wait(&bar.part_known[warp], 0);
         if (!stop && joins[0].n + joins[1].n > 0) stop = named_barrier_any(kAllSoftmax, kT, failed);
-        // this CTA's elements of both items, one after the other
-        int from[2], count[2];
-#pragma unroll
-        for (int sl = 0; sl < 2; ++sl) {
+        // this CTA's elements of both items; a warp's threads are all at one item
+        const int count0 = !stop && (a.share_joins || came_last[0]) ? joins[0].count : 0;
+        const int count1 = !stop && (a.share_joins || came_last[1]) ? joins[1].count : 0;
+        const int second = ((count0 << joins[0].lg) + 31) & ~31, work = second + (count1 << joins[1].lg);
+        for (int base = 0; base < work; base += kT) {
+            const int at = base + tid, sl = at < second ? 0 : 1;
             const Join &j = joins[sl];
-            from[sl] = count[sl] = 0;
-            if (stop || j.n == 0 || !(a.share_joins || came_last[sl])) continue;
-            const int all = j.rows * (D / 16), sharers = a.share_joins ? j.n : 1, mine = a.share_joins ? (int)blockIdx.x - j.first_cta : 0;
-            from[sl] = (int)((uint32_t)(all * mine) / (uint32_t)sharers);
-            count[sl] = (int)((uint32_t)(all * (mine + 1)) / (uint32_t)sharers) - from[sl];
-        }
-        const int work = count[0] + count[1], most = max(joins[0].n, joins[1].n);
-        int lg = 0;                                                // log2 of the threads of an element, two parts each at least
-        while (lg < 5 && (4 << lg) <= most && work << (lg + 1) <= kT) ++lg;
-        const int step = 1 << lg, p0 = tid & (step - 1);
-        for (int base = 0; base < work; base += kT >> lg) {
-            const int k = base + (tid >> lg), sl = k < count[0] ? 0 : 1;
-            const Join &j = joins[sl];
-            const int e = k < count[0] ? from[0] + k : from[1] + k - count[0], n = k < work ? j.n : 0;
-            const int g = k < work ? (int)((uint32_t)e / (uint32_t)j.rows) : 0, r = k < work ? e - g * j.rows : 0;   // columns 16 g on; over the item's row tiles
+            const int step = 1 << j.lg, p0 = tid & (step - 1), k = (sl ? at - second : at) >> j.lg;
+            const bool mine = k < (sl ? count1 : count0);
+            const int e = j.from + k, n = mine ? j.n : 0;
+            const int g = mine ? (int)((uint32_t)e / (uint32_t)j.rows) : 0, r = mine ? e - g * j.rows : 0;   // columns 16 g on; over the item's row tiles
             // the first part; the others are one slot on, then every second
             const float *first_part = a.parts + ((int64_t)j.first_cta * 2 + 1) * S::kPartFloats + (r >> 7) * 128 * (D + 2);
             float M = -INFINITY, L = 0.f, o[16];
