@@ -364,6 +364,8 @@ spec_status spec_paged_store(const void *k, const void *v, int64_t tokens, int64
  *             (16-byte aligned, strides non-negative multiples of 8), t < tokens;
  *   batch     block_table, cu_new, seq_lens, lanes, max_pages, page_size; row t of q belongs
  *             to the lane with cu_new[lane] <= t < cu_new[lane+1];
+ *   heads_q   a multiple of cache->heads; tokens * heads_q below 2^31, and
+ *             tokens * heads_q / 128 + min(tokens, lanes) * cache->heads below 2^23;
  *   scale     positive and finite, usually 1 / sqrt(head_dim);
  *   max_new   the longest chunk to expect (0: not known): a hint for the choice of tiles and
  *             of the launch; any value gives a right answer;

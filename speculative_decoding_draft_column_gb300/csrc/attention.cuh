@@ -61,6 +61,7 @@ namespace attn {
 constexpr float kLag = 8.f;      // log2 units the running maximum may lag
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kItemBit = 40;     // a step's tiles are counted below this bit of a word, its items above (the host checks that they fit)
 constexpr int kMaxSms = 512;     // counters at the start of the workspace: [2][kMaxSms]
 
 template <int D_, int QT_>
@@ -97,6 +98,7 @@ struct Args {
     const int32_t *block_table, *cu_new, *seq_lens;
     int64_t max_pages;
     int32_t lanes;
+    int32_t most_keys;     // what a lane's length is cut to, so that the step has at most 2^kItemBit tiles
     int32_t share_joins;   // the CTAs of an item share its join (a cooperative launch); else its last part's CTA does it
     float c;               // scale * log2(e)
     int64_t window;
@@ -373,9 +375,9 @@ __device__ __forceinline__ Lane lane_of(const Args &a, int l)
     const int32_t end = c1 < r.first ? r.first : c1 > t ? t : c1;
     r.n = end - r.first;
     // a lane cut by the buffer keeps its tokens' positions; a length that is no
-    // length (near 2^31) must not overflow the tiles' arithmetic
-    const int32_t seq = __ldg(a.seq_lens + l), most = 0x7FFF0000;
-    r.seq = (seq < 0 ? 0 : seq > most ? most : seq) - (c1 > end && r.n > 0 ? c1 - end : 0);
+    // length must not overflow the tiles' arithmetic
+    const int32_t seq = __ldg(a.seq_lens + l);
+    r.seq = (seq < 0 ? 0 : seq > a.most_keys ? a.most_keys : seq) - (c1 > end && r.n > 0 ? c1 - end : 0);
     return r;
 }
 
@@ -546,7 +548,6 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         const int per = (a.lanes + S::kThreads - 1) / S::kThreads;
         const int l0 = by_warp ? warp : min(tid * per, a.lanes), l1 = by_warp ? min(warp + 1, a.lanes) : min(l0 + per, a.lanes);
         // units in the low bits, items (a CTA of its own each, if there are enough) above
-        constexpr int kItemBit = 40;
         constexpr int64_t kUnits = (1ll << kItemBit) - 1;
         int64_t mine = 0, head = 0, incl;
         if (by_warp) {

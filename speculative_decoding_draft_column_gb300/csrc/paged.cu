@@ -317,6 +317,11 @@ spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q,
     if (heads_q < 1 || heads_q % c.heads != 0)
         return fail(SPEC_ERR_ARG, "heads_q = %d: need a positive multiple of the cache's %d heads", heads_q, c.heads);
     if ((int64_t)tokens * heads_q > INT32_MAX) return fail(SPEC_ERR_ARG, "tokens * heads_q exceeds 2^31-1");
+    // the items of the step at most: row tiles of 128 rows, a partial one for each head of a lane with tokens
+    const int64_t items = tokens * heads_q / 128 + (tokens < b.lanes ? tokens : b.lanes) * c.heads;
+    if (items >= 1ll << (63 - attn::kItemBit))
+        return fail(SPEC_ERR_ARG, "tokens, lanes and heads make up to %lld row tiles, need fewer than 2^%d", (long long)items,
+                    63 - attn::kItemBit);
     if (!(scale > 0.f) || !isfinite(scale)) return fail(SPEC_ERR_ARG, "scale = %g: must be positive and finite", scale);
     if (window < 0) return fail(SPEC_ERR_ARG, "window = %lld < 0", (long long)window);
     if (max_new < 0) return fail(SPEC_ERR_ARG, "max_new = %lld < 0", (long long)max_new);
@@ -350,6 +355,9 @@ spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q,
     a.group_magic = (uint32_t)((((1ull << a.group_shift) - a.group) << 32) / a.group + 1);
     a.block_table = b.block_table; a.cu_new = b.cu_new; a.seq_lens = b.seq_lens;
     a.lanes = (int32_t)b.lanes; a.max_pages = b.max_pages;
+    // (of tiles of 64 keys, the smaller; 2^31 - 2^16 unless there are 2^15 items)
+    const int64_t tiles = (1ll << attn::kItemBit) / items - 2;
+    a.most_keys = (int32_t)(tiles < (0x7FFF0000 >> 6) ? tiles << 6 : 0x7FFF0000);
     a.c = scale * attn::kLog2e; a.window = window;
     a.out = static_cast<uint16_t *>(out); a.lse = lse;
     a.counters = static_cast<unsigned int *>(workspace);
