@@ -304,7 +304,7 @@ typedef struct {
     int64_t k_strides[3], v_strides[3];
     int64_t pages;          /* 1 .. 2^31-1 */
     int32_t page_size;      /* tokens a page, >= 1 (attention: a power of two >= 8) */
-    int32_t heads;          /* key/value heads, >= 1 */
+    int32_t heads;          /* key/value heads, >= 1; heads * head_dim below 2^31 */
     int32_t head_dim;       /* a multiple of 8, at most 256 (attention: 64, 128 or 256) */
     int32_t dtype;          /* SPEC_BF16 or SPEC_F16 */
 } spec_paged_cache;

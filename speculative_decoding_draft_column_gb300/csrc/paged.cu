@@ -143,6 +143,8 @@ spec_status check_cache(const spec_paged_cache *c)
     if (c->heads < 1) return fail(SPEC_ERR_ARG, "cache: heads = %d < 1", c->heads);
     if (c->head_dim < 8 || c->head_dim > 256 || c->head_dim % 8 != 0)
         return fail(SPEC_ERR_ARG, "cache: head_dim = %d, need a multiple of 8 up to 256", c->head_dim);
+    if ((int64_t)c->heads * c->head_dim > INT32_MAX)
+        return fail(SPEC_ERR_ARG, "cache: heads * head_dim = %lld exceeds 2^31-1", (long long)c->heads * c->head_dim);
     for (int i = 0; i < 3; ++i)
         if (bad_stride(c->k_strides[i]) || bad_stride(c->v_strides[i]))
             return fail(SPEC_ERR_ARG, "cache: strides must be non-negative multiples of 8 elements below 2^39");

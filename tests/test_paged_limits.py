@@ -67,3 +67,12 @@ def test_plan_of_the_runs_cannot_overflow():
     for bound in (1, 1 << 14, 1 << 15, (1 << 23) - 1):
         tiles = min(0x7FFF0000 >> 6, (1 << 40) // bound - 2)
         assert tiles >= 1 << 16 and bound * (tiles + 1) < 1 << 40
+
+
+def test_cache_rows_of_too_many_elements(sd):
+    for heads, dim in ((1 << 28, 8), (1 << 25, 64), ((1 << 31) - 1, 256)):
+        c = ctypes.byref(_cache(sd, heads, dim))
+        assert sd.lib.spec_paged_store(P, P, 4, 128, 64, 128, 64, P, c) == sd.SPEC_ERR_ARG
+        assert "heads * head_dim" in sd.spec_last_error()
+    assert sd.lib.spec_paged_store(P, P, 4, 128, 64, 128, 64, None, ctypes.byref(_cache(sd, (1 << 25) - 1))) == sd.SPEC_ERR_ARG
+    assert "null pointer" in sd.spec_last_error()
