@@ -411,6 +411,8 @@ int64_t spec_paged_attention_workspace(void);
  *                equal ids of a lane add up, in their order, in fp32;
  *   mask         uint32 [mask_count][(V+31)/32]: bit t%32 of word t/32 set: t is allowed; mask_rows int32
  *                [lanes*cols]: the column's row of mask, outside [0, mask_count): no mask; or both NULL.
+ * A table of no entries may be NULL (history with history_stride 0, bias_ids and bias_vals with
+ * max_bias 0, mask with mask_count 0, while their lengths or rows are given).
  * Ids outside [0, V) are ignored.  out may be logits itself (in place), and
  * must not overlap it otherwise.  1 <= cols <= SPEC_MAX_GAMMA + 1. */
 spec_status spec_logits_process(const uint16_t *logits, int64_t lanes, int32_t cols, int64_t V,

@@ -388,11 +388,13 @@ spec_status spec_logits_process(const uint16_t *logits, int64_t lanes, int32_t c
         return fail(SPEC_ERR_ARG, "history_stride, max_bias and mask_count must not be negative");
     if (lanes == 0) return SPEC_OK;
     if (!logits || !out) return fail(SPEC_ERR_ARG, "null pointer");
-    if (!!history != !!prompt_lens || !!history != !!history_lens)
+    // (a table of no entries has no address: with its lengths or rows it is a rule that changes nothing)
+    if (!!prompt_lens != !!history_lens || (history_stride > 0 ? !!history != !!prompt_lens : history && !prompt_lens))
         return fail(SPEC_ERR_ARG, "history, prompt_lens and history_lens go together");
-    if (!!bias_ids != !!bias_vals || !!bias_ids != !!bias_lens)
+    if (max_bias > 0 ? !!bias_ids != !!bias_vals || !!bias_ids != !!bias_lens : (bias_ids || bias_vals) && !bias_lens)
         return fail(SPEC_ERR_ARG, "bias_ids, bias_vals and bias_lens go together");
-    if (!!mask != !!mask_rows) return fail(SPEC_ERR_ARG, "mask and mask_rows go together");
+    if (mask_count > 0 ? !!mask != !!mask_rows : mask && !mask_rows)
+        return fail(SPEC_ERR_ARG, "mask and mask_rows go together");
     if (misaligned(logits, 2) || misaligned(out, 2)) return fail(SPEC_ERR_ARG, "misaligned pointer (logits need 2 bytes)");
     const void *words[] = {history, prompt_lens, history_lens, drafts, penalties, bias_ids, bias_vals, bias_lens, mask, mask_rows};
     for (const void *p : words)

@@ -260,7 +260,8 @@ def spec_logits_process(logits, lanes, cols, V, out, *, history=None, prompt_len
                         drafts=None, penalties=None, bias_ids=None, bias_vals=None, bias_lens=None, mask=None,
                         mask_rows=None):
     """Penalties, biases and grammar masks on bf16 logits [lanes*cols, V] into
-    ``out`` (which may be ``logits``); every rule's tensors may be left out."""
+    ``out`` (which may be ``logits``); every rule's tensors may be left out, and
+    its tables may have no entries (a history [lanes, 0], say)."""
     t = _torch()
     i32, f32 = t.int32, t.float32
     ln, cs, vs = _n(lanes), _n(cols), _n(V)
@@ -271,6 +272,12 @@ def spec_logits_process(logits, lanes, cols, V, out, *, history=None, prompt_len
     dev = t.cuda.current_device()
     lg = None if logits is None else _array(logits, logits.dtype, n, dev, "logits")
     o = None if out is None else _array(out, out.dtype, n, dev, "out")
+    if (history is None) != (prompt_lens is None) or (history is None) != (history_lens is None):
+        _bad("history, prompt_lens and history_lens go together")
+    if (bias_ids is None) != (bias_vals is None) or (bias_ids is None) != (bias_lens is None):
+        _bad("bias_ids, bias_vals and bias_lens go together")
+    if (mask is None) != (mask_rows is None):
+        _bad("mask and mask_rows go together")
     hs = nb = rows = 0
     h = pl = hl = d = pen = bi = bv = bl = m = mr = None
     if history is not None:
