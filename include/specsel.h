@@ -337,9 +337,10 @@ typedef struct {
  *              int32 [1], the pages of the list used up before (NULL: 0).
  * When the list runs out, lanes take what is left in order, and tokens without
  * a page get slot -1; nothing is read or written out of range, and info tells.
- * Outputs must not alias inputs (keep two held and info buffers and swap them
- * from step to step); block_table is updated in place, only at entries the
- * step adds, so repeating a call repeats its results.
+ * Outputs must not overlap inputs, and are refused where they do (keep two held
+ * buffers and swap them from step to step; copy the next cursor out of info);
+ * block_table is updated in place, only at entries the step adds, so repeating
+ * a call repeats its results.
  * One launch.  lanes == 0 still writes cu_new[0], the padding and info. */
 spec_status spec_paged_plan(const spec_paged_batch *batch, const int32_t *free_pages, int64_t num_free,
                             const int32_t *cursor);

@@ -106,6 +106,18 @@ spec_status device(Device **out)
 
 bool misaligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
+// A call's buffer, for the checks of what must not overlap.
+struct Range {
+    const void *p;
+    int64_t bytes;
+    const char *name;
+};
+bool overlap(const Range &a, const Range &b)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + (uint64_t)b.bytes && y < x + (uint64_t)a.bytes;
+}
+
 constexpr int64_t kMaxStride = 1ll << 39;
 
 bool bad_stride(int64_t s) { return s < 0 || s >= kMaxStride || s % 8 != 0; }
@@ -249,8 +261,16 @@ spec_status spec_paged_plan(const spec_paged_batch *batch, const int32_t *free_p
     for (const void *p : words)
         if (misaligned(p, 4)) return fail(SPEC_ERR_ARG, "misaligned pointer (int32 arrays need 4 bytes)");
     if (misaligned(b.slots, 8)) return fail(SPEC_ERR_ARG, "misaligned pointer (slots need 8 bytes)");
-    if (b.lanes > 0 && (b.held == b.held_out || b.context_lens == b.seq_lens))
-        return fail(SPEC_ERR_ARG, "outputs must not alias inputs (held_out and held, seq_lens and context_lens)");
+    // every CTA reads the inputs while others write the outputs
+    const int64_t l4 = b.lanes * 4, t4 = b.tokens < INT64_MAX / 8 ? b.tokens * 4 : INT64_MAX / 2;
+    const Range in[] = {{b.context_lens, l4, "context_lens"}, {b.new_lens, l4, "new_lens"}, {b.held, l4, "held"},
+                        {free_pages, num_free * 4, "free_pages"}, {cursor, 4, "cursor"}};
+    const Range out[] = {{b.info, 16, "info"}, {b.held_out, l4, "held_out"}, {b.seq_lens, l4, "seq_lens"},
+                         {b.cu_new, l4 + 4, "cu_new"}, {b.positions, t4, "positions"}, {b.slots, 2 * t4, "slots"},
+                         {b.block_table, l4 * b.max_pages, "block_table"}};
+    for (const Range &o : out)
+        for (const Range &i : in)
+            if (overlap(o, i)) return fail(SPEC_ERR_ARG, "outputs must not alias inputs (%s and %s)", o.name, i.name);
     Device *d = nullptr;
     st = device(&d);
     if (st != SPEC_OK) return st;

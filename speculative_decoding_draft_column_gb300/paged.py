@@ -193,7 +193,9 @@ class PagedBatch:
 
 def spec_paged_plan(batch, free_pages, cursor=None):
     """Plan a step into the batch's buffers; ``free_pages`` int32, ``cursor``
-    int32 [1] (the pages of the list used before) or None."""
+    int32 [1] (the pages of the list used before) or None.  The call writes the
+    next step's cursor to ``batch.info[1]``: copy it from there, since a cursor
+    inside ``info`` would be written while it is read, and is refused."""
     if not batch.plannable:
         _bad("batch: made without the plan's buffers")
     i32 = _torch().int32
