@@ -371,7 +371,8 @@ spec_status spec_paged_store(const void *k, const void *v, int64_t tokens, int64
  *   max_new   the longest chunk to expect (0: not known): a hint for the choice of tiles and
  *             of the launch; any value gives a right answer;
  *   out       cache->dtype, contiguous [tokens][heads_q][head_dim], 16-byte aligned;
- *   lse       fp32 [tokens][heads_q], or NULL; out and lse must not overlap what the call reads;
+ *   lse       fp32 [tokens][heads_q], or NULL; out and lse must not overlap what the call reads, nor
+ *             each other (refused but for the cache, whose pages are scattered);
  *   workspace device, 16-byte aligned, spec_paged_attention_workspace() bytes, zeroed once before
  *             its first use (and after a wait that gave up, which spec_device_status reports);
  *             calls that may overlap on the GPU need one each.

@@ -7,6 +7,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "specsel.h"
@@ -354,13 +355,22 @@ spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q,
     if (misaligned(q, 16) || misaligned(out, 16) || misaligned(workspace, 16) || misaligned(lse, 4) ||
         misaligned(b.block_table, 4) || misaligned(b.cu_new, 4) || misaligned(b.seq_lens, 4))
         return fail(SPEC_ERR_ARG, "misaligned pointer (q, out and workspace need 16 bytes, int32 and lse 4)");
-    const char *q0 = static_cast<const char *>(q), *out0 = static_cast<const char *>(out);
-    if (q0 >= out0 && q0 < out0 + tokens * heads_q * c.head_dim * 2) return fail(SPEC_ERR_ARG, "out overlaps q");
+    // from q's first element to its last, whatever lies between its rows
+    const __int128 span = ((__int128)(tokens - 1) * q_token_stride + (__int128)(heads_q - 1) * q_head_stride + c.head_dim) * 2;
+    const Range in[] = {{q, span < INT64_MAX ? (int64_t)span : INT64_MAX, "q"}, {b.block_table, b.lanes * b.max_pages * 4, "block_table"},
+                        {b.cu_new, (b.lanes + 1) * 4, "cu_new"}, {b.seq_lens, b.lanes * 4, "seq_lens"}};
+    const Range o = {out, tokens * heads_q * c.head_dim * 2, "out"}, ls = {lse, tokens * heads_q * 4, "lse"};
+    for (const Range &i : in)
+        for (const Range *w : {&o, &ls})
+            if (overlap(*w, i)) return fail(SPEC_ERR_ARG, "%s overlaps %s", w->name, i.name);
+    if (overlap(o, ls)) return fail(SPEC_ERR_ARG, "out overlaps lse");
     const int64_t need = spec_paged_attention_workspace();
     if (need < 0) return (spec_status)need;
     if (workspace_bytes < need)
         return fail(SPEC_ERR_ARG, "workspace: %lld bytes, the call needs %lld", (long long)workspace_bytes,
                     (long long)need);
+    if (overlap(o, {workspace, need, ""}) || overlap(ls, {workspace, need, ""}))
+        return fail(SPEC_ERR_ARG, "out or lse overlaps workspace");
     Device *d = nullptr;
     st = device(&d);
     if (st != SPEC_OK) return st;

@@ -50,3 +50,44 @@ def test_plan_outputs_over_inputs(sd, out, inp):
     for where in (at + SIZE[inp] - 4, at - SIZE[out] + step):
         where = where // step * step
         _refused(sd, _plan(sd, **{out: where}), "alias", out)
+
+
+# where each buffer of an attention call lies: 4 tokens of 6 heads of 64 (3,072 bytes), tables of 3 lanes
+Q, OUT, LSE, TABLE, CU, SEQ, WS, WS_BYTES = 0x200000, 0x210000, 0x220000, 0x230000, 0x240000, 0x250000, 0x1000000, 1 << 40
+
+
+def _attend(sd, q=Q, out=OUT, lse=LSE, table=TABLE, cu=CU, seq=SEQ, ws=WS, token_stride=6 * 64, head_stride=64, tokens=4):
+    three = ctypes.c_int64 * 3
+    c = sd.paged._CacheStruct(0x300000, 0x400000, three(2048, 128, 64), three(2048, 128, 64), 10, 16, 2, 64, sd.SPEC_BF16)
+    b = sd.paged._BatchStruct(block_table=table, cu_new=cu, seq_lens=seq, lanes=3, max_pages=8, page_size=16)
+    return sd.lib.spec_paged_attention(q, tokens, 6, token_stride, head_stride, ctypes.byref(c), ctypes.byref(b), 0.1, 0, 0, out,
+                                       lse, ws, WS_BYTES)
+
+
+@pytest.mark.parametrize("at", [-3_072 + 16, -16, 0, 16, 3_072 - 16])
+def test_out_over_queries(sd, at):
+    """Wherever out begins: before q's first element, at it, or among its rows."""
+    _refused(sd, _attend(sd, out=Q + at), "out overlaps q")
+
+
+def test_out_over_strided_queries(sd):
+    """Queries whose rows lie apart: up to the last row's last element."""
+    last = 3 * 18 * 64 + 5 * 64 + 64
+    for at in (0, 6 * 64 * 2, (last - 8) * 2):
+        _refused(sd, _attend(sd, out=Q + at, token_stride=18 * 64), "out overlaps q")
+        _refused(sd, _attend(sd, lse=Q + at, token_stride=18 * 64), "lse overlaps q")
+    # strides whose product is past 64 bits are no way round the check
+    _refused(sd, _attend(sd, out=Q + (1 << 30), token_stride=(1 << 39) - 8, tokens=1 << 27), "out overlaps q")
+
+
+@pytest.mark.parametrize("name,size", [("table", 3 * 8 * 4), ("cu", 16), ("seq", 12)])
+def test_results_over_what_is_read(sd, name, size):
+    at = dict(table=TABLE, cu=CU, seq=SEQ)[name]
+    for where in (at, at + size - 4, at - 32):
+        _refused(sd, _attend(sd, lse=where), "lse overlaps")
+        _refused(sd, _attend(sd, out=where // 16 * 16), "out overlaps")
+
+
+def test_results_over_each_other(sd):
+    for at in (-92, 0, 3_072 - 4):
+        _refused(sd, _attend(sd, lse=OUT + at), "out overlaps lse")
