@@ -383,7 +383,8 @@ spec_status spec_paged_store(const void *k, const void *v, int64_t tokens, int64
  * matter; values at positions inside seq_len must be finite.  Table entries outside
  * [0, pages) read as zero keys and values.
  * The scores and their sums are fp32; the weights w enter the second product
- * rounded to dtype, unnormalised; out is rounded once.  The sums' order follows
+ * rounded to dtype, unnormalised (in fp16 the largest as 2^7 or more, so that a long
+ * context's small weights still count); out is rounded once.  The sums' order follows
  * from the lengths, the arguments and the device alone: equal calls give equal bits.
  * One launch: a grid of one CTA per SM, cooperative where items are shared by
  * several CTAs and their parts are not small.  Its waits are bounded. */

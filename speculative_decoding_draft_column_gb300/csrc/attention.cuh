@@ -10,9 +10,14 @@
 // thread owns one row.
 //
 // The running maximum m is a reference, not the exact maximum: it moves only
-// when a tile exceeds it by more than 2^8 (kLag), and only then O and the sum
-// are rescaled.  P stays below 2^8, where its 16-bit rounding is as relative
-// as below 1, and the sum is kept in fp32 either way.
+// when a tile exceeds it by more than 2^8 (kLag; 2^4 in fp16), and only then O and the sum
+// are rescaled.  A bf16 weight rounds relative to itself at any size.  An fp16 one does
+// from 2^-14 on and is lost below 2^-25, while a long context's weights may add up
+// to something at 2^-25 of the largest each; so fp16's reference lies 2^7 below the
+// maximum (kRaise): the largest weight is 2^7 .. 2^11, and the others round relative to
+// themselves down to 2^-21 of it, to 2^-32 of it below that.  (Above 2^11 there is
+// room up to fp16's 65,504 for what fp32 leaves open between a score and the maximum it was
+// compared with: 2^4 where scores reach 2^27.)  The sum is kept in fp32, of unrounded weights.
 //
 // Two streams hide the softmax of one behind the products of the other: with
 // two row tiles in a CTA (QT = 2, chunks) each stream has its rows and both
@@ -58,7 +63,10 @@
 
 namespace attn {
 
-constexpr float kLag = 8.f;      // log2 units the running maximum may lag
+template <bool F16>
+constexpr float kLag = F16 ? 4.f : 8.f;     // log2 units the running maximum may lag
+template <bool F16>
+constexpr float kRaise = F16 ? 7.f : 0.f;   // log2 units of the reference below the maximum it was taken from
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kItemBit = 40;     // a step's tiles are counted below this bit of a word, its items above (the host checks that they fit)
@@ -960,10 +968,10 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     named_barrier(pair, 64);
                     top = fmaxf(top, mx[(half ^ 1) * 128]);
                     // a new reference only past the lag (or for a row's first key)
-                    const bool move = valid && (top > m + kLag || (m == -INFINITY && top > -INFINITY));
+                    const bool move = valid && (top > m + (kLag<F16> + kRaise<F16>) || (m == -INFINITY && top > -INFINITY));
                     if (__any_sync(kFull, move)) {
-                        const float f = move ? exp2_fast(m - top) : 1.f;
-                        if (move) m = top;
+                        const float to = top - kRaise<F16>, f = move ? exp2_fast(m - to) : 1.f;
+                        if (move) m = to;
                         l *= f;
                         if (i > 0) {
                             wait(&bar.o_done[st], (pv_n - 1) & 1);
