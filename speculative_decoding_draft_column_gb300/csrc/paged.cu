@@ -188,20 +188,25 @@ spec_status launch_attention(const Device &d, const attn::Args &a, int64_t chunk
     const dim3 grid((unsigned)attention_grid(d));
     const size_t smem = (size_t)d.attn_smem[shape_index<D, QT>()][f16];
     // Whether an item's parts are joined by all its CTAs (a cooperative launch) or
-    // by the last part's CTA alone (an ordinary one: 3 us less a call in a
-    // stream; one token at 1,013 keys 12.7 against 16.4 us, 64 lanes of up to 16
-    // tokens at 6,000 keys 27.0 against 30.8, 8 lanes of 8 at 500-16,000 keys 65.7
-    // against 68.8).  Alone, a CTA joins 128 KB in 2 us.  The lengths are on the device, so the number of parts is
-    // estimated from the items that the lanes and heads make, and bounded by the
-    // table's width; where lengths are so uneven that it comes to far more, kAlone
-    // bytes a part keep the loss small.
-    constexpr int64_t kAlone = 32 << 10, kAloneAll = 128 << 10;
+    // by the last part's CTA alone (an ordinary one: 2-4 us less a call in a
+    // stream, 1 in a graph; 8 lanes of 8 tokens at 8,000 keys 51.8 against 55.3 us, 64 lanes of
+    // 16 tokens at 3,000 keys 30.8 against 34.8, 8 lanes of a token at 2,000 keys of one head
+    // 12.0 against 14.4).  The lengths are on the device, so the number of parts is
+    // estimated twice: from the items that the lanes and heads make if they are
+    // even, and from one lane having all the keys (the others short, or without tokens, as in
+    // a padded batch), whose heads then share the GPU.  Both are bounded by the table's
+    // width and the window.  Alone, a CTA joins the even case's 128 KB in 2 us.  Of 64 lanes
+    // of 4 tokens, one with 60,000 keys, it takes 29.4 against 20.5 us in a stream where that lane has
+    // one head (152 parts of 8 KB), 26.6 against 23.5 where it has two (76 parts); of 64 lanes
+    // of 16 tokens, one with 131,072 keys of one head (152 parts of 32 KB), 66 against 24 in a graph.
+    constexpr int64_t kAlone = 32 << 10, kAloneAll = 128 << 10, kAloneWorst = 1 << 20, kAloneParts = 96;
     attn::Args b = a;
     const int64_t ctas = grid.x, rows = chunk * a.group < S::kRows ? chunk * a.group : S::kRows;
-    const int64_t widest = ((a.max_pages << a.log_page) / S::BK + 2) / S::kLeast + 2;
-    const int64_t items = (int64_t)a.lanes * a.heads_kv, likely = ctas / items + 2;
-    const int64_t parts = widest < likely ? widest : likely, part = rows * D * 4;
-    b.share_joins = part > kAlone || parts * part > kAloneAll;
+    const int64_t table = a.max_pages << a.log_page, seen = a.window + S::kRows / a.group + 2;
+    const int64_t widest = ((a.window > 0 && seen < table ? seen : table) / S::BK + 2) / S::kLeast + 2;
+    const int64_t items = (int64_t)a.lanes * a.heads_kv, likely = ctas / items + 2, one = ctas / a.heads_kv + 2;
+    const int64_t parts = widest < likely ? widest : likely, worst = widest < one ? widest : one, part = rows * D * 4;
+    b.share_joins = part > kAlone || parts * part > kAloneAll || worst * part > kAloneWorst || worst > kAloneParts;
     if (b.share_joins)   // CTAs wait for one another's parts
         return f16 ? launch<true>(attn::attention_kernel<D, QT, true>, grid, S::kThreads, smem, b)
                    : launch<true>(attn::attention_kernel<D, QT, false>, grid, S::kThreads, smem, b);

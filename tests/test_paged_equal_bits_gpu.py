@@ -41,7 +41,9 @@ def _step(sd, new, ctx, hk, group, dim, ps, seed=0):
 @pytest.mark.parametrize("cold", [False, True])
 @pytest.mark.parametrize("dim,lanes,new,hk,group,tiles", [
     (64, 20, 1, 1, 8, 12), (64, 40, 8, 1, 4, 30), (64, 20, 4, 1, 4, 30), (128, 40, 1, 1, 8, 30), (128, 20, 1, 2, 4, 12),
-    (128, 40, 4, 1, 4, 4), (128, 40, 8, 1, 4, 12), (256, 40, 1, 1, 8, 4), (256, 20, 1, 2, 4, 12)])
+    (128, 40, 4, 1, 4, 4), (128, 40, 8, 1, 4, 12), (256, 40, 1, 1, 8, 4), (256, 20, 1, 2, 4, 12),
+    # narrower tables, for which the last CTA joins alone
+    (64, 40, 8, 1, 4, 12), (64, 20, 4, 1, 4, 12), (64, 40, 4, 1, 4, 12), (128, 40, 1, 1, 8, 12)])
 def test_ragged_lanes_repeat(sd, dim, lanes, new, hk, group, tiles, cold):
     """Lanes long and short in turn, whose items go to two to a dozen CTAs and
     are joined by the one that comes last: its other item has another number of
