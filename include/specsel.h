@@ -293,6 +293,7 @@ spec_status spec_shortlist_topk(const uint16_t *hidden, int64_t cols, int64_t d,
 #define SPEC_BF16 0
 #define SPEC_F16 1
 #define SPEC_PAGED_MAX_LANES 4096
+#define SPEC_PAGED_WORKSPACE_ZEROED 4096   /* bytes at the start of an attention workspace that are zero between calls */
 
 /* Keys and values of one layer: element (page, token, head, i) of k lies at
  * k + page*k_strides[0] + token*k_strides[1] + head*k_strides[2] + i (strides in
@@ -373,8 +374,9 @@ spec_status spec_paged_store(const void *k, const void *v, int64_t tokens, int64
  *   out       cache->dtype, contiguous [tokens][heads_q][head_dim], 16-byte aligned;
  *   lse       fp32 [tokens][heads_q], or NULL; out and lse must not overlap what the call reads, nor
  *             each other (refused but for the cache, whose pages are scattered);
- *   workspace device, 16-byte aligned, spec_paged_attention_workspace() bytes, zeroed once before
- *             its first use (and after a wait that gave up, which spec_device_status reports);
+ *   workspace device, 16-byte aligned, spec_paged_attention_workspace() bytes, the first
+ *             SPEC_PAGED_WORKSPACE_ZEROED of them zeroed once before its first use (and after a
+ *             wait that gave up, which spec_device_status reports); the others may hold anything;
  *             calls that may overlap on the GPU need one each.
  * Rows of q past cu_new[lanes] are left alone.  A row with no key in reach (a
  * seq_len below the chunk) gets out = 0 and lse = -inf; a row whose scores are

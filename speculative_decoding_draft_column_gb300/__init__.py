@@ -31,7 +31,7 @@ __all__ = [
     "spec_set_stream", "spec_get_stream", "spec_reserve", "spec_release", "spec_last_error",
     "spec_launch_count", "spec_device_status", "topk", "topk_mapped", "verify", "round_step", "EXPORTS",
     "spec_shortlist_pack", "spec_shortlist_logits", "spec_shortlist_topk",
-    "SPEC_BF16", "SPEC_F16", "SPEC_PAGED_MAX_LANES", "PagedCache", "PagedBatch", "spec_paged_plan", "spec_paged_store",
+    "SPEC_BF16", "SPEC_F16", "SPEC_PAGED_MAX_LANES", "SPEC_PAGED_WORKSPACE_ZEROED", "PagedCache", "PagedBatch", "spec_paged_plan", "spec_paged_store",
     "spec_paged_attention", "spec_paged_attention_workspace", "new_attention_workspace", "spec_logits_process",
     "paged_attention", "process_logits",
 ]
@@ -431,6 +431,6 @@ def round_step(draft_logits, k: int, target_logits, drafts):
 
 # the paged cache and the logits rules (they use the checks above)
 from .paged import (  # noqa: E402
-    SPEC_BF16, SPEC_F16, SPEC_PAGED_MAX_LANES, PagedBatch, PagedCache, new_attention_workspace, paged_attention,
-    process_logits, spec_logits_process, spec_paged_attention, spec_paged_attention_workspace, spec_paged_plan,
-    spec_paged_store)
+    SPEC_BF16, SPEC_F16, SPEC_PAGED_MAX_LANES, SPEC_PAGED_WORKSPACE_ZEROED, PagedBatch, PagedCache,
+    new_attention_workspace, paged_attention, process_logits, spec_logits_process, spec_paged_attention,
+    spec_paged_attention_workspace, spec_paged_plan, spec_paged_store)

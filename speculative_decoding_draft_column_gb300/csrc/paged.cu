@@ -178,6 +178,8 @@ spec_status check_batch(const spec_paged_batch *b)
 constexpr int64_t max2(int64_t a, int64_t b) { return a > b ? a : b; }
 constexpr int64_t kPartFloats = max2(attn::Shape<128, 2>::kPartFloats, attn::Shape<256, 1>::kPartFloats);
 
+static_assert(SPEC_PAGED_WORKSPACE_ZEROED == 2 * attn::kMaxSms * sizeof(unsigned int), "the counters");
+
 int attention_grid(const Device &d) { return d.sms < attn::kMaxSms ? d.sms : attn::kMaxSms; }
 
 template <int D, int QT>
@@ -321,7 +323,7 @@ int64_t spec_paged_attention_workspace(void)
     Device *d = nullptr;
     const spec_status st = device(&d);
     if (st != SPEC_OK) return st;
-    return 2 * (int64_t)attn::kMaxSms * 4 + (int64_t)attention_grid(*d) * 2 * kPartFloats * 4;
+    return SPEC_PAGED_WORKSPACE_ZEROED + (int64_t)attention_grid(*d) * 2 * kPartFloats * 4;
 }
 
 spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
@@ -398,7 +400,7 @@ spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q,
     a.c = scale * attn::kLog2e; a.window = window;
     a.out = static_cast<uint16_t *>(out); a.lse = lse;
     a.counters = static_cast<unsigned int *>(workspace);
-    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + 2 * attn::kMaxSms * 4);
+    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + SPEC_PAGED_WORKSPACE_ZEROED);
     const int64_t hint = max_new < tokens ? max_new : tokens, chunk = hint > 0 ? hint : (tokens + b.lanes - 1) / b.lanes;
     const bool two = chunk * a.group > 128;   // more rows than one tile: two tiles share every K/V tile
     const bool f16 = c.dtype == SPEC_F16;

@@ -13,7 +13,7 @@ import ctypes
 from . import SPEC_ERR_ARG, SpecError, _check, _n, lib
 
 SPEC_BF16, SPEC_F16 = 0, 1
-SPEC_PAGED_MAX_LANES = 4096
+SPEC_PAGED_MAX_LANES, SPEC_PAGED_WORKSPACE_ZEROED = 4096, 4096
 
 _p, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 
@@ -231,10 +231,12 @@ def spec_paged_attention_workspace() -> int:
 
 
 def new_attention_workspace(device="cuda"):
-    """A zeroed workspace for spec_paged_attention (one per stream that may run it)."""
+    """A workspace for spec_paged_attention (one per stream that may run it), its counters zeroed."""
     import torch
     with torch.cuda.device(device):
-        return torch.zeros(spec_paged_attention_workspace(), dtype=torch.uint8, device=device)
+        ws = torch.empty(spec_paged_attention_workspace(), dtype=torch.uint8, device=device)
+        ws[:SPEC_PAGED_WORKSPACE_ZEROED].zero_()
+        return ws
 
 
 def spec_paged_attention(q, cache, batch, scale, out, lse, workspace, window=0, max_new=0):
@@ -317,7 +319,8 @@ def spec_logits_process(logits, lanes, cols, V, out, *, history=None, prompt_len
 # ---- allocating conveniences ------------------------------------------------
 
 def paged_attention(q, cache, batch, scale=None, window=0, max_new=0, workspace=None):
-    """(out, lse) of spec_paged_attention; a fresh workspace unless one is given."""
+    """(out, lse) of spec_paged_attention; a fresh workspace unless one is given.
+    Rows past the step's tokens are not written and hold anything."""
     import torch
     out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
