@@ -315,7 +315,7 @@ typedef struct {
  * there).  All device memory of the caller, int32 unless noted. */
 typedef struct {
     const int32_t *context_lens;   /* [lanes] tokens already cached (negative: 0) */
-    const int32_t *new_lens;       /* [lanes] new tokens of this step, 0 allowed (negative: 0) */
+    const int32_t *new_lens;       /* [lanes] new tokens of this step, 0 allowed (negative: 0); context + new below 2^31 */
     const int32_t *held;           /* [lanes] pages the lane's table row holds already */
     int32_t *block_table;          /* [lanes][max_pages] page of each page_size tokens; rows are contiguous */
     int32_t *cu_new;               /* [lanes+1] where each lane's new tokens start; the last is their total */
@@ -350,7 +350,7 @@ spec_status spec_paged_plan(const spec_paged_batch *batch, const int32_t *free_p
  * k + t*k_token_stride + head*k_head_stride + i; 16-byte aligned, strides
  * non-negative multiples of 8 elements) go to slot slots[t] of the cache.
  * Tokens whose slot lies outside [0, pages*page_size) are skipped.  Two tokens
- * must not share a slot. */
+ * must not share a slot, nor k and v lie in slots that are stored to. */
 spec_status spec_paged_store(const void *k, const void *v, int64_t tokens, int64_t k_token_stride,
                              int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
                              const int64_t *slots, const spec_paged_cache *cache);
@@ -411,7 +411,7 @@ int64_t spec_paged_attention_workspace(void);
  *                those up to history_lens[l] the output (lengths are cut to the stride);
  *                NULL (with both lengths): no history;
  *   drafts       int32 [lanes][cols-1], or NULL: no drafts counted;
- *   penalties    fp32 [lanes][3]: r > 0 (1: none), f, p; or NULL: none;
+ *   penalties    fp32 [lanes][3]: r > 0 and no subnormal (1: none), f, p; or NULL: none;
  *   bias_ids, bias_vals   int32, fp32 [lanes][max_bias], the first bias_lens[l] in use; or all NULL;
  *                equal ids of a lane add up, in their order, in fp32;
  *   mask         uint32 [mask_count][(V+31)/32]: bit t%32 of word t/32 set: t is allowed; mask_rows int32
@@ -419,7 +419,7 @@ int64_t spec_paged_attention_workspace(void);
  * A table of no entries may be NULL (history with history_stride 0, bias_ids and bias_vals with
  * max_bias 0, mask with mask_count 0, while their lengths or rows are given).
  * Ids outside [0, V) are ignored.  out may be logits itself (in place), and
- * must not overlap it otherwise.  1 <= cols <= SPEC_MAX_GAMMA + 1. */
+ * must not overlap it otherwise, nor the rules' tables.  1 <= cols <= SPEC_MAX_GAMMA + 1. */
 spec_status spec_logits_process(const uint16_t *logits, int64_t lanes, int32_t cols, int64_t V,
                                 const int32_t *history, int64_t history_stride, const int32_t *prompt_lens,
                                 const int32_t *history_lens, const int32_t *drafts, const float *penalties,

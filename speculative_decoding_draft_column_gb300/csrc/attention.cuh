@@ -36,21 +36,21 @@
 // other parts and joins its share of the item's elements, in an order of sums that
 // follows from the item and the CTA's place in it, not from timing.  (The
 // launch is cooperative, so all CTAs are there; runs are equal, so the wait is
-// short, and it is bounded.  One token of one head over 19,456 keys, 152 parts: 17 us;
-// 47 us with the last part's CTA joining alone -- 927 us for 128 rows of 256 --, 28 us with a
-// second kernel, which costs every call 4 us.)  Where the parts of an item are small,
+// short, and it is bounded.  Items in 152 parts, in a graph: one token of one head of 128 over
+// 38,912 keys 16 us, 24 with the last part's CTA joining alone; 128 rows of 256 over
+// 19,456 keys 30 against 284.  A second kernel for the joins cost every call 4 us.)  Where the parts of an item are small,
 // the last part's CTA does join alone, and the launch is an ordinary one (the
 // host's rule is at the launch).  The loader warp works the items out and hands them
 // to the others through a ring in shared memory.
 //
 // What bounds it, on GB300 (graph-replayed; fractions of a measured copy, 6,788 GB/s, and
 // of a cuBLAS bf16 product, 1,886 TFLOP/s).  Many cached keys for few rows: the cache's bytes --
-// 16 lanes of 8 tokens over 16,000 keys, 32 query on 8 key/value heads of 128, 166 us, 0.93; 16
+// 16 lanes of 8 tokens over 16,000 keys, 32 query on 8 key/value heads of 128, 167 us, 0.93; 16
 // tokens over 262,144 keys 162 us, 0.98.  Chunks: the chain of a stream from one S to
 // the next (product, softmax, product) with the tensor pipe 50-60% busy -- 2,048 tokens over
-// 30,000 keys 709 us, 1,467 TFLOP/s, 0.78; heads of 64 867 TFLOP/s (the same softmax for half
-// the products), heads of 256 1,125 (K and V tiles of 64 keys from L2 for one row tile).  A prompt of
-// 2,048 at 0 keys 52 us, 659 TFLOP/s: rows of Q, edges, outputs and joins as much as tiles.  Little
+// 30,000 keys 708 us, 1,470 TFLOP/s, 0.78; heads of 64 870 TFLOP/s (the same softmax for half
+// the products), heads of 256 1,130 (K and V tiles of 64 keys from L2 for one row tile).  A prompt of
+// 2,048 at 0 keys 52 us, 660 TFLOP/s: rows of Q, edges, outputs and joins as much as tiles.  Little
 // work: the chain of one tile, 8 us (lengths 1.0, runs 1.5, first tile 1.5, scores 0.4, softmax
 // 1-2, product 0.4, output 1), and 3 us more where parts are joined.  Neither the exponentials (a polynomial for a
 // quarter of them: 748 -> 804 us) nor the second pass over S (held back in registers: 745 -> 769 us)
