@@ -204,8 +204,8 @@ spec_status launch_attention(const Device &d, const attn::Args &a, int64_t chunk
     constexpr int64_t kAlone = 32 << 10, kAloneAll = 128 << 10, kAloneWorst = 1 << 20, kAloneParts = 96;
     attn::Args b = a;
     const int64_t ctas = grid.x, rows = chunk * a.group < S::kRows ? chunk * a.group : S::kRows;
-    const int64_t table = a.max_pages << a.log_page, seen = a.window + S::kRows / a.group + 2;
-    const int64_t widest = ((a.window > 0 && seen < table ? seen : table) / S::BK + 2) / S::kLeast + 2;
+    const int64_t table = a.max_pages << a.log_page, seen = a.window > 0 && a.window < table ? a.window + S::kRows / a.group + 2 : table;
+    const int64_t widest = ((seen < table ? seen : table) / S::BK + 2) / S::kLeast + 2;
     const int64_t items = (int64_t)a.lanes * a.heads_kv, likely = ctas / items + 2, one = ctas / a.heads_kv + 2;
     const int64_t parts = widest < likely ? widest : likely, worst = widest < one ? widest : one, part = rows * D * 4;
     b.share_joins = part > kAlone || parts * part > kAloneAll || worst * part > kAloneWorst || worst > kAloneParts;

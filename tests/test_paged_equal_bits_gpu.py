@@ -88,3 +88,14 @@ def test_shared_joins_in_a_graph(sd, dim, new, ctx, hk, group):
         torch.cuda.synchronize()
         sd.spec_device_status()
         assert torch.equal(out.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("window", [1 << 20, 1 << 40, (1 << 63) - 1])
+def test_a_window_past_every_key(sd, window):
+    """Any window is taken; one wider than the context is none."""
+    import torch
+    for new, ctx, hk, group, dim in (([1, 3], [700, 20_000], 1, 4, 128), ([300], [2_000], 2, 4, 64)):
+        q, cache, batch = _step(sd, new, ctx, hk, group, dim, 64)
+        want = sd.paged_attention(q, cache, batch, max_new=max(new))
+        out, lse = sd.paged_attention(q, cache, batch, max_new=max(new), window=window)
+        assert torch.equal(out.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
