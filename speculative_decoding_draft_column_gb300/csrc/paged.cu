@@ -397,7 +397,8 @@ spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q,
     // (of tiles of 64 keys, the smaller; 2^31 - 2^16 unless there are 2^15 items)
     const int64_t tiles = (1ll << attn::kItemBit) / items - 2;
     a.most_keys = (int32_t)(tiles < (0x7FFF0000 >> 6) ? tiles << 6 : 0x7FFF0000);
-    a.c = scale * attn::kLog2e; a.window = window;
+    a.c = scale * attn::kLog2e;
+    a.window = window > INT32_MAX ? 0 : window;   // past every position: none (and positions less it stay within 64 bits)
     a.out = static_cast<uint16_t *>(out); a.lse = lse;
     a.counters = static_cast<unsigned int *>(workspace);
     a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + SPEC_PAGED_WORKSPACE_ZEROED);

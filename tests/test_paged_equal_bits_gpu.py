@@ -99,3 +99,17 @@ def test_a_window_past_every_key(sd, window):
         want = sd.paged_attention(q, cache, batch, max_new=max(new))
         out, lse = sd.paged_attention(q, cache, batch, max_new=max(new), window=window)
         assert torch.equal(out.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_the_widest_window_over_rows_with_no_key(sd, dim):
+    """A seq_len below the chunk: its first rows' positions lie below zero."""
+    import torch
+    for new, ctx, seq in (([4, 3], [0, 0], [2, 0]), ([200, 1], [0, 0], [150, 0])):
+        q, cache, batch = _step(sd, new, ctx, 1, 4, dim, 64)
+        batch.seq_lens.copy_(torch.tensor(seq, dtype=torch.int32))
+        want = sd.paged_attention(q, cache, batch, max_new=max(new))
+        assert (want[0][:new[0] - seq[0]] == 0).all() and want[1][:new[0] - seq[0]].isneginf().all()
+        for window in (1 << 31, (1 << 63) - 1):
+            out, lse = sd.paged_attention(q, cache, batch, max_new=max(new), window=window)
+            assert torch.equal(out.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
