@@ -399,6 +399,142 @@ spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q,
  * sizes; a negative status on failure. */
 int64_t spec_paged_attention_workspace(void);
 
+/* ---- The 8-bit cache: half the bytes of the 16-bit one ---------------------
+ *
+ * A vector (the head_dim elements of a token's key, or value, of one head) is
+ * head_dim e4m3 codes (sign, 4 bits of exponent, 3 of fraction; largest 448) and
+ * one byte of scale: element i is code[i] * 2^(scale - 127).  spec_paged_store8
+ * quantises as it stores, spec_paged_attention8 (and spec_tree_attention8) reads.
+ * Strides as in spec_paged_cache but multiples of 16; scales are contiguous
+ * [pages][heads][page_size]; all four addresses 16-byte aligned. */
+typedef struct {
+    void *k, *v;                   /* device, codes */
+    uint8_t *k_scales, *v_scales;  /* device, [pages][heads][page_size] */
+    int64_t k_strides[3], v_strides[3];
+    int64_t pages;          /* 1 .. 2^31-1 */
+    int32_t page_size;      /* tokens a page, >= 1 (attention: a power of two >= 16) */
+    int32_t heads;          /* key/value heads, >= 1; heads * head_dim below 2^31 */
+    int32_t head_dim;       /* a multiple of 16, at most 256 (attention: 64, 128 or 256) */
+    int32_t dtype;          /* SPEC_BF16 or SPEC_F16: what is stored from, and of q and out */
+} spec_paged_cache8;
+
+/* spec_paged_store into an 8-bit cache; k and v of type cache->dtype.  A vector's
+ * exponent e is the smallest for which its largest magnitude is at most
+ * 448 * 2^e, from -120 (fp16: -14) to 7; element x becomes the code nearest to
+ * x / 2^e (ties to even).  So a value is off by at most 2^-4 of itself or 2^-10 * 2^e;
+ * magnitudes above 57,344 become 57,344, and a vector that holds an infinity or a
+ * NaN reads as NaN throughout (scale 255, codes 127). */
+spec_status spec_paged_store8(const void *k, const void *v, int64_t tokens, int64_t k_token_stride,
+                              int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                              const int64_t *slots, const spec_paged_cache8 *cache);
+
+/* spec_paged_attention over an 8-bit cache: the same arguments, workspace and
+ * limits, pages of 16 tokens or more, q and out of type cache->dtype.  Codes times
+ * their scale are exact in dtype, so the result is that of spec_paged_attention over
+ * those values.  What the cache holds past a lane's last position or before its
+ * window, scales included, does not matter. */
+spec_status spec_paged_attention8(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
+                                  int64_t q_head_stride, const spec_paged_cache8 *cache, const spec_paged_batch *batch,
+                                  float scale, int64_t window, int64_t max_new, void *out, float *lse,
+                                  void *workspace, int64_t workspace_bytes);
+
+/* ---- Rounds whose drafts form a tree --------------------------------------
+ *
+ * A lane's new tokens are the nodes of a tree: node 0 the anchor (the last
+ * committed token, not yet cached), every other node a draft that follows its
+ * parent, parents before their children.  The lanes' nodes lie one after the
+ * other: node i of lane l is row cu[l] + i of the step (cu of spec_paged_plan, whose
+ * slots take the nodes' keys and values in that order).  parents[t] is the
+ * parent's index within the lane; what node 0 has there is ignored, and a node
+ * whose parent is not an earlier node of its lane has none (it starts a tree of
+ * its own, and no verify reaches it).
+ *
+ * A round is spec_paged_plan, spec_tree_plan, per layer spec_paged_store and
+ * spec_tree_attention, then spec_tree_verify (or _sampled), and per layer
+ * spec_tree_commit.  Nothing waits for the host. */
+#define SPEC_TREE_MAX_NODES 256   /* nodes of a lane, the anchor among them */
+
+/* What each node sees, and where it stands: for node i of a lane
+ *   masks[t][w], bit b: node 32 w + b is node i or above it (uint32 [tokens][mask_words]);
+ *   positions[t] = context + the number of nodes above it, context = seq_len - new (for
+ *   rotary positions; spec_paged_plan's count the nodes in a row).
+ * Rows past the step's total get 0.  1 <= mask_words <= 8; nodes from 32 * mask_words on
+ * have no bit.  parents int32 [tokens]; masks and positions must not overlap the inputs, or
+ * each other.  Reads the batch's cu_new and seq_lens.  One launch. */
+spec_status spec_tree_plan(const int32_t *parents, int64_t tokens, const spec_paged_batch *batch, uint32_t *masks,
+                           int32_t mask_words, int32_t *positions);
+
+/* spec_paged_attention for trees: node i of a lane attends the lane's cached
+ * tokens (positions below seq_len - new) and those new tokens j <= i whose bit of
+ * masks[t] is set -- any bits: those of spec_tree_plan, or a caller's own.  With a window
+ * the cached tokens are cut to positions above p - window, p = context + (set bits up to i) - 1;
+ * a tree's window is 0 or at least SPEC_TREE_MAX_NODES.  A row that sees no key
+ * gets out = 0 and lse = -inf.  All else, workspace included, as there; values of all the
+ * step's new tokens must be finite, seen or not. */
+spec_status spec_tree_attention(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
+                                int64_t q_head_stride, const spec_paged_cache *cache, const spec_paged_batch *batch,
+                                const uint32_t *masks, int32_t mask_words, float scale, int64_t window, int64_t max_new,
+                                void *out, float *lse, void *workspace, int64_t workspace_bytes);
+
+/* The same over an 8-bit cache. */
+spec_status spec_tree_attention8(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
+                                 int64_t q_head_stride, const spec_paged_cache8 *cache, const spec_paged_batch *batch,
+                                 const uint32_t *masks, int32_t mask_words, float scale, int64_t window, int64_t max_new,
+                                 void *out, float *lse, void *workspace, int64_t workspace_bytes);
+
+/* Greedy verify of trees: from the anchor on, the target's argmax of a node's
+ * column (ties to the smaller id) is committed; a child of the node that holds
+ * that token (the first of them) is accepted, and its column comes next.
+ *   target_logits bf16 [tokens][V], row t the target's logits after node t (any
+ *                 2-byte alignment; no NaN);
+ *   drafts        int32 [tokens], the nodes' tokens (an anchor's is not read; ids outside
+ *                 [0, V) never match);
+ *   parents       int32 [tokens];  cu int32 [lanes+1], as above (a lane without nodes
+ *                 gets length 0 and -1 throughout; nodes past SPEC_TREE_MAX_NODES are not reached);
+ *   depth         the most drafts that may be accepted, 1 .. SPEC_TREE_MAX_NODES - 1;
+ *   out_accept_len int32 [lanes]: a, the accepted drafts;
+ *   out_commit_ids int32 [lanes][depth+1]: their tokens, then the target's own, then -1;
+ *   out_path       int32 [lanes][depth+1]: 0 (the anchor), the accepted nodes, then -1.
+ * For a chain of gamma = depth drafts this is spec_verify_v.  Only the columns of a
+ * lane's path have to be read, and where there are many nodes only they are.  lanes at
+ * most 65,535.  Outputs must not overlap inputs or each other.  One launch; scratch as for spec_verify
+ * (spec_reserve(tokens, top_k, lanes, SPEC_MAX_GAMMA) covers it). */
+spec_status spec_tree_verify(const uint16_t *target_logits, const int32_t *drafts, const int32_t *parents,
+                             const int32_t *cu, int64_t tokens, int64_t lanes, int32_t depth, int64_t V,
+                             int32_t *out_accept_len, int32_t *out_commit_ids, int32_t *out_path);
+
+/* Sampled verify of trees, drafts one-hot (the target's distribution q of a
+ * column as in spec_verify_sampled).  At a node the children are tried in
+ * order: child c, with token x, is accepted when
+ *   uniforms[c][0] * (what of q is left) < q(x),
+ * else x is taken out of q (a later child with the same x finds nothing).  When no child
+ * is accepted -- or depth drafts are -- the token committed is the first in the nucleus (list
+ * order, tokens taken out skipped) whose running q exceeds uniforms[node][1] times what of q
+ * is left.  So the committed tokens follow the target's distribution whatever the tree.
+ *   uniforms  double [tokens][2], each in [0, 1).
+ * A chain is spec_verify_sampled with the accepting uniforms one row on. */
+spec_status spec_tree_verify_sampled(const uint16_t *target_logits, const int32_t *drafts, const int32_t *parents,
+                                     const int32_t *cu, int64_t tokens, int64_t lanes, int32_t depth, int64_t V,
+                                     double temperature, double top_p, int32_t top_k, const double *uniforms,
+                                     int32_t *out_accept_len, int32_t *out_commit_ids, int32_t *out_path);
+
+/* The accepted path's keys and values moved to where a row of tokens has them:
+ * for each lane and i = 1 .. min(accept_lens[l], depth), the vectors at position
+ * context + path[l][i] of the cache go to context + i (context = seq_len - new, as the
+ * step had it).  In place: path[i] >= i, as in a verify's path; entries outside
+ * [i, new) end a lane's path.
+ *   path         int32 [lanes][depth+1], accept_lens int32 [lanes] (a verify's outputs);
+ *   context_out  int32 [lanes]: context + 1 + the drafts moved, the next step's context (context
+ *                itself for a lane without new tokens), or NULL.
+ * Reads the batch's block_table, cu_new and seq_lens.  Table entries outside [0, pages) are
+ * skipped.  context_out must not overlap what the call reads.  One launch for a layer. */
+spec_status spec_tree_commit(const spec_paged_cache *cache, const spec_paged_batch *batch, const int32_t *path,
+                             const int32_t *accept_lens, int32_t depth, int32_t *context_out);
+
+/* The same in an 8-bit cache, codes and scales. */
+spec_status spec_tree_commit8(const spec_paged_cache8 *cache, const spec_paged_batch *batch, const int32_t *path,
+                              const int32_t *accept_lens, int32_t depth, int32_t *context_out);
+
 /* Penalties, biases and grammar masks on logits, before they are verified or
  * sampled: logits bf16 [lanes][cols][V] (any 2-byte alignment) -> out, the same layout.
  * Column j of a lane predicts the token after the lane's history and its first

@@ -34,6 +34,8 @@ __all__ = [
     "SPEC_BF16", "SPEC_F16", "SPEC_PAGED_MAX_LANES", "SPEC_PAGED_WORKSPACE_ZEROED", "PagedCache", "PagedBatch", "spec_paged_plan", "spec_paged_store",
     "spec_paged_attention", "spec_paged_attention_workspace", "new_attention_workspace", "spec_logits_process",
     "paged_attention", "process_logits",
+    "SPEC_TREE_MAX_NODES", "PagedCache8", "spec_paged_store8", "spec_paged_attention8", "spec_tree_plan", "spec_tree_attention",
+    "spec_tree_attention8", "spec_tree_verify", "spec_tree_verify_sampled", "spec_tree_commit", "spec_tree_commit8", "tree_verify",
 ]
 
 SPEC_OK, SPEC_ERR_ARG, SPEC_ERR_ALLOC, SPEC_ERR_CUDA = 0, -1, -2, -3
@@ -78,6 +80,15 @@ _SIGS = {
     "spec_paged_store": [_p, _p, _i64, _i64, _i64, _i64, _i64, _p, _p],
     "spec_paged_attention": [_p, _i64, _i32, _i64, _i64, _p, _p, ctypes.c_float, _i64, _i64, _p, _p, _p, _i64],
     "spec_paged_attention_workspace": [],
+    "spec_paged_store8": [_p, _p, _i64, _i64, _i64, _i64, _i64, _p, _p],
+    "spec_paged_attention8": [_p, _i64, _i32, _i64, _i64, _p, _p, ctypes.c_float, _i64, _i64, _p, _p, _p, _i64],
+    "spec_tree_plan": [_p, _i64, _p, _p, _i32, _p],
+    "spec_tree_attention": [_p, _i64, _i32, _i64, _i64, _p, _p, _p, _i32, ctypes.c_float, _i64, _i64, _p, _p, _p, _i64],
+    "spec_tree_attention8": [_p, _i64, _i32, _i64, _i64, _p, _p, _p, _i32, ctypes.c_float, _i64, _i64, _p, _p, _p, _i64],
+    "spec_tree_verify": [_p, _p, _p, _p, _i64, _i64, _i32, _i64, _p, _p, _p],
+    "spec_tree_verify_sampled": [_p, _p, _p, _p, _i64, _i64, _i32, _i64, ctypes.c_double, ctypes.c_double, _i32, _p, _p, _p, _p],
+    "spec_tree_commit": [_p, _p, _p, _p, _i32, _p],
+    "spec_tree_commit8": [_p, _p, _p, _p, _i32, _p],
     "spec_logits_process": [_p, _i64, _i32, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _i64, _p, _p, _i64, _p, _p],
 }
 EXPORTS = tuple(_SIGS)
@@ -431,6 +442,8 @@ def round_step(draft_logits, k: int, target_logits, drafts):
 
 # the paged cache and the logits rules (they use the checks above)
 from .paged import (  # noqa: E402
-    SPEC_BF16, SPEC_F16, SPEC_PAGED_MAX_LANES, SPEC_PAGED_WORKSPACE_ZEROED, PagedBatch, PagedCache,
-    new_attention_workspace, paged_attention, process_logits, spec_logits_process, spec_paged_attention,
-    spec_paged_attention_workspace, spec_paged_plan, spec_paged_store)
+    SPEC_BF16, SPEC_F16, SPEC_PAGED_MAX_LANES, SPEC_PAGED_WORKSPACE_ZEROED, SPEC_TREE_MAX_NODES, PagedBatch, PagedCache,
+    PagedCache8, new_attention_workspace, paged_attention, process_logits, spec_logits_process, spec_paged_attention,
+    spec_paged_attention8, spec_paged_attention_workspace, spec_paged_plan, spec_paged_store, spec_paged_store8,
+    spec_tree_attention, spec_tree_attention8, spec_tree_commit, spec_tree_commit8, spec_tree_plan, spec_tree_verify,
+    spec_tree_verify_sampled, tree_verify)

@@ -9,7 +9,7 @@ import tempfile
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SRCS = [os.path.join(CSRC, f) for f in ("specsel.cu", "paged.cu")]
+SRCS = [os.path.join(CSRC, f) for f in ("specsel.cu", "paged.cu", "attention_tree.cu", "attention8.cu", "tree.cu")]
 HDR = os.path.join(ROOT, "include", "specsel.h")
 LIB = os.path.join(PKG, "libspecsel.so")
 

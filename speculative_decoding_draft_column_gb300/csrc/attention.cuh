@@ -59,6 +59,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace attn {
@@ -72,21 +74,30 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kItemBit = 40;     // a step's tiles are counted below this bit of a word, its items above (the host checks that they fit)
 constexpr int kMaxSms = 512;     // counters at the start of the workspace: [2][kMaxSms]
 
-template <int D_, int QT_>
+// kQ8: the cache holds e4m3 codes with a power-of-two scale a vector; kTree: the
+// new tokens of a lane are the nodes of a tree, with a mask each.
+template <int D_, int QT_, bool Q8_ = false, bool TREE_ = false>
 struct Shape {
     static constexpr int D = D_, QT = QT_;
+    static constexpr bool kQ8 = Q8_, kTree = TREE_;
     static constexpr int BK = D == 256 ? 64 : 128;             // keys of a tile
     static constexpr int NS = D == 256 ? 1 : 2;                // streams (softmax warpgroups)
     static constexpr int NB = D / 64;                          // 128-byte-wide blocks of an operand
     static constexpr int kQBytes = 128 * D * 2;                // one row tile
     static constexpr int kStageBytes = BK * D * 2;             // a K or a V tile
-    static constexpr int QB = QT == 1 && D <= 128 ? 2 : 1;     // Q buffers
-    static constexpr int kStages = (224 * 1024 - QB * QT * kQBytes) / kStageBytes < 12
-                                       ? (224 * 1024 - QB * QT * kQBytes) / kStageBytes : 12;
+    static constexpr int QB = QT == 1 && D <= (kQ8 ? 64 : 128) ? 2 : 1;   // Q buffers
+    static constexpr int kRoom = 224 * 1024 - QB * QT * kQBytes;
+    // 8 bits: as many 16-bit tiles as keep the products fed, the rest for codes on their way
+    static constexpr int kStages = kQ8 ? (D == 64 ? 4 : 3) : kRoom / kStageBytes < 12 ? kRoom / kStageBytes : 12;
+    static constexpr int kRawCodes = BK * D;                   // codes of a tile, then 128 bytes for a page's scales
+    static constexpr int kRawBytes = kRawCodes + BK / 16 * 128;
+    static constexpr int kRawMost = (kRoom - kStages * kStageBytes) / kRawBytes;
+    static constexpr int kRaw = !kQ8 ? 0 : kRawMost < 8 ? kRawMost : 8;
     static constexpr int kSoftmaxWarps = NS * 8;
-    static constexpr int kThreads = kSoftmaxWarps * 32 + 128;  // softmax; K/V loader, MMA, two Q loaders
+    static constexpr int kConverters = kQ8 ? 4 : 0;            // warps
+    static constexpr int kThreads = kSoftmaxWarps * 32 + 128 + kConverters * 32;  // softmax; K/V loader, MMA, two Q loaders; converters
     static constexpr int kSwap = 512;                          // floats that softmax warps exchange through
-    static constexpr int kPayload = QB * QT * kQBytes + kStages * kStageBytes + kSwap * 4;
+    static constexpr int kPayload = QB * QT * kQBytes + kStages * kStageBytes + kRaw * kRawBytes + kSwap * 4;
     static constexpr int kRows = QT * 128;
     static constexpr int kExtra = QT == 2 ? 4 : 3;             // tiles that an item's other work costs
     static constexpr int kLeast = QT == 1 ? 2 : 1;             // units of a run that an item is cut into, at least
@@ -95,6 +106,7 @@ struct Shape {
     static constexpr int kPartFloats = kRows * (D + 2);        // O, then m and sum
     static_assert(D == 64 || D == 128 || (D == 256 && QT == 1), "");
     static_assert(kO + NS * D <= 512, "TMEM");
+    static_assert(!kQ8 || kRaw >= 2, "a K and a V tile on their way");
 };
 
 struct Args {
@@ -114,6 +126,11 @@ struct Args {
     float *lse;
     unsigned int *counters;   // [2][kMaxSms], zero between calls: parts published, and joiners done, of the item begun by a CTA
     float *parts;          // [grid][2][kPartFloats]
+    const uint32_t *masks; // kTree: [tokens][mask_words], bit j: the token sees its lane's new token j
+    int32_t mask_words;
+};
+struct Args8 : Args {
+    CUtensorMap ksmap, vsmap;   // the scales
 };
 
 // An item in parts that this CTA has one of: the second slot's part of CTA
@@ -140,7 +157,7 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
                  : "memory");
     return ok != 0;
 }
-__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity)
+static __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity)
 {
     const uint64_t t0 = global_ns();
     for (;;) {
@@ -260,6 +277,31 @@ __device__ __forceinline__ void mask_scores(uint32_t (&x)[32], int from, int to)
         if (e < from || e >= to) x[e] = 0xFF800000u;
 }
 
+// The scores of a tree's nodes that the row does not see are -inf: x[e] belongs
+// to new token at + e of the lane (below 0: a cached one, seen).
+__device__ __forceinline__ void mask_nodes(uint32_t (&x)[32], const uint32_t *mask, int words, int at)
+{
+    if (at <= -32) return;
+    const int w = at >> 5, s = at & 31;                    // at >= -31: w is -1 or more
+    const uint32_t lo = w < 0 ? kFull : w < words ? __ldg(mask + w) : 0u;
+    const uint32_t hi = w + 1 < words ? __ldg(mask + w + 1) : 0u;
+    const uint32_t seen = __funnelshift_r(lo, hi, s);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (!(seen >> e & 1u)) x[e] = 0xFF800000u;
+}
+
+// The depth of new token `tok` in its tree: the nodes above it.
+__device__ __forceinline__ int node_depth(const uint32_t *mask, int words, int tok)
+{
+    int n = 0;
+    for (int w = 0; w < words && 32 * w <= tok; ++w) {
+        const uint32_t m = __ldg(mask + w);
+        n += __popc(tok - 32 * w < 31 ? m & ((2u << (tok - 32 * w)) - 1u) : m);
+    }
+    return n > 0 ? n - 1 : 0;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
@@ -310,6 +352,22 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, i
                  : "memory");
 }
 
+// 8 bits: `rows` vectors of codes of a page, and their scales
+__device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap *map, int row, int head, int page, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+                 "%4, %5}], [%6];" ::"r"(dst),
+                 "l"(map), "r"(0), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tma_scales(uint32_t dst, const CUtensorMap *map, int row, int head, int page, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+                 "%4}], [%5];" ::"r"(dst),
+                 "l"(map), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 // 16 bytes global -> shared, and the wait for all of the thread's
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
 {
@@ -356,7 +414,8 @@ __device__ __forceinline__ Reach reach_of(const Args &a, int n, int seq, int rt)
     r.hi = seq - n + e + 1;
     r.lo = 0;
     if (a.window > 0) {
-        const int64_t lo = (int64_t)(seq - n + (int)div_group(a, row0)) - a.window + 1;
+        // (a tree's node lies at its depth, 0 at least)
+        const int64_t lo = (int64_t)(seq - n + (S::kTree ? 0 : (int)div_group(a, row0))) - a.window + 1;
         r.lo = lo > 0 ? (int)lo : 0;
     }
     if (r.hi > r.lo) {
@@ -474,6 +533,7 @@ constexpr int kItems = 4;
 template <typename S>
 struct Bars {
     uint64_t full[S::kStages], empty[S::kStages];
+    uint64_t raw_full[S::kRaw + 1], raw_empty[S::kRaw + 1];   // of the codes (8 bits)
     uint64_t s_full[2], p_full[2], o_done[2];
     uint64_t q_full[2], q_empty[2], item_full[kItems], item_empty[kItems], drain;
     uint64_t part_full[2], part_known[2];   // the part in a slot is written; the others know
@@ -502,10 +562,89 @@ __device__ __forceinline__ uint32_t ld_acquire(const unsigned int *p)
 }
 constexpr int kAllSoftmax = 9;   // barrier ids: 1 .. 8 a pair of warps with the same rows, 9 all softmax warps
 
-template <int D, int QT, bool F16>
-__global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(const __grid_constant__ Args a)
+// A scale's byte (its exponent + 127) as a pair of 16-bit factors for codes that were
+// widened by their bits.  e4m3's bits, shifted into bf16's places, are the value times
+// 2^-120 (the exponents' offsets are 7 and 127; fractions of 0 exponent go along), so that one multiplication
+// by 2^(120 + exponent) gives the value, exactly; in fp16 the conversion is an
+// instruction of its own, and the factor 2^exponent.  255 stands for a vector that is no number.
+template <bool F16>
+__device__ __forceinline__ uint32_t scale_pair(uint32_t byte)
 {
-    using S = Shape<D, QT>;
+    const uint32_t b = byte < 134u ? byte : 134u;
+    const uint32_t h = byte == 255u ? (F16 ? 0x7E00u : 0x7FC0u) : F16 ? ((b < 113u ? 113u : b) - 112u) << 10 : (b + 120u) << 7;
+    return h | h << 16;
+}
+
+// Four codes to four 16-bit values.
+template <bool F16>
+__device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t scale)
+{
+    uint2 r;
+    if (F16) {
+        asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 x, y;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 x, l;\n\t"
+            "cvt.rn.f16x2.e4m3x2 y, h;\n\tmul.rn.f16x2 %0, x, %3;\n\tmul.rn.f16x2 %1, y, %3;\n\t}"
+            : "=r"(r.x), "=r"(r.y) : "r"(w), "r"(scale));
+    } else {
+        const uint32_t x = __byte_perm(w, 0u, 0x1404), y = __byte_perm(w, 0u, 0x3424);   // a code in the upper byte of each half
+        const uint32_t bx = (x & 0x80008000u) | (x >> 4 & 0x07F007F0u), by = (y & 0x80008000u) | (y >> 4 & 0x07F007F0u);
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(bx), "r"(scale));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(by), "r"(scale));
+    }
+    return r;
+}
+
+// The converting warps (8 bits): each tile of codes, as it lands, into a 16-bit tile in the
+// layout of the products' operands.  A thread takes 16 codes of a row at a time; lanes of the
+// second block of 64 elements write their two pieces in the other order, so that the eight
+// threads of a row are on different banks.
+template <typename S, bool F16>
+__device__ __forceinline__ void convert_tiles(Bars<S> &bar, Item *items, const uint8_t *raw_smem, uint8_t *kv_smem, int rows,
+                                              int warp, int lane)
+{
+    constexpr int kPieces = S::D / 16, kStep = S::kConverters * 32 / kPieces;   // threads a row, rows a pass
+    const int id = warp * 32 + lane, p = id % kPieces, r0 = id / kPieces;
+    const int log_rows = 31 - __clz(rows);
+    const int block = p >> 2, piece = (p & 3) * 2, flip = block & 1;
+    uint32_t idx = 0;
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+        if (!__all_sync(kFull, wait(&bar.item_full[n % kItems], (n / kItems) & 1))) break;
+        const int tiles = items[n % kItems].tiles;
+        __syncwarp();
+        if (tiles == 0) break;
+        if (lane == 0) mbar_arrive(&bar.item_empty[n % kItems]);
+        for (int t = 0; t < 2 * tiles; ++t, ++idx) {
+            const uint32_t rs = idx % S::kRaw, st = idx % S::kStages;
+            ok = wait(&bar.raw_full[rs], (idx / S::kRaw) & 1) && wait(&bar.empty[st], ((idx / S::kStages) & 1) ^ 1);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            const uint8_t *codes = raw_smem + rs * S::kRawBytes, *scales = codes + S::kRawCodes;
+            uint8_t *tile = kv_smem + st * S::kStageBytes + block * (S::BK * 128);
+#pragma unroll 4
+            for (int r = r0; r < S::BK; r += kStep) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(codes + r * S::D + p * 16);
+                const uint32_t f = scale_pair<F16>(scales[(r >> log_rows) * 128 + (r & (rows - 1))]);
+                const uint2 a = widen4<F16>(w.x, f), b = widen4<F16>(w.y, f), c = widen4<F16>(w.z, f), d = widen4<F16>(w.w, f);
+                const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, d.x, d.y);
+                uint8_t *row = tile + r * 128;
+                *reinterpret_cast<uint4 *>(row + (((piece + flip) ^ (r & 7)) << 4)) = flip ? hi : lo;
+                *reinterpret_cast<uint4 *>(row + (((piece + (flip ^ 1)) ^ (r & 7)) << 4)) = flip ? lo : hi;
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bar.full[st]);
+                mbar_arrive(&bar.raw_empty[rs]);
+            }
+        }
+    }
+}
+
+template <int D, int QT, bool F16, bool Q8, bool TREE>
+__global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
+    attention_kernel(const __grid_constant__ std::conditional_t<Q8, Args8, Args> a)
+{
+    using S = Shape<D, QT, Q8, TREE>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars<S> bar;
     __shared__ Item items[kItems];
@@ -515,14 +654,18 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
     __shared__ Plan plan;
     __shared__ __align__(16) int64_t warp_units[S::kThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kLoader = S::kSoftmaxWarps, kMma = kLoader + 1, kQLoader = kLoader + 2;
+    constexpr int kLoader = S::kSoftmaxWarps, kMma = kLoader + 1, kQLoader = kLoader + 2, kConvert = kLoader + 4;
 
     pdl_launch_dependents();
     if (tid == 0) {
         s_gave_up = 0u;
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.full[i], Q8 ? S::kConverters : 1);
             mbar_init(&bar.empty[i], 1);
+        }
+        for (int i = 0; i < S::kRaw; ++i) {
+            mbar_init(&bar.raw_full[i], 1);
+            mbar_init(&bar.raw_empty[i], S::kConverters);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
@@ -535,7 +678,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&bar.item_full[i], 1);
-            mbar_init(&bar.item_empty[i], S::kSoftmaxWarps + 3);
+            mbar_init(&bar.item_empty[i], S::kSoftmaxWarps + 3 + S::kConverters);
         }
         mbar_init(&bar.drain, 1);
         fence_mbar_init();
@@ -543,6 +686,10 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
     if (warp == kLoader && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&a.kmap) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&a.vmap) : "memory");
+        if constexpr (Q8) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&a.ksmap) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&a.vsmap) : "memory");
+        }
     }
     if (warp == kMma) tmem_alloc(&tmem_slot);
     pdl_wait();
@@ -641,7 +788,8 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
 
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *q_smem = smem, *kv_smem = smem + S::QB * QT * S::kQBytes;
-    float *swap = reinterpret_cast<float *>(kv_smem + S::kStages * S::kStageBytes);
+    uint8_t *raw_smem = kv_smem + S::kStages * S::kStageBytes;
+    float *swap = reinterpret_cast<float *>(raw_smem + S::kRaw * S::kRawBytes);
 
     if (warp == kLoader) {
         // ---- the items of this CTA's run, and their K and V tiles: a lane of
@@ -678,7 +826,9 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         const int rows = min(1 << a.log_page, S::BK);            // rows of a box
         const int boxes = S::BK / rows;
         const bool whole = rows == S::BK;                        // one box brings all blocks
-        const uint32_t box_bytes = (uint32_t)rows * D * 2;
+        const uint32_t box_bytes = (uint32_t)rows * (Q8 ? D + 1 : D * 2);
+        constexpr uint32_t kRing = Q8 ? S::kRaw : S::kStages;    // where the copies land
+        uint64_t *landed = Q8 ? bar.raw_full : bar.full, *room = Q8 ? bar.raw_empty : bar.empty;
         auto page_of = [&](const Segment &s, int t) -> int {     // of this lane's box of tile t
             const int64_t k0 = (int64_t)(s.tile + t) * S::BK + lane * rows, pi = k0 >> a.log_page;
             return lane < boxes && k0 < s.r.hi && k0 + rows > s.r.lo && pi < a.max_pages
@@ -715,13 +865,19 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                 const int row = k0 & ((1 << a.log_page) - 1);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++idx) {
-                    const uint32_t st = idx % S::kStages, use = idx / S::kStages;
-                    ok = ok && wait(&bar.empty[st], (use & 1) ^ 1);
+                    const uint32_t st = idx % kRing, use = idx / kRing;
+                    ok = ok && wait(&room[st], (use & 1) ^ 1);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], bytes);
+                    if (lane == 0) mbar_arrive_expect_tx(&landed[st], bytes);
                     __syncwarp();
-                    if (mine) {
+                    if constexpr (Q8) {
+                        if (mine) {
+                            const uint32_t dst = smem_u32(raw_smem) + st * S::kRawBytes;
+                            tma_codes(dst + lane * rows * D, kv ? &a.vmap : &a.kmap, row, s.head, page, &landed[st]);
+                            tma_scales(dst + S::kRawCodes + lane * 128, kv ? &a.vsmap : &a.ksmap, row, s.head, page, &landed[st]);
+                        }
+                    } else if (mine) {
                         const CUtensorMap *map = kv ? &a.vmap : &a.kmap;
                         const uint32_t dst = smem_u32(kv_smem) + st * S::kStageBytes + lane * rows * 128;
                         if (whole) tma_page(dst, map, row, 0, s.head, page, &bar.full[st]);
@@ -757,9 +913,9 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
         if (!ok) {
             // given up: the copies in flight still have to land (each stage's
             // last use; bounded, whatever the other waits did)
-            for (uint32_t i = idx > (uint32_t)S::kStages ? idx - S::kStages : 0; i < idx; ++i) {
+            for (uint32_t i = idx > kRing ? idx - kRing : 0; i < idx; ++i) {
                 const uint64_t t0 = global_ns();
-                while (!mbar_try_wait(&bar.full[i % S::kStages], (i / S::kStages) & 1) && global_ns() - t0 < kWaitLimitNs) {}
+                while (!mbar_try_wait(&landed[i % kRing], (i / kRing) & 1) && global_ns() - t0 < kWaitLimitNs) {}
             }
         }
     } else if (warp == kMma) {
@@ -838,6 +994,8 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             while (!mbar_try_wait(&bar.drain, 0) && global_ns() - t0 < kWaitLimitNs) {}
         }
         __syncwarp();
+    } else if (Q8 && warp >= kConvert) {
+        if constexpr (Q8) convert_tiles<S, F16>(bar, items, raw_smem, kv_smem, min(1 << a.log_page, S::BK), warp - kConvert, lane);
     } else if (warp >= kQLoader) {
         // ---- Q: 16-byte pieces of the item's rows, consecutive lanes on
         // consecutive pieces, all of them on their way together; rows past the item's
@@ -920,9 +1078,10 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
             const int64_t gr = (int64_t)it.rt * S::kRows + (QT == 2 ? st * 128 : 0) + row;
             const bool valid = gr < (int64_t)it.n * a.group;
             const int tok = valid ? (int)div_group(a, (uint32_t)gr) : 0;
-            const int pos = it.seq - it.n + tok;
-            const int64_t klo64 = a.window > 0 ? (int64_t)pos - a.window + 1 : 0;
-            const int klo = klo64 > 0 ? (int)klo64 : 0, khi = valid ? pos + 1 : klo;   // keys of this row
+            const int ctx = it.seq - it.n;
+            const uint32_t *mask = TREE ? a.masks + (int64_t)(it.first + tok) * a.mask_words : nullptr;
+            const int64_t klo64 = a.window > 0 ? (int64_t)ctx + (TREE ? node_depth(mask, a.mask_words, tok) : tok) - a.window + 1 : 0;
+            const int klo = klo64 > 0 ? (int)klo64 : 0, khi = valid ? ctx + tok + 1 : klo;   // keys of this row
             const bool live = __any_sync(kFull, khi > klo);
             // the quads of rows in use, and this thread's place among those who clear V rows
             const int64_t rows_left = (int64_t)it.n * a.group - (int64_t)it.rt * S::kRows - (QT == 2 ? st * 128 : 0);
@@ -943,7 +1102,7 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     const uint32_t sa = tmem + lane_base + b * S::BK + half * kW;
                     // columns of this row in the half tile; what a row past the item's holds is nobody's
                     const int from = valid ? klo - key0 - half * kW : 0, to = valid ? khi - key0 - half * kW : kW;
-                    const bool edge = __any_sync(kFull, from > 0 || to < kW);
+                    const bool edge = __any_sync(kFull, from > 0 || to < kW) || (TREE && key0 + half * kW + kW > ctx);
                     // two passes over S in TMEM (other warps hide the loads; the
                     // half row in registers would not fit), rolled: the kernel's
                     // code is read from L2 once a launch, and its size counts
@@ -952,7 +1111,10 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                     for (int c = 0; c < kW; c += 32) {
                         uint32_t x[32];
                         tmem_ld32(x, sa + c);
-                        if (edge) mask_scores(x, from - c, to - c);
+                        if (edge) {
+                            mask_scores(x, from - c, to - c);
+                            if (TREE) mask_nodes(x, mask, a.mask_words, key0 + half * kW + c - ctx);
+                        }
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
 #pragma unroll
@@ -995,7 +1157,10 @@ __global__ void __launch_bounds__(Shape<D, QT>::kThreads, 1) attention_kernel(co
                         // P of columns c .. c+31 covers columns c/2 .. c/2+15 of this half's S, read before
                         uint32_t x[32], pk[16];
                         tmem_ld32(x, sa + c);
-                        if (edge) mask_scores(x, from - c, to - c);
+                        if (edge) {
+                            mask_scores(x, from - c, to - c);
+                            if (TREE) mask_nodes(x, mask, a.mask_words, key0 + half * kW + c - ctx);
+                        }
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float p0, p1;

@@ -11,9 +11,10 @@
 #include <mutex>
 
 #include "specsel.h"
+#include "checks.h"
 #include "common.cuh"
 #include "paged.cuh"
-#include "attention.cuh"
+#include "attention_launch.cuh"
 #include "logits_rules.cuh"
 #include "host.h"
 
@@ -22,7 +23,7 @@ using host::fail;
 
 namespace {
 
-constexpr int kMaxDevices = 64;
+using attn::kMaxDevices;
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -30,40 +31,9 @@ using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t,
 
 struct Device {
     bool init = false;
-    int sms = 0;
+    int index = 0, sms = 0;
     EncodeTiled encode = nullptr;
-    int attn_smem[5][2];   // dynamic shared memory of the attention kernels, [shape][fp16]
 };
-
-template <int D, int QT>
-constexpr int shape_index() { return D == 64 ? QT - 1 : D == 128 ? QT + 1 : 4; }
-
-// Give an attention kernel all the shared memory a CTA can have (one CTA an SM,
-// so that TMEM is never contended), and check what the kernel relies on: its
-// static shared memory stays below the first 1,024-byte boundary.
-template <int D, int QT, bool F16>
-spec_status prepare_attention(Device &d, int smem_max)
-{
-    using S = attn::Shape<D, QT>;
-    auto kernel = attn::attention_kernel<D, QT, F16>;
-    cudaFuncAttributes at;
-    cudaError_t e = cudaFuncGetAttributes(&at, kernel);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes");
-    const int dynamic = smem_max - (int)at.sharedSizeBytes;
-    if (at.sharedSizeBytes > 1024 || 1024 + S::kPayload > smem_max)
-        return fail(SPEC_ERR_CUDA, "attention: %d bytes of shared memory are not enough", smem_max);
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dynamic);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-    d.attn_smem[shape_index<D, QT>()][F16] = dynamic;
-    return SPEC_OK;
-}
-
-template <int D, int QT>
-spec_status prepare_attention(Device &d, int smem_max)
-{
-    const spec_status st = prepare_attention<D, QT, false>(d, smem_max);
-    return st == SPEC_OK ? prepare_attention<D, QT, true>(d, smem_max) : st;
-}
 
 std::mutex g_paged_mu;
 Device g_devices[kMaxDevices];
@@ -84,46 +54,28 @@ spec_status device(Device **out)
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
         e = cudaFuncSetAttribute(rules::process_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, rules::smem_bytes(true));
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-        int smem_max = 0;
-        e = cudaDeviceGetAttribute(&smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-        spec_status st = prepare_attention<64, 1>(d, smem_max);
-        if (st == SPEC_OK) st = prepare_attention<64, 2>(d, smem_max);
-        if (st == SPEC_OK) st = prepare_attention<128, 1>(d, smem_max);
-        if (st == SPEC_OK) st = prepare_attention<128, 2>(d, smem_max);
-        if (st == SPEC_OK) st = prepare_attention<256, 1>(d, smem_max);
-        if (st != SPEC_OK) return st;
+        size_t smem = 0;   // (the kernels are loaded now, not inside a capture)
+        const spec_status made[] = {attn::prepare<64, 1, false, false, false>(dev, &smem), attn::prepare<64, 1, true, false, false>(dev, &smem),
+                                    attn::prepare<64, 2, false, false, false>(dev, &smem), attn::prepare<64, 2, true, false, false>(dev, &smem),
+                                    attn::prepare<128, 1, false, false, false>(dev, &smem), attn::prepare<128, 1, true, false, false>(dev, &smem),
+                                    attn::prepare<128, 2, false, false, false>(dev, &smem), attn::prepare<128, 2, true, false, false>(dev, &smem),
+                                    attn::prepare<256, 1, false, false, false>(dev, &smem), attn::prepare<256, 1, true, false, false>(dev, &smem)};
+        for (const spec_status st : made)
+            if (st != SPEC_OK) return st;
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
         e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
         if (e != cudaSuccess) return cuda_fail(e, "cudaGetDriverEntryPointByVersion");
         if (!fn || found != cudaDriverEntryPointSuccess) return fail(SPEC_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
         d.encode = reinterpret_cast<EncodeTiled>(fn);
+        d.index = dev;
         d.init = true;
     }
     *out = &d;
     return SPEC_OK;
 }
 
-bool misaligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
-
-// A call's buffer, for the checks of what must not overlap.
-struct Range {
-    const void *p;
-    int64_t bytes;
-    const char *name;
-};
-bool overlap(const Range &a, const Range &b)
-{
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + (uint64_t)b.bytes && y < x + (uint64_t)a.bytes;
-}
-
-constexpr int64_t kMaxStride = 1ll << 39;
-
-bool bad_stride(int64_t s) { return s < 0 || s >= kMaxStride || s % 8 != 0; }
-
-template <bool kCooperative = false, typename K, typename A>
+template <typename K, typename A>
 spec_status launch(K kernel, dim3 grid, unsigned block, size_t smem, const A &a)
 {
     cudaLaunchConfig_t cfg;
@@ -132,46 +84,14 @@ spec_status launch(K kernel, dim3 grid, unsigned block, size_t smem, const A &a)
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = host::stream();
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeCooperative;
-    attr[1].val.cooperative = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = kCooperative ? 2 : 1;
+    cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
     host::count_launch();
-    return SPEC_OK;
-}
-
-spec_status check_cache(const spec_paged_cache *c)
-{
-    if (!c || !c->k || !c->v) return fail(SPEC_ERR_ARG, "cache: null pointer");
-    if (c->dtype != SPEC_BF16 && c->dtype != SPEC_F16) return fail(SPEC_ERR_ARG, "cache: unknown dtype %d", c->dtype);
-    if (misaligned(c->k, 16) || misaligned(c->v, 16))
-        return fail(SPEC_ERR_ARG, "cache: keys and values must be 16-byte aligned");
-    if (c->pages < 1 || c->pages > INT32_MAX) return fail(SPEC_ERR_ARG, "cache: pages = %lld", (long long)c->pages);
-    if (c->page_size < 1) return fail(SPEC_ERR_ARG, "cache: page_size = %d < 1", c->page_size);
-    if (c->heads < 1) return fail(SPEC_ERR_ARG, "cache: heads = %d < 1", c->heads);
-    if (c->head_dim < 8 || c->head_dim > 256 || c->head_dim % 8 != 0)
-        return fail(SPEC_ERR_ARG, "cache: head_dim = %d, need a multiple of 8 up to 256", c->head_dim);
-    if ((int64_t)c->heads * c->head_dim > INT32_MAX)
-        return fail(SPEC_ERR_ARG, "cache: heads * head_dim = %lld exceeds 2^31-1", (long long)c->heads * c->head_dim);
-    for (int i = 0; i < 3; ++i)
-        if (bad_stride(c->k_strides[i]) || bad_stride(c->v_strides[i]))
-            return fail(SPEC_ERR_ARG, "cache: strides must be non-negative multiples of 8 elements below 2^39");
-    return SPEC_OK;
-}
-
-spec_status check_batch(const spec_paged_batch *b)
-{
-    if (!b) return fail(SPEC_ERR_ARG, "batch: null pointer");
-    if (b->lanes < 0 || b->lanes > SPEC_PAGED_MAX_LANES)
-        return fail(SPEC_ERR_ARG, "batch: lanes = %lld outside [0, %d]", (long long)b->lanes, SPEC_PAGED_MAX_LANES);
-    if (b->max_pages < 1 || b->max_pages > INT32_MAX)
-        return fail(SPEC_ERR_ARG, "batch: max_pages = %lld", (long long)b->max_pages);
-    if (b->page_size < 1) return fail(SPEC_ERR_ARG, "batch: page_size = %d < 1", b->page_size);
     return SPEC_OK;
 }
 
@@ -181,40 +101,6 @@ constexpr int64_t kPartFloats = max2(attn::Shape<128, 2>::kPartFloats, attn::Sha
 static_assert(SPEC_PAGED_WORKSPACE_ZEROED == 2 * attn::kMaxSms * sizeof(unsigned int), "the counters");
 
 int attention_grid(const Device &d) { return d.sms < attn::kMaxSms ? d.sms : attn::kMaxSms; }
-
-template <int D, int QT>
-spec_status launch_attention(const Device &d, const attn::Args &a, int64_t chunk, bool f16)
-{
-    using S = attn::Shape<D, QT>;
-    static_assert(S::kPartFloats <= kPartFloats, "");
-    const dim3 grid((unsigned)attention_grid(d));
-    const size_t smem = (size_t)d.attn_smem[shape_index<D, QT>()][f16];
-    // Whether an item's parts are joined by all its CTAs (a cooperative launch) or
-    // by the last part's CTA alone (an ordinary one: 2-4 us less a call in a
-    // stream, 1 in a graph; 8 lanes of 8 tokens at 8,000 keys 51.8 against 55.3 us, 64 lanes of
-    // 16 tokens at 3,000 keys 30.8 against 34.8, 8 lanes of a token at 2,000 keys of one head
-    // 12.0 against 14.4).  The lengths are on the device, so the number of parts is
-    // estimated twice: from the items that the lanes and heads make if they are
-    // even, and from one lane having all the keys (the others short, or without tokens, as in
-    // a padded batch), whose heads then share the GPU.  Both are bounded by the table's
-    // width and the window.  Alone, a CTA joins the even case's 128 KB in 2 us.  Of 64 lanes
-    // of 4 tokens, one with 60,000 keys, it takes 29.4 against 20.5 us in a stream where that lane has
-    // one head (152 parts of 8 KB), 26.6 against 23.5 where it has two (76 parts); of 64 lanes
-    // of 16 tokens, one with 131,072 keys of one head (152 parts of 32 KB), 66 against 24 in a graph.
-    constexpr int64_t kAlone = 32 << 10, kAloneAll = 128 << 10, kAloneWorst = 1 << 20, kAloneParts = 96;
-    attn::Args b = a;
-    const int64_t ctas = grid.x, rows = chunk * a.group < S::kRows ? chunk * a.group : S::kRows;
-    const int64_t table = a.max_pages << a.log_page, seen = a.window > 0 && a.window < table ? a.window + S::kRows / a.group + 2 : table;
-    const int64_t widest = ((seen < table ? seen : table) / S::BK + 2) / S::kLeast + 2;
-    const int64_t items = (int64_t)a.lanes * a.heads_kv, likely = ctas / items + 2, one = ctas / a.heads_kv + 2;
-    const int64_t parts = widest < likely ? widest : likely, worst = widest < one ? widest : one, part = rows * D * 4;
-    b.share_joins = part > kAlone || parts * part > kAloneAll || worst * part > kAloneWorst || worst > kAloneParts;
-    if (b.share_joins)   // CTAs wait for one another's parts
-        return f16 ? launch<true>(attn::attention_kernel<D, QT, true>, grid, S::kThreads, smem, b)
-                   : launch<true>(attn::attention_kernel<D, QT, false>, grid, S::kThreads, smem, b);
-    return f16 ? launch(attn::attention_kernel<D, QT, true>, grid, S::kThreads, smem, b)
-               : launch(attn::attention_kernel<D, QT, false>, grid, S::kThreads, smem, b);
-}
 
 // The cache as TMA sees it: [page][head][block of 64][token][64], boxes of one
 // page's tokens (at most a tile's) by 64 elements -- all blocks at once where
@@ -235,17 +121,158 @@ spec_status page_map(const Device &d, const spec_paged_cache &c, void *base, con
     return SPEC_OK;
 }
 
+
+// The 8-bit cache as TMA sees it: codes [page][head][token][head_dim], boxes of one page's
+// tokens (at most a tile's), and scales [page][head][token].
+spec_status code_maps(const Device &d, const spec_paged_cache8 &c, void *codes, const int64_t *strides, void *scales,
+                      CUtensorMap *map, CUtensorMap *smap)
+{
+    const int tile = c.head_dim == 256 ? attn::Shape<256, 1>::BK : attn::Shape<128, 1>::BK;
+    const cuuint32_t rows = (cuuint32_t)(c.page_size < tile ? c.page_size : tile);
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)c.pages};
+    const cuuint64_t st[3] = {(cuuint64_t)strides[1], (cuuint64_t)strides[2], (cuuint64_t)strides[0]};
+    const cuuint32_t box[4] = {(cuuint32_t)c.head_dim, rows, 1, 1};
+    CUresult r = d.encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, codes, dims, st, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) {
+        const cuuint64_t st2[2] = {(cuuint64_t)c.page_size, (cuuint64_t)c.page_size * c.heads};
+        const cuuint32_t box2[3] = {rows, 1, 1};
+        r = d.encode(smap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, scales, dims + 1, st2, box2, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    }
+    if (r != CUDA_SUCCESS) return fail(SPEC_ERR_ARG, "cache: its layout has no tensor map (driver error %d)", (int)r);
+    return SPEC_OK;
+}
+
+// A call of attention, whichever entry point it came through (its cache is checked there).
+struct AttentionCall {
+    const void *q;
+    int64_t tokens;
+    int32_t heads_q;
+    int64_t q_token_stride, q_head_stride;
+    const spec_paged_cache *cache;      // one of the two
+    const spec_paged_cache8 *cache8;
+    const spec_paged_batch *batch;
+    const uint32_t *masks;
+    int32_t mask_words;
+    bool tree;
+    float scale;
+    int64_t window, max_new;
+    void *out;
+    float *lse;
+    void *workspace;
+    int64_t workspace_bytes;
+};
+
+spec_status attention_call(const AttentionCall &call)
+{
+    spec_status st = check_batch(call.batch);
+    if (st != SPEC_OK) return st;
+    const spec_paged_batch &b = *call.batch;
+    const bool eight = call.cache8 != nullptr;
+    struct { int32_t page_size, heads, head_dim, dtype; } c;   // of either cache
+    if (eight) c = {call.cache8->page_size, call.cache8->heads, call.cache8->head_dim, call.cache8->dtype};
+    else c = {call.cache->page_size, call.cache->heads, call.cache->head_dim, call.cache->dtype};
+    const int64_t tokens = call.tokens, window = call.window, max_new = call.max_new;
+    const int32_t heads_q = call.heads_q;
+    const void *q = call.q;
+    void *out = call.out, *workspace = call.workspace;
+    float *lse = call.lse;
+    if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256)
+        return fail(SPEC_ERR_ARG, "head_dim = %d: attention takes 64, 128 or 256", c.head_dim);
+    if (c.page_size < (eight ? 16 : 8) || (c.page_size & (c.page_size - 1)) != 0)
+        return fail(SPEC_ERR_ARG, "page_size = %d: attention takes powers of two from %d", c.page_size, eight ? 16 : 8);
+    if (b.page_size != c.page_size)
+        return fail(SPEC_ERR_ARG, "page_size of batch (%d) and cache (%d) differ", b.page_size, c.page_size);
+    if (tokens < 0 || tokens > INT32_MAX) return fail(SPEC_ERR_ARG, "tokens = %lld", (long long)tokens);
+    if (heads_q < 1 || heads_q % c.heads != 0)
+        return fail(SPEC_ERR_ARG, "heads_q = %d: need a positive multiple of the cache's %d heads", heads_q, c.heads);
+    if ((int64_t)tokens * heads_q > INT32_MAX) return fail(SPEC_ERR_ARG, "tokens * heads_q exceeds 2^31-1");
+    // the items of the step at most: row tiles of 128 rows, a partial one for each head of a lane with tokens
+    const int64_t items = tokens * heads_q / 128 + (tokens < b.lanes ? tokens : b.lanes) * c.heads;
+    if (items >= 1ll << (63 - attn::kItemBit))
+        return fail(SPEC_ERR_ARG, "tokens, lanes and heads make up to %lld row tiles, need fewer than 2^%d", (long long)items,
+                    63 - attn::kItemBit);
+    if (!(call.scale > 0.f) || !isfinite(call.scale))
+        return fail(SPEC_ERR_ARG, "scale = %g: must be positive and finite", call.scale);
+    if (window < 0) return fail(SPEC_ERR_ARG, "window = %lld < 0", (long long)window);
+    if (call.tree && window > 0 && window < SPEC_TREE_MAX_NODES)
+        return fail(SPEC_ERR_ARG, "window = %lld: a tree's is 0 or at least %d", (long long)window, SPEC_TREE_MAX_NODES);
+    if (call.tree && (call.mask_words < 1 || call.mask_words > SPEC_TREE_MAX_NODES / 32))
+        return fail(SPEC_ERR_ARG, "mask_words = %d outside [1, %d]", call.mask_words, SPEC_TREE_MAX_NODES / 32);
+    if (max_new < 0) return fail(SPEC_ERR_ARG, "max_new = %lld < 0", (long long)max_new);
+    if (bad_stride(call.q_token_stride) || bad_stride(call.q_head_stride))
+        return fail(SPEC_ERR_ARG, "strides must be non-negative multiples of 8 elements below 2^39");
+    if (tokens == 0 || b.lanes == 0) return SPEC_OK;
+    if (!q || !out || !b.block_table || !b.cu_new || !b.seq_lens || !workspace || (call.tree && !call.masks))
+        return fail(SPEC_ERR_ARG, "null pointer");
+    if (misaligned(q, 16) || misaligned(out, 16) || misaligned(workspace, 16) || misaligned(lse, 4) ||
+        misaligned(b.block_table, 4) || misaligned(b.cu_new, 4) || misaligned(b.seq_lens, 4) ||
+        misaligned(call.masks, 4))
+        return fail(SPEC_ERR_ARG, "misaligned pointer (q, out and workspace need 16 bytes, int32, masks and lse 4)");
+    // from q's first element to its last, whatever lies between its rows
+    const __int128 span = ((__int128)(tokens - 1) * call.q_token_stride + (__int128)(heads_q - 1) * call.q_head_stride + c.head_dim) * 2;
+    const Range in[] = {{q, span < INT64_MAX ? (int64_t)span : INT64_MAX, "q"}, {b.block_table, b.lanes * b.max_pages * 4, "block_table"},
+                        {b.cu_new, (b.lanes + 1) * 4, "cu_new"}, {b.seq_lens, b.lanes * 4, "seq_lens"},
+                        {call.masks, call.tree ? tokens * call.mask_words * 4 : 0, "masks"}};
+    const Range o = {out, tokens * heads_q * c.head_dim * 2, "out"}, ls = {lse, tokens * heads_q * 4, "lse"};
+    for (const Range &i : in)
+        for (const Range *w : {&o, &ls})
+            if (overlap(*w, i)) return fail(SPEC_ERR_ARG, "%s overlaps %s", w->name, i.name);
+    if (overlap(o, ls)) return fail(SPEC_ERR_ARG, "out overlaps lse");
+    const int64_t need = spec_paged_attention_workspace();
+    if (need < 0) return (spec_status)need;
+    if (call.workspace_bytes < need)
+        return fail(SPEC_ERR_ARG, "workspace: %lld bytes, the call needs %lld", (long long)call.workspace_bytes,
+                    (long long)need);
+    if (overlap(o, {workspace, need, ""}) || overlap(ls, {workspace, need, ""}))
+        return fail(SPEC_ERR_ARG, "out or lse overlaps workspace");
+    Device *d = nullptr;
+    st = device(&d);
+    if (st != SPEC_OK) return st;
+    attn::Args8 a;
+    memset(&a, 0, sizeof a);
+    if (eight) {
+        const spec_paged_cache8 &c8 = *call.cache8;
+        st = code_maps(*d, c8, c8.k, c8.k_strides, c8.k_scales, &a.kmap, &a.ksmap);
+        if (st == SPEC_OK) st = code_maps(*d, c8, c8.v, c8.v_strides, c8.v_scales, &a.vmap, &a.vsmap);
+    } else {
+        st = page_map(*d, *call.cache, call.cache->k, call.cache->k_strides, &a.kmap);
+        if (st == SPEC_OK) st = page_map(*d, *call.cache, call.cache->v, call.cache->v_strides, &a.vmap);
+    }
+    if (st != SPEC_OK) return st;
+    a.q = static_cast<const uint16_t *>(q);
+    a.tokens = tokens; a.qs_t = call.q_token_stride; a.qs_h = call.q_head_stride;
+    a.heads_q = heads_q; a.heads_kv = c.heads; a.group = heads_q / c.heads;
+    while ((1 << a.log_page) < c.page_size) ++a.log_page;
+    while ((1u << a.group_shift) < (uint32_t)a.group) ++a.group_shift;
+    a.group_magic = (uint32_t)((((1ull << a.group_shift) - a.group) << 32) / a.group + 1);
+    a.block_table = b.block_table; a.cu_new = b.cu_new; a.seq_lens = b.seq_lens;
+    a.lanes = (int32_t)b.lanes; a.max_pages = b.max_pages;
+    // (of tiles of 64 keys, the smaller; 2^31 - 2^16 unless there are 2^15 items)
+    const int64_t tiles = (1ll << attn::kItemBit) / items - 2;
+    a.most_keys = (int32_t)(tiles < (0x7FFF0000 >> 6) ? tiles << 6 : 0x7FFF0000);
+    a.c = call.scale * attn::kLog2e;
+    a.window = window > INT32_MAX ? 0 : window;   // past every position: none (and positions less it stay within 64 bits)
+    a.out = static_cast<uint16_t *>(out); a.lse = lse;
+    a.counters = static_cast<unsigned int *>(workspace);
+    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + SPEC_PAGED_WORKSPACE_ZEROED);
+    a.masks = call.tree ? call.masks : nullptr;
+    a.mask_words = call.mask_words;
+    const int64_t hint = max_new < tokens ? max_new : tokens, chunk = hint > 0 ? hint : (tokens + b.lanes - 1) / b.lanes;
+    const bool two = chunk * a.group > 128;   // more rows than one tile: two tiles share every K/V tile
+    const attn::Pick pick = {c.head_dim, two, c.dtype == SPEC_F16, chunk, d->index, attention_grid(*d)};
+    if (eight) return attn::launch8(a, pick, call.tree);
+    const attn::Args &a16 = a;
+    return call.tree ? attn::launch_tree(a16, pick) : attn::launch<false, false>(a16, pick);
+}
+
 }  // namespace
 
 namespace host {
 
-cudaError_t take_paged_timeouts(unsigned int *flags)
-{
-    cudaError_t e = cudaMemcpyFromSymbol(flags, g_wait_timeouts, sizeof *flags);
-    if (e != cudaSuccess || *flags == 0) return e;
-    const unsigned int zero = 0;
-    return cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof zero);
-}
+cudaError_t take_paged_timeouts(unsigned int *flags) { return take_flag(g_wait_timeouts, flags); }
 
 }  // namespace host
 
@@ -298,14 +325,8 @@ spec_status spec_paged_store(const void *k, const void *v, int64_t tokens, int64
     host::clear_error();
     spec_status st = check_cache(cache);
     if (st != SPEC_OK) return st;
-    if (tokens < 0 || tokens > INT32_MAX) return fail(SPEC_ERR_ARG, "tokens = %lld", (long long)tokens);
-    if (tokens == 0) return SPEC_OK;
-    if (!k || !v || !slots) return fail(SPEC_ERR_ARG, "null pointer");
-    if (misaligned(k, 16) || misaligned(v, 16) || misaligned(slots, 8))
-        return fail(SPEC_ERR_ARG, "misaligned pointer (keys and values need 16 bytes, slots 8)");
-    if (bad_stride(k_token_stride) || bad_stride(k_head_stride) || bad_stride(v_token_stride) ||
-        bad_stride(v_head_stride))
-        return fail(SPEC_ERR_ARG, "strides must be non-negative multiples of 8 elements below 2^39");
+    st = check_new(k, v, tokens, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots);
+    if (st != SPEC_OK || tokens == 0) return st;
     Device *d = nullptr;
     st = device(&d);
     if (st != SPEC_OK) return st;
@@ -332,82 +353,46 @@ spec_status spec_paged_attention(const void *q, int64_t tokens, int32_t heads_q,
                                  void *workspace, int64_t workspace_bytes)
 {
     host::clear_error();
-    spec_status st = check_cache(cache);
-    if (st == SPEC_OK) st = check_batch(batch);
+    const spec_status st = check_cache(cache);
     if (st != SPEC_OK) return st;
-    const spec_paged_cache &c = *cache;
-    const spec_paged_batch &b = *batch;
-    if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256)
-        return fail(SPEC_ERR_ARG, "head_dim = %d: attention takes 64, 128 or 256", c.head_dim);
-    if (c.page_size < 8 || (c.page_size & (c.page_size - 1)) != 0)
-        return fail(SPEC_ERR_ARG, "page_size = %d: attention takes powers of two from 8", c.page_size);
-    if (b.page_size != c.page_size)
-        return fail(SPEC_ERR_ARG, "page_size of batch (%d) and cache (%d) differ", b.page_size, c.page_size);
-    if (tokens < 0 || tokens > INT32_MAX) return fail(SPEC_ERR_ARG, "tokens = %lld", (long long)tokens);
-    if (heads_q < 1 || heads_q % c.heads != 0)
-        return fail(SPEC_ERR_ARG, "heads_q = %d: need a positive multiple of the cache's %d heads", heads_q, c.heads);
-    if ((int64_t)tokens * heads_q > INT32_MAX) return fail(SPEC_ERR_ARG, "tokens * heads_q exceeds 2^31-1");
-    // the items of the step at most: row tiles of 128 rows, a partial one for each head of a lane with tokens
-    const int64_t items = tokens * heads_q / 128 + (tokens < b.lanes ? tokens : b.lanes) * c.heads;
-    if (items >= 1ll << (63 - attn::kItemBit))
-        return fail(SPEC_ERR_ARG, "tokens, lanes and heads make up to %lld row tiles, need fewer than 2^%d", (long long)items,
-                    63 - attn::kItemBit);
-    if (!(scale > 0.f) || !isfinite(scale)) return fail(SPEC_ERR_ARG, "scale = %g: must be positive and finite", scale);
-    if (window < 0) return fail(SPEC_ERR_ARG, "window = %lld < 0", (long long)window);
-    if (max_new < 0) return fail(SPEC_ERR_ARG, "max_new = %lld < 0", (long long)max_new);
-    if (bad_stride(q_token_stride) || bad_stride(q_head_stride))
-        return fail(SPEC_ERR_ARG, "strides must be non-negative multiples of 8 elements below 2^39");
-    if (tokens == 0 || b.lanes == 0) return SPEC_OK;
-    if (!q || !out || !b.block_table || !b.cu_new || !b.seq_lens || !workspace) return fail(SPEC_ERR_ARG, "null pointer");
-    if (misaligned(q, 16) || misaligned(out, 16) || misaligned(workspace, 16) || misaligned(lse, 4) ||
-        misaligned(b.block_table, 4) || misaligned(b.cu_new, 4) || misaligned(b.seq_lens, 4))
-        return fail(SPEC_ERR_ARG, "misaligned pointer (q, out and workspace need 16 bytes, int32 and lse 4)");
-    // from q's first element to its last, whatever lies between its rows
-    const __int128 span = ((__int128)(tokens - 1) * q_token_stride + (__int128)(heads_q - 1) * q_head_stride + c.head_dim) * 2;
-    const Range in[] = {{q, span < INT64_MAX ? (int64_t)span : INT64_MAX, "q"}, {b.block_table, b.lanes * b.max_pages * 4, "block_table"},
-                        {b.cu_new, (b.lanes + 1) * 4, "cu_new"}, {b.seq_lens, b.lanes * 4, "seq_lens"}};
-    const Range o = {out, tokens * heads_q * c.head_dim * 2, "out"}, ls = {lse, tokens * heads_q * 4, "lse"};
-    for (const Range &i : in)
-        for (const Range *w : {&o, &ls})
-            if (overlap(*w, i)) return fail(SPEC_ERR_ARG, "%s overlaps %s", w->name, i.name);
-    if (overlap(o, ls)) return fail(SPEC_ERR_ARG, "out overlaps lse");
-    const int64_t need = spec_paged_attention_workspace();
-    if (need < 0) return (spec_status)need;
-    if (workspace_bytes < need)
-        return fail(SPEC_ERR_ARG, "workspace: %lld bytes, the call needs %lld", (long long)workspace_bytes,
-                    (long long)need);
-    if (overlap(o, {workspace, need, ""}) || overlap(ls, {workspace, need, ""}))
-        return fail(SPEC_ERR_ARG, "out or lse overlaps workspace");
-    Device *d = nullptr;
-    st = device(&d);
+    return attention_call({q, tokens, heads_q, q_token_stride, q_head_stride, cache, nullptr, batch, nullptr, 0, false, scale,
+                           window, max_new, out, lse, workspace, workspace_bytes});
+}
+
+spec_status spec_paged_attention8(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
+                                  int64_t q_head_stride, const spec_paged_cache8 *cache, const spec_paged_batch *batch,
+                                  float scale, int64_t window, int64_t max_new, void *out, float *lse,
+                                  void *workspace, int64_t workspace_bytes)
+{
+    host::clear_error();
+    const spec_status st = check_cache8(cache);
     if (st != SPEC_OK) return st;
-    attn::Args a;
-    memset(&a, 0, sizeof a);
-    st = page_map(*d, c, c.k, c.k_strides, &a.kmap);
-    if (st == SPEC_OK) st = page_map(*d, c, c.v, c.v_strides, &a.vmap);
+    return attention_call({q, tokens, heads_q, q_token_stride, q_head_stride, nullptr, cache, batch, nullptr, 0, false, scale,
+                           window, max_new, out, lse, workspace, workspace_bytes});
+}
+
+spec_status spec_tree_attention(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
+                                int64_t q_head_stride, const spec_paged_cache *cache, const spec_paged_batch *batch,
+                                const uint32_t *masks, int32_t mask_words, float scale, int64_t window, int64_t max_new,
+                                void *out, float *lse, void *workspace, int64_t workspace_bytes)
+{
+    host::clear_error();
+    const spec_status st = check_cache(cache);
     if (st != SPEC_OK) return st;
-    a.q = static_cast<const uint16_t *>(q);
-    a.tokens = tokens; a.qs_t = q_token_stride; a.qs_h = q_head_stride;
-    a.heads_q = heads_q; a.heads_kv = c.heads; a.group = heads_q / c.heads;
-    while ((1 << a.log_page) < c.page_size) ++a.log_page;
-    while ((1u << a.group_shift) < (uint32_t)a.group) ++a.group_shift;
-    a.group_magic = (uint32_t)((((1ull << a.group_shift) - a.group) << 32) / a.group + 1);
-    a.block_table = b.block_table; a.cu_new = b.cu_new; a.seq_lens = b.seq_lens;
-    a.lanes = (int32_t)b.lanes; a.max_pages = b.max_pages;
-    // (of tiles of 64 keys, the smaller; 2^31 - 2^16 unless there are 2^15 items)
-    const int64_t tiles = (1ll << attn::kItemBit) / items - 2;
-    a.most_keys = (int32_t)(tiles < (0x7FFF0000 >> 6) ? tiles << 6 : 0x7FFF0000);
-    a.c = scale * attn::kLog2e;
-    a.window = window > INT32_MAX ? 0 : window;   // past every position: none (and positions less it stay within 64 bits)
-    a.out = static_cast<uint16_t *>(out); a.lse = lse;
-    a.counters = static_cast<unsigned int *>(workspace);
-    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + SPEC_PAGED_WORKSPACE_ZEROED);
-    const int64_t hint = max_new < tokens ? max_new : tokens, chunk = hint > 0 ? hint : (tokens + b.lanes - 1) / b.lanes;
-    const bool two = chunk * a.group > 128;   // more rows than one tile: two tiles share every K/V tile
-    const bool f16 = c.dtype == SPEC_F16;
-    if (c.head_dim == 256) return launch_attention<256, 1>(*d, a, chunk, f16);
-    if (c.head_dim == 128) return two ? launch_attention<128, 2>(*d, a, chunk, f16) : launch_attention<128, 1>(*d, a, chunk, f16);
-    return two ? launch_attention<64, 2>(*d, a, chunk, f16) : launch_attention<64, 1>(*d, a, chunk, f16);
+    return attention_call({q, tokens, heads_q, q_token_stride, q_head_stride, cache, nullptr, batch, masks, mask_words, true,
+                           scale, window, max_new, out, lse, workspace, workspace_bytes});
+}
+
+spec_status spec_tree_attention8(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
+                                 int64_t q_head_stride, const spec_paged_cache8 *cache, const spec_paged_batch *batch,
+                                 const uint32_t *masks, int32_t mask_words, float scale, int64_t window, int64_t max_new,
+                                 void *out, float *lse, void *workspace, int64_t workspace_bytes)
+{
+    host::clear_error();
+    const spec_status st = check_cache8(cache);
+    if (st != SPEC_OK) return st;
+    return attention_call({q, tokens, heads_q, q_token_stride, q_head_stride, nullptr, cache, batch, masks, mask_words, true,
+                           scale, window, max_new, out, lse, workspace, workspace_bytes});
 }
 
 spec_status spec_logits_process(const uint16_t *logits, int64_t lanes, int32_t cols, int64_t V,

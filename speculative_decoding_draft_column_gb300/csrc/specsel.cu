@@ -1096,10 +1096,14 @@ spec_status spec_device_status(void)
     unsigned int flags = 0, zero = 0;
     e = cudaMemcpyFromSymbol(&flags, g_wait_timeouts, sizeof flags);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyFromSymbol");
-    unsigned int paged = 0;
-    e = host::take_paged_timeouts(&paged);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyFromSymbol");
-    if ((flags | paged) == 0) return SPEC_OK;
+    for (auto take : {host::take_paged_timeouts, host::take_tree_attention_timeouts, host::take_attention8_timeouts,
+                      host::take_tree_timeouts}) {
+        unsigned int more = 0;
+        e = take(&more);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyFromSymbol");
+        flags |= more;
+    }
+    if (flags == 0) return SPEC_OK;
     e = cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof zero);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyToSymbol");
     return fail(SPEC_ERR_CUDA, "a kernel gave up a bounded wait on its copy pipeline; its results are invalid");
@@ -1231,6 +1235,21 @@ spec_status fail(spec_status st, const char *fmt, ...)
     va_end(ap);
     t_err = buf;
     return st;
+}
+
+
+bool lane_scratch(int64_t lanes, int64_t entries, unsigned int **tickets, unsigned long long **lists)
+{
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState *d = nullptr;
+    spec_status st = device_state(&d);
+    if (st == SPEC_OK) st = ensure_scratch(*d, {0, lanes, entries}, t_stream);
+    t_err.clear();
+    if (st != SPEC_OK) return false;
+    const ScratchPtrs sp = scratch_ptrs(*d);
+    *tickets = sp.lane_ticket;
+    *lists = sp.partials;
+    return true;
 }
 
 }  // namespace host

@@ -1,4 +1,4 @@
-"""Binding of the paged cache and the logits rules (see ``include/specsel.h``).
+"""Binding of the paged cache (16 and 8 bits), the rounds of trees and the logits rules (see ``include/specsel.h``).
 
 ``PagedCache`` and ``PagedBatch`` describe a caller's tensors to the library:
 they check them once, keep them alive and hold the C struct; they own no data
@@ -14,6 +14,7 @@ from . import SPEC_ERR_ARG, SpecError, _check, _n, lib
 
 SPEC_BF16, SPEC_F16 = 0, 1
 SPEC_PAGED_MAX_LANES, SPEC_PAGED_WORKSPACE_ZEROED = 4096, 4096
+SPEC_TREE_MAX_NODES = 256
 
 _p, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 
@@ -21,6 +22,11 @@ _p, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 class _CacheStruct(ctypes.Structure):
     _fields_ = [("k", _p), ("v", _p), ("k_strides", _i64 * 3), ("v_strides", _i64 * 3), ("pages", _i64),
                 ("page_size", _i32), ("heads", _i32), ("head_dim", _i32), ("dtype", _i32)]
+
+
+class _Cache8Struct(ctypes.Structure):
+    _fields_ = [("k", _p), ("v", _p), ("k_scales", _p), ("v_scales", _p), ("k_strides", _i64 * 3), ("v_strides", _i64 * 3),
+                ("pages", _i64), ("page_size", _i32), ("heads", _i32), ("head_dim", _i32), ("dtype", _i32)]
 
 
 class _BatchStruct(ctypes.Structure):
@@ -111,6 +117,11 @@ def _rows_of(x, lanes, name):
     return shape[1]
 
 
+def _is_cache(cache, kind):
+    if type(cache) is not kind and not isinstance(cache, kind):
+        _bad(f"cache: a {type(cache).__name__}, the call takes a {kind.__name__}")
+
+
 def _on_current_device(index, name):
     cur = _torch().cuda.current_device()
     if index != cur:
@@ -140,6 +151,50 @@ class PagedCache:
         self._c = _CacheStruct(k.data_ptr(), v.data_ptr(), three(*k.stride()[:3]), three(*v.stride()[:3]), self.pages,
                                self.page_size, self.heads, self.head_dim, _dtype_code(k, "k"))
         self._ref = ctypes.byref(self._c)
+
+
+class PagedCache8:
+    """Keys and values of one layer in 8 bits: codes in two CUDA tensors [pages, page_size, heads,
+    head_dim] (torch.float8_e4m3fn, or uint8 with the same bits), any strides over the first three
+    dimensions, and their scales in two contiguous uint8 tensors [pages, heads, page_size].  ``dtype``
+    (torch.bfloat16 or torch.float16) is what is stored from and attended with."""
+
+    def __init__(self, k, k_scales, v, v_scales, *, dtype=None):
+        import torch
+        dtype = torch.bfloat16 if dtype is None else dtype
+        for x, name in ((k, "k"), (v, "v")):
+            if not getattr(x, "is_cuda", False):
+                _bad(f"{name}: need a CUDA tensor")
+            if x.dtype not in (torch.float8_e4m3fn, torch.uint8):
+                _bad(f"{name}: dtype {x.dtype}, need float8_e4m3fn or uint8")
+            if x.dim() != 4:
+                _bad(f"{name}: need [pages, page_size, heads, head_dim], got {tuple(x.shape)}")
+            if x.stride(3) != 1:
+                _bad(f"{name}: the last dimension must be contiguous")
+        if k.shape != v.shape or k.device != v.device:
+            _bad("k and v must have one shape and device")
+        self.pages, self.page_size, self.heads, self.head_dim = k.shape
+        self.device, self.torch_dtype = k.device.index, dtype
+        for x, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            _array(x, torch.uint8, self.pages * self.heads * self.page_size, self.device, name)
+            if tuple(x.shape) != (self.pages, self.heads, self.page_size):
+                _bad(f"{name}: shape {tuple(x.shape)}, need [pages, heads, page_size]")
+        if dtype not in (torch.bfloat16, torch.float16):
+            _bad(f"dtype {dtype}: need bfloat16 or float16")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        three = _i64 * 3
+        self._c = _Cache8Struct(k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                                three(*k.stride()[:3]), three(*v.stride()[:3]), self.pages, self.page_size, self.heads,
+                                self.head_dim, SPEC_BF16 if dtype is torch.bfloat16 else SPEC_F16)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def create(cls, pages, page_size, heads, head_dim, dtype=None, device="cuda"):
+        """A cache of its own zeroed codes and scales."""
+        import torch
+        z = lambda *n: torch.zeros(n, dtype=torch.uint8, device=device)  # noqa: E731
+        shape, scales = (pages, page_size, heads, head_dim), (pages, heads, page_size)
+        return cls(z(*shape), z(*scales), z(*shape), z(*scales), dtype=dtype)
 
 
 class PagedBatch:
@@ -209,17 +264,27 @@ def spec_paged_plan(batch, free_pages, cursor=None):
         _check(st)
 
 
-def spec_paged_store(k, v, slots, cache):
-    """Store k, v [tokens, heads, head_dim] at slots int64 [tokens] of the cache."""
+def _store(call, kind, k, v, slots, cache):
+    _is_cache(cache, kind)
     tokens = k.shape[0]
     shape = (tokens, cache.heads, cache.head_dim)
     ks, vs = _rows(k, shape, cache, "k"), _rows(v, shape, cache, "v")
     dev = _on_current_device(cache.device, "cache")
     sl = _array(slots, _torch().int64, tokens, dev, "slots")
     _set_stream(dev)
-    st = lib.spec_paged_store(k.data_ptr(), v.data_ptr(), tokens, ks[0], ks[1], vs[0], vs[1], sl, cache._ref)
+    st = call(k.data_ptr(), v.data_ptr(), tokens, ks[0], ks[1], vs[0], vs[1], sl, cache._ref)
     if st:
         _check(st)
+
+
+def spec_paged_store(k, v, slots, cache):
+    """Store k, v [tokens, heads, head_dim] at slots int64 [tokens] of the cache."""
+    _store(lib.spec_paged_store, PagedCache, k, v, slots, cache)
+
+
+def spec_paged_store8(k, v, slots, cache):
+    """The same into a PagedCache8, quantised: a power-of-two scale a vector, e4m3 codes."""
+    _store(lib.spec_paged_store8, PagedCache8, k, v, slots, cache)
 
 
 def spec_paged_attention_workspace() -> int:
@@ -239,9 +304,8 @@ def new_attention_workspace(device="cuda"):
         return ws
 
 
-def spec_paged_attention(q, cache, batch, scale, out, lse, workspace, window=0, max_new=0):
-    """Attention of the batch's new tokens: q [tokens, heads_q, head_dim] into
-    out (same shape, contiguous) and lse fp32 [tokens, heads_q] (or None)."""
+def _attention(call, kind, q, cache, batch, tree, scale, out, lse, workspace, window, max_new):
+    _is_cache(cache, kind)
     shape = q.shape
     qs = _rows(q, None, cache, "q")
     dev = _on_current_device(cache.device, "cache")
@@ -253,11 +317,116 @@ def spec_paged_attention(q, cache, batch, scale, out, lse, workspace, window=0, 
     o = _array(out, cache.torch_dtype, tokens * heads_q * dim, dev, "out")
     ls = None if lse is None else _array(lse, _torch().float32, tokens * heads_q, dev, "lse")
     ws = _array(workspace, workspace.dtype, 0, dev, "workspace")
+    if tree is not None:
+        if tree.dim() != 2 or tree.shape[0] < tokens:
+            _bad(f"masks: need [tokens, words], got {tuple(tree.shape)}")
+        words = tree.shape[1]
+        tree = (_array(tree, _torch().int32, tokens * words, dev, "masks"), words)
     _set_stream(dev)
-    st = lib.spec_paged_attention(q.data_ptr(), tokens, heads_q, qs[0], qs[1], cache._ref, batch._ref, scale, window,
-                                  max_new, o, ls, ws, workspace.numel() * workspace.element_size())
+    st = call(q.data_ptr(), tokens, heads_q, qs[0], qs[1], cache._ref, batch._ref, *(tree or ()), scale, window,
+              max_new, o, ls, ws, workspace.numel() * workspace.element_size())
     if st:
         _check(st)
+
+
+def spec_paged_attention(q, cache, batch, scale, out, lse, workspace, window=0, max_new=0):
+    """Attention of the batch's new tokens: q [tokens, heads_q, head_dim] into
+    out (same shape, contiguous) and lse fp32 [tokens, heads_q] (or None)."""
+    _attention(lib.spec_paged_attention, PagedCache, q, cache, batch, None, scale, out, lse, workspace, window, max_new)
+
+
+def spec_paged_attention8(q, cache, batch, scale, out, lse, workspace, window=0, max_new=0):
+    """The same over a PagedCache8."""
+    _attention(lib.spec_paged_attention8, PagedCache8, q, cache, batch, None, scale, out, lse, workspace, window, max_new)
+
+
+def spec_tree_attention(q, cache, batch, masks, scale, out, lse, workspace, window=0, max_new=0):
+    """Attention where a lane's new tokens are the nodes of a tree: masks int32 [tokens, words], bit b of word w
+    set where the token sees its lane's new token 32 w + b (``spec_tree_plan`` writes them)."""
+    _attention(lib.spec_tree_attention, PagedCache, q, cache, batch, masks, scale, out, lse, workspace, window, max_new)
+
+
+def spec_tree_attention8(q, cache, batch, masks, scale, out, lse, workspace, window=0, max_new=0):
+    """The same over a PagedCache8."""
+    _attention(lib.spec_tree_attention8, PagedCache8, q, cache, batch, masks, scale, out, lse, workspace, window, max_new)
+
+
+def spec_tree_plan(parents, batch, masks, positions):
+    """Masks int32 [tokens, words] and positions int32 [tokens] of the step's trees, from parents int32 [tokens]."""
+    t = _torch()
+    dev = _on_current_device(batch.device, "batch")
+    tokens = parents.numel()
+    if masks.dim() != 2 or masks.shape[0] != tokens:
+        _bad(f"masks: need [{tokens}, words], got {tuple(masks.shape)}")
+    words = masks.shape[1]
+    p, m = _array(parents, t.int32, tokens, dev, "parents"), _array(masks, t.int32, tokens * words, dev, "masks")
+    at = _array(positions, t.int32, tokens, dev, "positions")
+    _set_stream(dev)
+    st = lib.spec_tree_plan(p, tokens, batch._ref, m, words, at)
+    if st:
+        _check(st)
+
+
+def _tree_arrays(logits, drafts, parents, cu, lanes, depth, V, accept, commit, path):
+    t = _torch()
+    dev = t.cuda.current_device()
+    if logits.dtype is not t.bfloat16 and logits.dtype not in (t.int16, t.uint16):
+        _bad(f"target_logits: dtype {logits.dtype} is not bf16 bits")
+    tokens, ln, width = drafts.numel(), _n(lanes), _n(depth) + 1
+    i32 = t.int32
+    return (dev, tokens, (_array(logits, logits.dtype, tokens * _n(V), dev, "target_logits"), _array(drafts, i32, tokens, dev, "drafts"),
+                          _array(parents, i32, tokens, dev, "parents"), _array(cu, i32, ln + 1, dev, "cu")),
+            (_array(accept, i32, ln, dev, "out_accept_len"), _array(commit, i32, ln * width, dev, "out_commit_ids"),
+             _array(path, i32, ln * width, dev, "out_path")))
+
+
+def spec_tree_verify(target_logits, drafts, parents, cu, lanes, depth, V, out_accept_len, out_commit_ids, out_path):
+    """Greedy verify of trees: bf16 target_logits [tokens, V], drafts and parents int32 [tokens], cu int32 [lanes+1]
+    into int32 [lanes], [lanes, depth+1] and [lanes, depth+1]."""
+    dev, tokens, ins, outs = _tree_arrays(target_logits, drafts, parents, cu, lanes, depth, V, out_accept_len,
+                                          out_commit_ids, out_path)
+    _set_stream(dev)
+    st = lib.spec_tree_verify(*ins, tokens, lanes, depth, V, *outs)
+    if st:
+        _check(st)
+
+
+def spec_tree_verify_sampled(target_logits, drafts, parents, cu, lanes, depth, V, temperature, top_p, top_k, uniforms,
+                             out_accept_len, out_commit_ids, out_path):
+    """Sampled verify of trees; uniforms float64 [tokens, 2]."""
+    dev, tokens, ins, outs = _tree_arrays(target_logits, drafts, parents, cu, lanes, depth, V, out_accept_len,
+                                          out_commit_ids, out_path)
+    u = _array(uniforms, _torch().float64, 2 * tokens, dev, "uniforms")
+    _set_stream(dev)
+    st = lib.spec_tree_verify_sampled(*ins, tokens, lanes, depth, V, temperature, top_p, top_k, u, *outs)
+    if st:
+        _check(st)
+
+
+def _commit(call, kind, cache, batch, path, accept_lens, depth, context_out):
+    _is_cache(cache, kind)
+    i32 = _torch().int32
+    dev = _on_current_device(cache.device, "cache")
+    if batch.device != dev:
+        _bad("batch and cache are on different devices")
+    p = _array(path, i32, batch.lanes * (_n(depth) + 1), dev, "path")
+    a = _array(accept_lens, i32, batch.lanes, dev, "accept_lens")
+    c = None if context_out is None else _array(context_out, i32, batch.lanes, dev, "context_out")
+    _set_stream(dev)
+    st = call(cache._ref, batch._ref, p, a, depth, c)
+    if st:
+        _check(st)
+
+
+def spec_tree_commit(cache, batch, path, accept_lens, depth, context_out=None):
+    """Move the accepted nodes' keys and values to where a row of tokens has them; the next step's
+    context lengths into ``context_out`` int32 [lanes] (or None)."""
+    _commit(lib.spec_tree_commit, PagedCache, cache, batch, path, accept_lens, depth, context_out)
+
+
+def spec_tree_commit8(cache, batch, path, accept_lens, depth, context_out=None):
+    """The same in a PagedCache8."""
+    _commit(lib.spec_tree_commit8, PagedCache8, cache, batch, path, accept_lens, depth, context_out)
 
 
 def spec_logits_process(logits, lanes, cols, V, out, *, history=None, prompt_lens=None, history_lens=None,
@@ -318,17 +487,37 @@ def spec_logits_process(logits, lanes, cols, V, out, *, history=None, prompt_len
 
 # ---- allocating conveniences ------------------------------------------------
 
-def paged_attention(q, cache, batch, scale=None, window=0, max_new=0, workspace=None):
-    """(out, lse) of spec_paged_attention; a fresh workspace unless one is given.
+def paged_attention(q, cache, batch, scale=None, window=0, max_new=0, workspace=None, masks=None):
+    """(out, lse) of spec_paged_attention, spec_tree_attention (with ``masks``) or, for a PagedCache8, their 8-bit
+    forms; a fresh workspace unless one is given.
     Rows past the step's tokens are not written and hold anything."""
     import torch
     out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = new_attention_workspace(q.device)
-    spec_paged_attention(q, cache, batch, cache.head_dim ** -0.5 if scale is None else scale, out, lse, workspace,
-                         window, max_new)
+    scale = cache.head_dim ** -0.5 if scale is None else scale
+    eight = isinstance(cache, PagedCache8)
+    if masks is None:
+        (spec_paged_attention8 if eight else spec_paged_attention)(q, cache, batch, scale, out, lse, workspace, window, max_new)
+    else:
+        (spec_tree_attention8 if eight else spec_tree_attention)(q, cache, batch, masks, scale, out, lse, workspace, window,
+                                                                 max_new)
     return out, lse
+
+
+def tree_verify(target_logits, drafts, parents, cu, depth, uniforms=None, temperature=1.0, top_p=1.0, top_k=64):
+    """(accept_lens, commit_ids, path) of spec_tree_verify or, with uniforms, spec_tree_verify_sampled."""
+    import torch
+    lanes, V = cu.numel() - 1, target_logits.shape[-1]
+    e = lambda *n: torch.empty(n, dtype=torch.int32, device=cu.device)  # noqa: E731
+    acc, commit, path = e(lanes), e(lanes, depth + 1), e(lanes, depth + 1)
+    if uniforms is None:
+        spec_tree_verify(target_logits, drafts, parents, cu, lanes, depth, V, acc, commit, path)
+    else:
+        spec_tree_verify_sampled(target_logits, drafts, parents, cu, lanes, depth, V, temperature, top_p, min(top_k, V),
+                                 uniforms, acc, commit, path)
+    return acc, commit, path
 
 
 def process_logits(logits, lanes, cols, **rules):
