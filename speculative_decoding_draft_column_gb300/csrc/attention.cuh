@@ -87,14 +87,14 @@ struct Shape {
     static constexpr int kStageBytes = BK * D * 2;             // a K or a V tile
     static constexpr int QB = QT == 1 && D <= (kQ8 ? 64 : 128) ? 2 : 1;   // Q buffers
     static constexpr int kRoom = 224 * 1024 - QB * QT * kQBytes;
-    // 8 bits: as many 16-bit tiles as keep the products fed, the rest for codes on their way
-    static constexpr int kStages = kQ8 ? (D == 64 ? 4 : 3) : kRoom / kStageBytes < 12 ? kRoom / kStageBytes : 12;
+    // 8 bits: as many 16-bit tiles as keep the products fed, the rest for tiles of codes on their way
+    static constexpr int kStages = kQ8 ? (D == 64 ? 6 : 3) : kRoom / kStageBytes < 12 ? kRoom / kStageBytes : 12;
     static constexpr int kRawCodes = BK * D;                   // codes of a tile, then 128 bytes for a page's scales
     static constexpr int kRawBytes = kRawCodes + BK / 16 * 128;
     static constexpr int kRawMost = (kRoom - kStages * kStageBytes) / kRawBytes;
-    static constexpr int kRaw = !kQ8 ? 0 : kRawMost < 8 ? kRawMost : 8;
+    static constexpr int kRaw = !kQ8 ? 0 : kRawMost < 6 ? kRawMost : 6;
     static constexpr int kSoftmaxWarps = NS * 8;
-    static constexpr int kConverters = kQ8 ? 4 : 0;            // warps
+    static constexpr int kConverters = kQ8 ? 8 : 0;            // warps
     static constexpr int kThreads = kSoftmaxWarps * 32 + 128 + kConverters * 32;  // softmax; K/V loader, MMA, two Q loaders; converters
     static constexpr int kSwap = 512;                          // floats that softmax warps exchange through
     static constexpr int kPayload = QB * QT * kQBytes + kStages * kStageBytes + kRaw * kRawBytes + kSwap * 4;
@@ -352,19 +352,12 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, i
                  : "memory");
 }
 
-// 8 bits: `rows` vectors of codes of a page, and their scales
-__device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap *map, int row, int head, int page, uint64_t *bar)
+// 8 bits: codes of a page's vectors (x: 0, y: the first), or their scales (x: the first, y: 0)
+__device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap *map, int x, int y, int head, int page, uint64_t *bar)
 {
     asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
                  "%4, %5}], [%6];" ::"r"(dst),
-                 "l"(map), "r"(0), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void tma_scales(uint32_t dst, const CUtensorMap *map, int row, int head, int page, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-                 "%4}], [%5];" ::"r"(dst),
-                 "l"(map), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
+                 "l"(map), "r"(x), "r"(y), "r"(head), "r"(page), "r"(smem_u32(bar))
                  : "memory");
 }
 
@@ -533,7 +526,7 @@ constexpr int kItems = 4;
 template <typename S>
 struct Bars {
     uint64_t full[S::kStages], empty[S::kStages];
-    uint64_t raw_full[S::kRaw + 1], raw_empty[S::kRaw + 1];   // of the codes (8 bits)
+    uint64_t raw_full[S::kRaw + 1], raw_empty[S::kRaw + 1];   // of the codes' tiles (8 bits)
     uint64_t s_full[2], p_full[2], o_done[2];
     uint64_t q_full[2], q_empty[2], item_full[kItems], item_empty[kItems], drain;
     uint64_t part_full[2], part_known[2];   // the part in a slot is written; the others know
@@ -566,13 +559,12 @@ constexpr int kAllSoftmax = 9;   // barrier ids: 1 .. 8 a pair of warps with the
 // widened by their bits.  e4m3's bits, shifted into bf16's places, are the value times
 // 2^-120 (the exponents' offsets are 7 and 127; fractions of 0 exponent go along), so that one multiplication
 // by 2^(120 + exponent) gives the value, exactly; in fp16 the conversion is an
-// instruction of its own, and the factor 2^exponent.  255 stands for a vector that is no number.
+// instruction of its own, and the factor 2^exponent.  Above 134 (255 is stored) stands for a vector that is no number.
 template <bool F16>
 __device__ __forceinline__ uint32_t scale_pair(uint32_t byte)
 {
-    const uint32_t b = byte < 134u ? byte : 134u;
-    const uint32_t h = byte == 255u ? (F16 ? 0x7E00u : 0x7FC0u) : F16 ? ((b < 113u ? 113u : b) - 112u) << 10 : (b + 120u) << 7;
-    return h | h << 16;
+    const uint32_t h = byte > 134u ? (F16 ? 0x7E00u : 0x7FC0u) : F16 ? ((byte < 113u ? 113u : byte) - 112u) << 10 : (byte + 120u) << 7;
+    return __byte_perm(h, 0u, 0x1010);
 }
 
 // Four codes to four 16-bit values.
@@ -585,56 +577,72 @@ __device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t scale)
             "cvt.rn.f16x2.e4m3x2 y, h;\n\tmul.rn.f16x2 %0, x, %3;\n\tmul.rn.f16x2 %1, y, %3;\n\t}"
             : "=r"(r.x), "=r"(r.y) : "r"(w), "r"(scale));
     } else {
-        const uint32_t x = __byte_perm(w, 0u, 0x1404), y = __byte_perm(w, 0u, 0x3424);   // a code in the upper byte of each half
-        const uint32_t bx = (x & 0x80008000u) | (x >> 4 & 0x07F007F0u), by = (y & 0x80008000u) | (y >> 4 & 0x07F007F0u);
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(bx), "r"(scale));
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(by), "r"(scale));
+        // s eeee mmm -> s 0000 eee, e mmm 0000: the four upper bytes, the four lower ones, and pairs of them
+        const uint32_t hi = (w >> 4 & 0x07070707u) | (w & 0x80808080u), lo = w << 4 & 0xF0F0F0F0u;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(__byte_perm(lo, hi, 0x5140)), "r"(scale));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(__byte_perm(lo, hi, 0x7362)), "r"(scale));
     }
     return r;
 }
 
 // The converting warps (8 bits): each tile of codes, as it lands, into a 16-bit tile in the
-// layout of the products' operands.  A thread takes 16 codes of a row at a time; lanes of the
-// second block of 64 elements write their two pieces in the other order, so that the eight
-// threads of a row are on different banks.
+// layout of the products' operands.  A thread takes 16 codes of a row at a time; lanes of every
+// second block of 64 elements write their two pieces in the other order, so that eight lanes
+// are on different banks.
 template <typename S, bool F16>
-__device__ __forceinline__ void convert_tiles(Bars<S> &bar, Item *items, const uint8_t *raw_smem, uint8_t *kv_smem, int rows,
+__device__ __forceinline__ void convert_tiles(Bars<S> &bar, const Item *items, const uint8_t *raw_smem, uint8_t *kv_smem, int rows,
                                               int warp, int lane)
 {
-    constexpr int kPieces = S::D / 16, kStep = S::kConverters * 32 / kPieces;   // threads a row, rows a pass
+    constexpr int kPieces = S::D / 16, kStep = S::kConverters * 32 / kPieces, kPasses = S::BK / kStep;   // lanes a row, rows a pass
+    static_assert(kStep % 8 == 0 && S::BK % kStep == 0, "a thread's rows have one place in the swizzle");
     const int id = warp * 32 + lane, p = id % kPieces, r0 = id / kPieces;
-    const int log_rows = 31 - __clz(rows);
     const int block = p >> 2, piece = (p & 3) * 2, flip = block & 1;
-    uint32_t idx = 0;
-    bool ok = true;
-    for (uint32_t n = 0; ok; ++n) {
-        if (!__all_sync(kFull, wait(&bar.item_full[n % kItems], (n / kItems) & 1))) break;
+    // where the thread's pieces go, and the scale of each of its rows
+    const uint32_t x0 = ((piece + flip) ^ (r0 & 7)) << 4, x1 = x0 ^ 16;
+    uint8_t *const to = kv_smem + block * (S::BK * 128) + r0 * 128;
+    const int log_rows = 31 - __clz(rows);
+    int at[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) at[i] = S::kRawCodes + ((r0 + i * kStep) >> log_rows) * 128 + ((r0 + i * kStep) & (rows - 1));
+    uint32_t rs = 0, rs_phase = 0, st = 0, st_phase = 0;     // the next tile's slot and stage, K and V in turn
+    for (uint32_t n = 0;; ++n) {
+        if (!__all_sync(kFull, wait(&bar.item_full[n % kItems], (n / kItems) & 1))) return;
         const int tiles = items[n % kItems].tiles;
         __syncwarp();
-        if (tiles == 0) break;
+        if (tiles == 0) return;
         if (lane == 0) mbar_arrive(&bar.item_empty[n % kItems]);
-        for (int t = 0; t < 2 * tiles; ++t, ++idx) {
-            const uint32_t rs = idx % S::kRaw, st = idx % S::kStages;
-            ok = wait(&bar.raw_full[rs], (idx / S::kRaw) & 1) && wait(&bar.empty[st], ((idx / S::kStages) & 1) ^ 1);
-            ok = __all_sync(kFull, ok);
-            if (!ok) break;
-            const uint8_t *codes = raw_smem + rs * S::kRawBytes, *scales = codes + S::kRawCodes;
-            uint8_t *tile = kv_smem + st * S::kStageBytes + block * (S::BK * 128);
-#pragma unroll 4
-            for (int r = r0; r < S::BK; r += kStep) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(codes + r * S::D + p * 16);
-                const uint32_t f = scale_pair<F16>(scales[(r >> log_rows) * 128 + (r & (rows - 1))]);
-                const uint2 a = widen4<F16>(w.x, f), b = widen4<F16>(w.y, f), c = widen4<F16>(w.z, f), d = widen4<F16>(w.w, f);
-                const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, d.x, d.y);
-                uint8_t *row = tile + r * 128;
-                *reinterpret_cast<uint4 *>(row + (((piece + flip) ^ (r & 7)) << 4)) = flip ? hi : lo;
-                *reinterpret_cast<uint4 *>(row + (((piece + (flip ^ 1)) ^ (r & 7)) << 4)) = flip ? lo : hi;
+        for (int t = 0; t < 2 * tiles; ++t) {
+            if (!__all_sync(kFull, wait(&bar.empty[st], st_phase ^ 1) && wait(&bar.raw_full[rs], rs_phase))) return;
+            const uint8_t *raw = raw_smem + rs * S::kRawBytes;
+            uint8_t *tile = to + st * S::kStageBytes;
+            uint4 w[kPasses];
+            uint32_t f[kPasses];
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                w[i] = *reinterpret_cast<const uint4 *>(raw + id * 16 + i * (kStep * S::D));
+                f[i] = raw[at[i]];
+            }
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const uint32_t k = scale_pair<F16>(f[i]);
+                const uint2 b0 = widen4<F16>(w[i].x, k), b1 = widen4<F16>(w[i].y, k), b2 = widen4<F16>(w[i].z, k), b3 = widen4<F16>(w[i].w, k);
+                const uint4 u = make_uint4(b0.x, b0.y, b1.x, b1.y), v = make_uint4(b2.x, b2.y, b3.x, b3.y);
+                *reinterpret_cast<uint4 *>(tile + i * (kStep * 128) + x0) = flip ? v : u;
+                *reinterpret_cast<uint4 *>(tile + i * (kStep * 128) + x1) = flip ? u : v;
             }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&bar.full[st]);
                 mbar_arrive(&bar.raw_empty[rs]);
+                mbar_arrive(&bar.full[st]);
+            }
+            if (++rs == (uint32_t)S::kRaw) {
+                rs = 0;
+                rs_phase ^= 1;
+            }
+            if (++st == (uint32_t)S::kStages) {
+                st = 0;
+                st_phase ^= 1;
             }
         }
     }
@@ -824,17 +832,20 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
             }
         }
         const int rows = min(1 << a.log_page, S::BK);            // rows of a box
-        const int boxes = S::BK / rows;
-        const bool whole = rows == S::BK;                        // one box brings all blocks
+        const int boxes = S::BK / rows, box = Q8 ? lane & 7 : lane;   // (8 bits: 8 at most)
+        const bool whole = !Q8 && rows == S::BK;                 // one box brings all blocks
         const uint32_t box_bytes = (uint32_t)rows * (Q8 ? D + 1 : D * 2);
         constexpr uint32_t kRing = Q8 ? S::kRaw : S::kStages;    // where the copies land
-        uint64_t *landed = Q8 ? bar.raw_full : bar.full, *room = Q8 ? bar.raw_empty : bar.empty;
+        uint64_t *landed = Q8 ? bar.raw_full : bar.full;
         auto page_of = [&](const Segment &s, int t) -> int {     // of this lane's box of tile t
-            const int64_t k0 = (int64_t)(s.tile + t) * S::BK + lane * rows, pi = k0 >> a.log_page;
-            return lane < boxes && k0 < s.r.hi && k0 + rows > s.r.lo && pi < a.max_pages
+            const int64_t k0 = (int64_t)(s.tile + t) * S::BK + box * rows, pi = k0 >> a.log_page;
+            return box < boxes && k0 < s.r.hi && k0 + rows > s.r.lo && pi < a.max_pages
                        ? __ldg(a.block_table + s.lane * a.max_pages + pi) : -1;
         };
-        uint32_t idx = 0;                                        // stage uses so far
+        uint32_t idx = 0;                                        // stage uses so far (8 bits: of slots)
+        [[maybe_unused]] uint32_t slot = 0, phase = 0;           // 8 bits: the next slot, the parity of its use, what this lane copies
+        [[maybe_unused]] const CUtensorMap *map8 = &a.kmap;
+        if constexpr (Q8) map8 = lane < 8 ? &a.kmap : lane < 16 ? &a.vmap : lane < 24 ? &a.ksmap : &a.vsmap;
         bool ok = true;
         if (lane < 2) joins[lane].n = joins[lane].count = joins[lane].lg = came_last[lane] = 0;
         __syncwarp();
@@ -857,7 +868,36 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
             }
             __syncwarp();
             if (!more) break;
-            for (int t = 0; t < s.tiles && ok; ++t) {
+            if constexpr (Q8) {
+                // K and V of a tile at once, eight lanes each for the codes of K, of V, the scales of K, of V
+                for (int t = 0; t < s.tiles && ok; ++t) {
+                    const int k0 = (s.tile + t) * S::BK + box * rows, row = k0 & ((1 << a.log_page) - 1);
+                    const bool mine = box < boxes && k0 < s.r.hi && k0 + rows > s.r.lo;
+                    const uint32_t bytes = __popc(__ballot_sync(kFull, mine) & 0xFFu) * (uint32_t)(rows * (D + 1));
+                    const int next_page = t + 1 < s.tiles ? page_of(s, t + 1) : -1;   // on its way while this tile's copies wait for room
+                    const bool v = (lane >> 3) & 1;
+                    const uint32_t second = slot + 1 < (uint32_t)S::kRaw ? slot + 1 : 0, mine_slot = v ? second : slot;
+                    ok = __all_sync(kFull, wait(&bar.raw_empty[mine_slot], (v && second == 0 ? phase ^ 1 : phase) ^ 1));
+                    if (!ok) break;
+                    if (lane == 0 || lane == 8) mbar_arrive_expect_tx(&bar.raw_full[mine_slot], bytes);
+                    __syncwarp();
+                    if (mine) {
+                        const uint32_t dst = smem_u32(raw_smem) + mine_slot * S::kRawBytes;
+                        tma_codes(lane < 16 ? dst + box * rows * D : dst + S::kRawCodes + box * 128, map8, lane < 16 ? 0 : row,
+                                  lane < 16 ? row : 0, s.head, page, &bar.raw_full[mine_slot]);
+                    }
+                    __syncwarp();
+                    idx += 2;
+                    if (second == 0) phase ^= 1;
+                    slot = second + 1;
+                    if (slot == (uint32_t)S::kRaw) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                    page = next_page;
+                }
+            }
+            for (int t = 0; !Q8 && t < s.tiles && ok; ++t) {
                 const int k0 = (s.tile + t) * S::BK + lane * rows;
                 const bool mine = lane < boxes && k0 < s.r.hi && k0 + rows > s.r.lo;
                 if (t > 0) page = page_of(s, t);
@@ -865,19 +905,13 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
                 const int row = k0 & ((1 << a.log_page) - 1);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++idx) {
-                    const uint32_t st = idx % kRing, use = idx / kRing;
-                    ok = ok && wait(&room[st], (use & 1) ^ 1);
+                    const uint32_t st = idx % S::kStages, use = idx / S::kStages;
+                    ok = ok && wait(&bar.empty[st], (use & 1) ^ 1);
                     ok = __all_sync(kFull, ok);
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&landed[st], bytes);
+                    if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], bytes);
                     __syncwarp();
-                    if constexpr (Q8) {
-                        if (mine) {
-                            const uint32_t dst = smem_u32(raw_smem) + st * S::kRawBytes;
-                            tma_codes(dst + lane * rows * D, kv ? &a.vmap : &a.kmap, row, s.head, page, &landed[st]);
-                            tma_scales(dst + S::kRawCodes + lane * 128, kv ? &a.vsmap : &a.ksmap, row, s.head, page, &landed[st]);
-                        }
-                    } else if (mine) {
+                    if (mine) {
                         const CUtensorMap *map = kv ? &a.vmap : &a.kmap;
                         const uint32_t dst = smem_u32(kv_smem) + st * S::kStageBytes + lane * rows * 128;
                         if (whole) tma_page(dst, map, row, 0, s.head, page, &bar.full[st]);

@@ -123,7 +123,7 @@ spec_status page_map(const Device &d, const spec_paged_cache &c, void *base, con
 
 
 // The 8-bit cache as TMA sees it: codes [page][head][token][head_dim], boxes of one page's
-// tokens (at most a tile's), and scales [page][head][token].
+// tokens (at most a tile's), and scales [page][head][1][token].
 spec_status code_maps(const Device &d, const spec_paged_cache8 &c, void *codes, const int64_t *strides, void *scales,
                       CUtensorMap *map, CUtensorMap *smap)
 {
@@ -136,9 +136,10 @@ spec_status code_maps(const Device &d, const spec_paged_cache8 &c, void *codes, 
     CUresult r = d.encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, codes, dims, st, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r == CUDA_SUCCESS) {
-        const cuuint64_t st2[2] = {(cuuint64_t)c.page_size, (cuuint64_t)c.page_size * c.heads};
-        const cuuint32_t box2[3] = {rows, 1, 1};
-        r = d.encode(smap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, scales, dims + 1, st2, box2, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        const cuuint64_t dims2[4] = {(cuuint64_t)c.page_size, 1, (cuuint64_t)c.heads, (cuuint64_t)c.pages};
+        const cuuint64_t st2[3] = {(cuuint64_t)c.page_size, (cuuint64_t)c.page_size, (cuuint64_t)c.page_size * c.heads};
+        const cuuint32_t box2[4] = {rows, 1, 1, 1};
+        r = d.encode(smap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, scales, dims2, st2, box2, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     }
     if (r != CUDA_SUCCESS) return fail(SPEC_ERR_ARG, "cache: its layout has no tensor map (driver error %d)", (int)r);

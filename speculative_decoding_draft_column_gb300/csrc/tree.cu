@@ -18,11 +18,11 @@ namespace {
 
 // `cluster`: CTAs of a thread-block cluster (1: none)
 template <typename K, typename... A>
-spec_status launch(K kernel, int64_t grid, unsigned block, size_t smem, unsigned cluster, const A &...a)
+spec_status launch(K kernel, dim3 grid, unsigned block, size_t smem, unsigned cluster, const A &...a)
 {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = host::stream();
@@ -75,7 +75,7 @@ spec_status commit(tree::CommitArgs &a, const spec_paged_batch *batch, int32_t p
     a.page_size = page_size; a.depth = depth;
     a.block_table = b.block_table; a.cu = b.cu_new; a.seq_lens = b.seq_lens;
     a.path = path; a.accept = accept_lens; a.context_out = context_out;
-    return launch(tree::commit_kernel, b.lanes, tree::kCommitThreads, 0, 1, a);
+    return launch(tree::commit_kernel, dim3((unsigned)b.lanes), tree::kCommitThreads, 0, 1, a);
 }
 
 spec_status verify(const uint16_t *logits, const int32_t *drafts, const int32_t *parents, const int32_t *cu, int64_t tokens,
@@ -129,8 +129,8 @@ spec_status verify(const uint16_t *logits, const int32_t *drafts, const int32_t 
     while (ctas < tree::kMostCtas && (vectors > ctas * tree::kPart || (lanes * ctas * 2 <= sms && vectors >= 2 * ctas * tree::kThreads))) ctas *= 2;
     // All nodes' columns at once, where they fit the GPU together; else the paths' only.
     if (tokens * ctas <= 2 * sms && host::lane_scratch(lanes, tokens * a.k, &a.tickets, &a.lists) && tokens > 0)
-        return launch(tree::verify_kernel<true>, tokens * ctas, tree::kThreads, sizeof(tree::VerifySmem), ctas, a, (uint32_t)ctas);
-    return launch(tree::verify_kernel<false>, lanes * ctas, tree::kThreads, sizeof(tree::VerifySmem), ctas, a, (uint32_t)ctas);
+        return launch(tree::verify_kernel<true>, dim3((unsigned)(tokens * ctas)), tree::kThreads, sizeof(tree::VerifySmem), ctas, a, (uint32_t)ctas);
+    return launch(tree::verify_kernel<false>, dim3((unsigned)(lanes * ctas)), tree::kThreads, sizeof(tree::VerifySmem), ctas, a, (uint32_t)ctas);
 }
 
 }  // namespace
@@ -155,14 +155,27 @@ spec_status spec_paged_store8(const void *k, const void *v, int64_t tokens, int6
     int64_t sms = 0;
     st = sm_count(&sms);
     if (st != SPEC_OK) return st;
-    tree::StoreArgs a = {static_cast<const uint16_t *>(k), static_cast<const uint16_t *>(v), tokens,
-                         k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots, *cache, 2};
+    tree::StoreArgs a;
+    memset(&a, 0, sizeof a);
+    a.k = static_cast<const uint16_t *>(k); a.v = static_cast<const uint16_t *>(v);
+    a.tokens = tokens;
+    a.ks_t = k_token_stride; a.ks_h = k_head_stride; a.vs_t = v_token_stride; a.vs_h = v_head_stride;
+    a.slots = slots; a.c = *cache;
+    a.group = 2;
     while (a.group * 8 < cache->head_dim) a.group *= 2;
-    const int64_t per = tree::kStoreThreads / a.group;
-    int64_t grid = (tokens * cache->heads + per - 1) / per;
-    if (grid > 8 * sms) grid = 8 * sms;
-    return cache->dtype == SPEC_F16 ? launch(tree::store_kernel<true>, grid, tree::kStoreThreads, 0, 1, a)
-                                    : launch(tree::store_kernel<false>, grid, tree::kStoreThreads, 0, 1, a);
+    const int32_t most = tree::kStoreThreads / a.group;
+    a.heads = cache->heads < most ? cache->heads : most;
+    a.per = most / a.heads;
+    a.log_page = -1;
+    if ((cache->page_size & (cache->page_size - 1)) == 0) a.log_page = 31 - __builtin_clz((unsigned)cache->page_size);
+    // heads past a CTA's: more CTAs a token, as far as a grid's second dimension goes
+    const int64_t parts = ((int64_t)cache->heads + a.heads - 1) / a.heads;
+    if (parts > 65535) return fail(SPEC_ERR_ARG, "cache: heads = %d, the store takes %d of this size", cache->heads, 65535 * a.heads);
+    int64_t grid = (tokens + a.per - 1) / a.per;
+    const int64_t room = (tree::kStoreCtas * sms + parts - 1) / parts;
+    if (grid > room) grid = room;
+    return cache->dtype == SPEC_F16 ? launch(tree::store_kernel<true>, dim3((unsigned)grid, (unsigned)parts), tree::kStoreThreads, 0, 1, a)
+                                    : launch(tree::store_kernel<false>, dim3((unsigned)grid, (unsigned)parts), tree::kStoreThreads, 0, 1, a);
 }
 
 spec_status spec_tree_plan(const int32_t *parents, int64_t tokens, const spec_paged_batch *batch, uint32_t *masks,
@@ -187,7 +200,7 @@ spec_status spec_tree_plan(const int32_t *parents, int64_t tokens, const spec_pa
             if (overlap(*o, i)) return fail(SPEC_ERR_ARG, "%s overlaps %s", o->name, i.name);
     if (overlap(m, p)) return fail(SPEC_ERR_ARG, "masks overlaps positions");
     tree::PlanArgs a = {parents, b.cu_new, b.seq_lens, tokens, b.lanes, masks, mask_words, positions};
-    return launch(tree::plan_kernel, b.lanes, tree::kPlanThreads, 0, 1, a);
+    return launch(tree::plan_kernel, dim3((unsigned)b.lanes), tree::kPlanThreads, 0, 1, a);
 }
 
 spec_status spec_tree_verify(const uint16_t *target_logits, const int32_t *drafts, const int32_t *parents,

@@ -88,94 +88,108 @@ struct StoreArgs {
     const int64_t *slots;
     spec_paged_cache8 c;
     int32_t group;         // threads of a vector: the power of two that covers head_dim / 8
+    int32_t heads;         // of a token that a CTA deals with (blockIdx.y: which)
+    int32_t per;           // tokens at a time: kStoreThreads / (group * heads)
+    int32_t log_page;      // log2 of the page's size, -1 where it is no power of two
 };
 
-constexpr int kStoreThreads = 256;
+constexpr int kStoreThreads = 256, kStoreCtas = 4;   // of an SM
 
-template <bool F16>
-__device__ __forceinline__ float widen(uint32_t bits16)
-{
-    if (!F16) return __uint_as_float(bits16 << 16);
-    float f;
-    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(f) : "r"(bits16));
-    return f;
-}
+// Packed 16-bit magnitudes: the larger of each half (as numbers without sign: infinities above all others, NaN above those).
+__device__ __forceinline__ uint32_t max2x16(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
 // Eight elements of a vector to codes; `group` threads hold a vector and agree on its scale.
 // The exponent comes from the bits of the largest magnitude 1.f * 2^E: 1.f is at most 1.75 =
-// 448 / 2^8 or not.  x * 2^-e is exact in fp32, so each code is rounded once.
+// 448 / 2^8 or not.  x * 2^-e is exact (what a 16-bit product would lose lies below half the least code),
+// so each code is rounded once.
 template <bool F16>
 __device__ __forceinline__ void quantise(const uint4 &q, int group, uint2 &codes, uint32_t &scale)
 {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    float x[8];
-    uint32_t most = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = widen<F16>(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu);
-        const uint32_t m = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-        most = m > most ? m : most;
-    }
-    for (int d = 1; d < group; d <<= 1) {
-        const uint32_t m = __shfl_xor_sync(kFull, most, d);
-        most = m > most ? m : most;
-    }
-    if (most >= 0x7F800000u) {                        // an infinity or a NaN: no number throughout
+    uint32_t most = max2x16(max2x16(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), max2x16(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    for (int d = 1; d < group; d <<= 1) most = max2x16(most, __shfl_xor_sync(kFull, most, d));
+    most = max(most & 0xFFFFu, most >> 16);
+    if (most >= (F16 ? 0x7C00u : 0x7F80u)) {          // an infinity or a NaN: no number throughout
         codes = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
         scale = 255u;
         return;
     }
-    int e = (int)(most >> 23) - 127 - 8 + ((most & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    constexpr int kLeast = F16 ? -14 : -120;
+    constexpr int kBits = F16 ? 10 : 7, kBias = F16 ? 15 : 127, kLeast = F16 ? -14 : -120;
+    // (a subnormal's exponent comes out too small, and is cut to the least anyway: fp16's below 2^-14, bf16's below 2^-126)
+    int e = (int)(most >> kBits) - kBias - 8 + ((most & ((1u << kBits) - 1u)) > (3u << (kBits - 2)) ? 1 : 0);
     e = e < kLeast ? kLeast : e > 7 ? 7 : e;
-    const float f = __uint_as_float((uint32_t)(127 - e) << 23);
     uint32_t c[4];
+    if (F16) {
+        const uint32_t f = (uint32_t)(15 - e) << 10, ff = f | f << 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint16_t two;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(x[2 * i + 1] * f), "f"(x[2 * i] * f));
-        c[i] = two;
+        for (int i = 0; i < 4; ++i) {
+            uint16_t two;
+            asm("{\n\t.reg .b32 y;\n\tmul.rn.f16x2 y, %1, %2;\n\tcvt.rn.satfinite.e4m3x2.f16x2 %0, y;\n\t}" : "=h"(two) : "r"(w[i]), "r"(ff));
+            c[i] = two;
+        }
+    } else {
+        const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint16_t two;
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(__uint_as_float(w[i] & 0xFFFF0000u) * f), "f"(__uint_as_float(w[i] << 16) * f));
+            c[i] = two;
+        }
     }
     codes = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
     scale = (uint32_t)(e + 127);
 }
 
-// Bound by its bytes; `group` threads take 8 elements each of a token's key and value of a head,
-// both on their way together.
+// Bound by its bytes; `group` threads take 8 elements each of a token's key and value of a head.
+// Two tokens' keys and values are on their way together, and the slots of the next two: a
+// CTA's rounds follow one another, and each waits for its slots and then for its vectors.
 template <bool F16>
-__global__ void __launch_bounds__(kStoreThreads) store_kernel(const __grid_constant__ StoreArgs a)
+__global__ void __launch_bounds__(kStoreThreads, kStoreCtas) store_kernel(const __grid_constant__ StoreArgs a)
 {
+    constexpr int kAtOnce = 2;
     pdl_launch_dependents();
+    const int tid = threadIdx.x, each = a.group * a.heads, sub = tid / each, e = (tid & (a.group - 1)) * 8;
+    const int h = (int)blockIdx.y * a.heads + (tid - sub * each) / a.group;
+    const bool in = e < a.c.head_dim && h < a.c.heads && sub < a.per;
+    const uint16_t *k = a.k + h * a.ks_h + e, *v = a.v + h * a.vs_h + e;
+    uint8_t *kc = static_cast<uint8_t *>(a.c.k) + h * a.c.k_strides[2] + e, *vc = static_cast<uint8_t *>(a.c.v) + h * a.c.v_strides[2] + e;
+    const int64_t limit = a.c.pages * a.c.page_size, step = (int64_t)gridDim.x * a.per;
+    int64_t first = (int64_t)blockIdx.x * a.per, slot[kAtOnce];
     pdl_wait();
-    const int e = ((int)threadIdx.x & (a.group - 1)) * 8, per = kStoreThreads / a.group;
-    const bool in = e < a.c.head_dim;
-    const int64_t vectors = a.tokens * a.c.heads, limit = a.c.pages * a.c.page_size;
-    const int64_t step = (int64_t)gridDim.x * per, rounds = (vectors + step - 1) / step;
-    int64_t i = (int64_t)blockIdx.x * per + (int)threadIdx.x / a.group;
-    for (int64_t n = 0; n < rounds; ++n, i += step) {   // (all threads of a warp stay for the shuffles)
-        const int64_t t = i < vectors ? udiv(i, a.c.heads) : 0;
-        const int h = (int)(i - t * a.c.heads);
-        const int64_t slot = i < vectors ? __ldg(a.slots + t) : -1;
-        const bool on = slot >= 0 && slot < limit;
-        uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
-        if (on && in) {
-            kx = __ldg(reinterpret_cast<const uint4 *>(a.k + t * a.ks_t + h * a.ks_h + e));
-            vx = __ldg(reinterpret_cast<const uint4 *>(a.v + t * a.vs_t + h * a.vs_h + e));
+    auto slots_of = [&](int64_t t) {
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) slot[u] = in && t + u * step < a.tokens ? __ldg(a.slots + t + u * step) : -1;
+    };
+    slots_of(first + sub);
+    for (; first < a.tokens; first += step * kAtOnce) {   // (all threads of a warp stay for the shuffles)
+        uint4 x[kAtOnce][2];
+        int64_t at[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int64_t t = first + sub + u * step;
+            at[u] = slot[u] < limit ? slot[u] : -1;
+            x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+            if (at[u] >= 0) {
+                x[u][0] = __ldg(reinterpret_cast<const uint4 *>(k + t * a.ks_t));
+                x[u][1] = __ldg(reinterpret_cast<const uint4 *>(v + t * a.vs_t));
+            }
         }
-        uint2 kc, vc;
-        uint32_t ke, ve;
-        quantise<F16>(kx, a.group, kc, ke);
-        quantise<F16>(vx, a.group, vc, ve);
-        if (!on || !in) continue;
-        const int64_t page = udiv(slot, a.c.page_size), row = slot - page * a.c.page_size;
-        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.c.k) + page * a.c.k_strides[0] + row * a.c.k_strides[1] +
-                                   h * a.c.k_strides[2] + e) = kc;
-        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.c.v) + page * a.c.v_strides[0] + row * a.c.v_strides[1] +
-                                   h * a.c.v_strides[2] + e) = vc;
-        if (e == 0) {
-            const int64_t at = (page * a.c.heads + h) * a.c.page_size + row;
-            a.c.k_scales[at] = (uint8_t)ke;
-            a.c.v_scales[at] = (uint8_t)ve;
+        slots_of(first + sub + step * kAtOnce);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            uint2 code[2];
+            uint32_t scale[2];
+            quantise<F16>(x[u][0], a.group, code[0], scale[0]);
+            quantise<F16>(x[u][1], a.group, code[1], scale[1]);
+            if (at[u] < 0) continue;
+            const int64_t page = a.log_page >= 0 ? at[u] >> a.log_page : udiv(at[u], a.c.page_size), row = at[u] - page * a.c.page_size;
+            *reinterpret_cast<uint2 *>(kc + page * a.c.k_strides[0] + row * a.c.k_strides[1]) = code[0];
+            *reinterpret_cast<uint2 *>(vc + page * a.c.v_strides[0] + row * a.c.v_strides[1]) = code[1];
+            if (e == 0) {
+                const int64_t s = (page * a.c.heads + h) * a.c.page_size + row;
+                a.c.k_scales[s] = (uint8_t)scale[0];
+                a.c.v_scales[s] = (uint8_t)scale[1];
+            }
         }
     }
 }
