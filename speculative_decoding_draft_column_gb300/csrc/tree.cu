@@ -120,13 +120,15 @@ spec_status verify(const uint16_t *logits, const int32_t *drafts, const int32_t 
     a.logits = logits; a.drafts = drafts; a.parents = parents; a.cu = cu;
     a.tokens = tokens; a.lanes = lanes; a.V = V; a.depth = depth;
     a.k = sampled ? top_k : 1;
-    a.temperature = temperature; a.top_p = top_p; a.uniforms = sampled ? uniforms : nullptr;
+    a.temperature = temperature; a.top_p = top_p;
+    a.inv_temperature = (float)(1.0 / temperature); a.top_p_single = (float)top_p;
+    a.uniforms = sampled ? uniforms : nullptr;
     a.accept = accept; a.commit = commits; a.path = path;
-    // CTAs of a column: as few as hold it at once, and more while there are SMs for them and a
-    // part keeps every thread at a vector
+    // CTAs of a column: more while all lanes' make up four turns of the GPU (two are on an SM) at most, and a part keeps
+    // every thread at a vector or more (128 lanes of 16 nodes 88 us with four turns, 107 with one, 166 with a half)
     const int64_t vectors = (V + 14) / 8;
     unsigned ctas = 1;
-    while (ctas < tree::kMostCtas && (vectors > ctas * tree::kPart || (lanes * ctas * 2 <= sms && vectors >= 2 * ctas * tree::kThreads))) ctas *= 2;
+    while (ctas < tree::kMostCtas && lanes * ctas * 2 <= 8 * sms && vectors >= 2 * ctas * tree::kThreads) ctas *= 2;
     // All nodes' columns at once, where they fit the GPU together; else the paths' only.
     if (tokens * ctas <= 2 * sms && host::lane_scratch(lanes, tokens * a.k, &a.tickets, &a.lists) && tokens > 0)
         return launch(tree::verify_kernel<true>, dim3((unsigned)(tokens * ctas)), tree::kThreads, sizeof(tree::VerifySmem), ctas, a, (uint32_t)ctas);

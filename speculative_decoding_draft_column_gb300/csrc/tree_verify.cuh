@@ -28,6 +28,7 @@ constexpr int kLoads = 8;                        // 16-byte vectors of a thread
 constexpr int kPart = kThreads * kLoads;         // vectors of a part at a time
 constexpr int kMostCtas = 8;                     // of a cluster
 constexpr int kCand = 1024;                      // candidates of a part
+constexpr int kInbox = SPEC_MAX_K + 1;           // (the lists' entries of one place on different banks)
 
 struct VerifyArgs {
     const uint16_t *logits;
@@ -35,6 +36,7 @@ struct VerifyArgs {
     int64_t tokens, lanes, V;
     int32_t depth, k;
     double temperature, top_p;
+    float inv_temperature, top_p_single;         // (no FP64 division on the walk)
     const double *uniforms;                      // null: greedy
     int32_t *accept, *commit, *path;
     unsigned long long *lists;                   // kWide: [tokens][k]
@@ -43,14 +45,15 @@ struct VerifyArgs {
 
 struct VerifySmem {
     unsigned long long cand[kCand + SPEC_MAX_K];
-    unsigned long long inbox[2][kMostCtas][SPEC_MAX_K];
+    unsigned long long inbox[2][kMostCtas][kInbox];
     unsigned long long list[SPEC_MAX_K];         // a part's list, then the column's
     double2 uniform[kNodes];
     int32_t parent[kNodes], token[kNodes];
+    uint32_t hits[kNodes / 32];                  // children of the walk's node whose tokens are in its list,
+    int32_t place[kNodes];                       // and where
     uint32_t top[kThreads];                      // the threads' maxima
     uint32_t sec[64];                            // of 8 threads each
     uint32_t ncand, first, count;
-    int32_t listed;                              // entries of list
     int32_t next, chosen;                        // the decision: the accepted child (-1: none) and the token
     int32_t lane, n;
     int64_t row0;
@@ -124,9 +127,16 @@ __device__ __noinline__ void exact_candidates(const Piece p, int k, uint32_t T, 
     __syncthreads();
 }
 
+// The sum over eight neighbouring threads.
+__device__ __forceinline__ int sum_of_8(int x)
+{
+    x += __shfl_xor_sync(kFull, x, 1);
+    x += __shfl_xor_sync(kFull, x, 2);
+    return x + __shfl_xor_sync(kFull, x, 4);
+}
+
 // The k best elements of vectors [j0, j1) of column [cb, ce) of the logits (vector j: elements
-// [8j - mis, 8j - mis + 8) of the whole), sorted into s.list; s.listed of them (fewer where
-// the part has fewer).  A part of more than kPart vectors is taken in pieces, each with the
+// [8j - mis, 8j - mis + 8) of the whole), sorted into s.list (zeros behind them where the part has fewer).  A part of more than kPart vectors is taken in pieces, each with the
 // list of those before among its candidates.  All threads of the CTA call it.
 __device__ __forceinline__ void part_best(const VerifyArgs &a, int64_t j0, int64_t j1, int64_t cb, int64_t ce, VerifySmem &s)
 {
@@ -209,13 +219,15 @@ __device__ __forceinline__ void part_best(const VerifyArgs &a, int64_t j0, int64
         for (; um; um &= um - 1) {
             const int u = __ffs(um) - 1;
             const uint4 v = gm::pick(q, u);
+            // (most vectors here hold one such element: the eight are compared at once, and those that reach T dealt with)
+            uint32_t hits = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) hits |= order_key(gm::half_of(v, e)) >= T ? 1u << e : 0u;
 #pragma unroll 1
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t raw = gm::half_of(v, e), key = order_key(raw);
-                if (key >= T) {
-                    const uint32_t at = atomicAdd(&s.ncand, 1u);
-                    if (at < (uint32_t)kCand) s.cand[at] = gm::make_entry(key, id0 + (uint32_t)(8 * (u * kThreads + t) + e), raw);
-                }
+            for (; hits; hits &= hits - 1) {
+                const int e = __ffs(hits) - 1;
+                const uint32_t raw = gm::half_of(v, e), at = atomicAdd(&s.ncand, 1u);
+                if (at < (uint32_t)kCand) s.cand[at] = gm::make_entry(order_key(raw), id0 + (uint32_t)(8 * (u * kThreads + t) + e), raw);
             }
         }
         __syncthreads();
@@ -227,51 +239,63 @@ __device__ __forceinline__ void part_best(const VerifyArgs &a, int64_t j0, int64
         if (t < have) s.cand[n + t] = s.list[t];
         __syncthreads();
         n += have;
-        for (int i = t; i < n; i += kThreads) {
-            const unsigned long long e = s.cand[i];
+        // a candidate's rank, by eight threads that compare it with an eighth of them each
+        for (int base = 0; base < n; base += kThreads / 8) {
+            const int i = base + (t >> 3);
+            const unsigned long long e = i < n ? s.cand[i] : ~0ull;
             int rank = 0;
 #pragma unroll 4
-            for (int j = 0; j < n; ++j) rank += s.cand[j] > e ? 1 : 0;
-            if (rank < k) s.list[rank] = e;
+            for (int j = t & 7; j < n; j += 8) rank += s.cand[j] > e ? 1 : 0;
+            rank = sum_of_8(rank);
+            if ((t & 7) == 0 && i < n && rank < k) s.list[rank] = e;
         }
         have = n < k ? n : k;
         __syncthreads();
     }
-    if (t == 0) s.listed = have;
+    if (t < k && t >= have) s.list[t] = 0ull;
     __syncthreads();
 }
 
 // The lists of the cluster's CTAs, merged into s.list: an entry's rank is its place in its own list and,
-// in each of the others, the number of larger ones.
-__device__ __forceinline__ void merge_parts(const unsigned long long (*in)[SPEC_MAX_K], int ctas, int k, VerifySmem &s)
+// in each of the others, the number of larger ones, which eight threads (one a list) look for by bisection.
+__device__ __forceinline__ void merge_parts(const unsigned long long (*in)[kInbox], int ctas, int k, VerifySmem &s)
 {
-    const int t = threadIdx.x, mine = t / SPEC_MAX_K, i = t % SPEC_MAX_K;
-    static_assert(kThreads == kMostCtas * SPEC_MAX_K, "a thread an entry");
-    if (t == 0) s.listed = 0;
+    static_assert(kMostCtas == 8 && kThreads == 512, "eight entries of each of eight lists at a time");
+    const int t = threadIdx.x, mine = (t >> 3) & 7, other = t & 7, top = 1 << (31 - __clz(k));
+    if (t < k) s.list[t] = 0ull;                 // (fewer than k where the column has fewer)
     __syncthreads();
-    const unsigned long long e = mine < ctas && i < k ? in[mine][i] : 0ull;
-    if (e) {
-        int rank = i;
-#pragma unroll
-        for (int c = 0; c < kMostCtas; ++c) {
-            if (c >= ctas || c == mine) continue;
-            int lo = 0, hi = k;                  // entries above e: [0, lo)
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (in[c][mid] > e) lo = mid + 1;
-                else hi = mid;
-            }
-            rank += lo;
-        }
-        if (rank < k) {
-            s.list[rank] = e;
-            atomicMax(&s.listed, rank + 1);
-        }
+    // (the k best of all are among the first eight of each list, mostly: then one turn places them)
+    for (int base = 0, placed = 0; base < k && placed < k; base += 8) {
+        const int i = base + (t >> 6);
+        const unsigned long long e = mine < ctas && i < k ? in[mine][i] : 0ull;
+        int above = 0;                           // entries above e in the other list: [0, above)
+        if (e && other < ctas && other != mine)
+            for (int step = top; step; step >>= 1)
+                if (above + step <= k && in[other][above + step - 1] > e) above += step;
+        const int rank = i + sum_of_8(above);
+        const bool in_list = other == 0 && e && rank < k;
+        if (in_list) s.list[rank] = e;
+        placed += __syncthreads_count(in_list);
     }
-    __syncthreads();
 }
 
 // ---- the decision at a node -------------------------------------------------------
+
+// The children of node `cur` whose tokens are in its list, by `threads` threads (whole warps).
+__device__ __forceinline__ void match_children(const VerifyArgs &a, VerifySmem &s, int cur, bool last_level, int t, int threads)
+{
+    for (int i = t; (i & ~31) < s.n; i += threads) {
+        const int32_t x = i > 0 && i < s.n && !last_level && s.parent[i] == cur ? s.token[i] : -1;
+        int place = -1;
+        if (x >= 0)
+#pragma unroll 4
+            for (int e = 0; e < a.k; ++e)
+                if ((int32_t)entry_id(s.list[e]) == x && s.list[e]) place = e;
+        const uint32_t hits = __ballot_sync(kFull, place >= 0);
+        if (place >= 0) s.place[i] = place;
+        if ((i & 31) == 0) s.hits[i >> 5] = hits;
+    }
+}
 
 __device__ __forceinline__ float warp_sum(float v) { return warp_sum_f(v); }
 __device__ __forceinline__ double warp_sum(double v) { return warp_sum_d(v); }
@@ -279,26 +303,26 @@ __device__ __forceinline__ float warp_scan(float v, int lane) { return warp_scan
 __device__ __forceinline__ double warp_scan(double v, int lane) { return warp_scan_d(v, lane); }
 
 // Sampled decision at node `cur` from its column's list, by one warp, in R.  Entry t of the list is in lane t,
-// or t - 32.  In double the rounding of sums by trees is some 1e-16.  In float it is first tried
-// whether every comparison is clear of its border: a term exp((v - v0) / T) is off by less than
-// 3e-7, so with at most 32 of them and a nucleus of at least 1/4 the q and their sums are off by less than
-// 2e-4, a product with a uniform by no more; what is nearer than 5e-4 is left to double (returns
-// false).  FP64 runs at a small fraction of the FP32 rate here.
+// or t - 32, n entries.  In double the rounding of sums by trees is some 1e-16.  In float it is first
+// tried whether every comparison is clear of its border (FP64 runs at a small fraction of the FP32 rate here), else
+// false is returned and double decides.  With at most 32 terms e = exp(x), x = (v - v0) / T: x is off by
+// 3 * 2^-24 |x| and exp by 2 units, so a term by 1.8e-7 |x| e + 2.4e-7 e, of which |x| e <= 0.37; the terms' sum S >= 1 by
+// 2.1e-6 + 2.4e-7 S and five roundings; running sums of e / S by 6e-6 then, and those over a nucleus of
+// weight C by 1.2e-5 / C, a uniform's product with what is left the same.
 template <typename R>
-__device__ __forceinline__ bool decide_sampled(const VerifyArgs &a, VerifySmem &s, int cur, bool last_level, int lane, int32_t &next,
+__device__ __forceinline__ bool decide_sampled(const VerifyArgs &a, VerifySmem &s, int n, int cur, int lane, int32_t &next,
                                                int32_t &token)
 {
     constexpr bool kSingle = sizeof(R) == 4;
-    constexpr R kSure = (R)5e-4;
-    const int n = s.listed;
+    constexpr R kSureP = (R)2e-5, kSureQ = (R)5e-5;   // above 6e-6; above 2 * 1.2e-5, over C
     if (kSingle && n > 32) return false;
-    auto near = [&](R x, R y) { return kSingle && !(x - y > kSure || y - x > kSure); };   // (a NaN is near)
+    auto near = [&](R x, R y, R sure) { return kSingle && !(x - y > sure || y - x > sure); };   // (a NaN is near)
     const bool ha = lane < n, hb = lane + 32 < n;
     const unsigned long long ea_ = ha ? s.list[lane] : 0ull, eb_ = hb ? s.list[lane + 32] : 0ull;
     const float v0 = bf16_as_float(entry_raw(s.list[0]));
     R ea, eb = 0;
     if (kSingle) {
-        ea = ha ? (R)expf((bf16_as_float(entry_raw(ea_)) - v0) * (float)(1.0 / a.temperature)) : (R)0;
+        ea = ha ? (R)expf((bf16_as_float(entry_raw(ea_)) - v0) * a.inv_temperature) : (R)0;
     } else {
         const double z0 = (double)v0 / a.temperature;
         ea = ha ? (R)exp((double)bf16_as_float(entry_raw(ea_)) / a.temperature - z0) : (R)0;
@@ -308,35 +332,31 @@ __device__ __forceinline__ bool decide_sampled(const VerifyArgs &a, VerifySmem &
     const R inv = (R)1 / warp_sum(ea + eb);
     const R pa = ea * inv, pb = eb * inv;
     // the nucleus: the shortest prefix whose running sum reaches top_p
-    const R top_p = (R)a.top_p;
+    const R top_p = kSingle ? (R)a.top_p_single : (R)a.top_p;
     const R ca = warp_scan(pa, lane), cb = __shfl_sync(kFull, ca, 31) + (kSingle ? (R)0 : warp_scan(pb, lane));
-    if (__any_sync(kFull, (ha && near(ca, top_p)) || (hb && near(cb, top_p)))) return false;
+    if (__any_sync(kFull, (ha && near(ca, top_p, kSureP)) || (hb && near(cb, top_p, kSureP)))) return false;
     const uint32_t ra = __ballot_sync(kFull, ha && ca >= top_p), rb = __ballot_sync(kFull, hb && cb >= top_p);
     const int last = ra ? __ffs(ra) - 1 : rb ? 31 + __ffs(rb) : n - 1;
     const R C = last < 32 ? __shfl_sync(kFull, ca, last & 31) : __shfl_sync(kFull, cb, last & 31);
     if (kSingle && !(C >= (R)0.25)) return false;
-    const R invC = (R)1 / C;
+    const R invC = (R)1 / C, sure = kSureQ * invC;
     R qa = lane <= last ? pa * invC : (R)0, qb = lane + 32 <= last ? pb * invC : (R)0;   // of what is left
     R left = warp_sum(qa + qb);
     next = -1;
-    for (int base = 0; base < s.n && !last_level; base += 32) {
-        const int i = base + lane;
-        uint32_t kids = __ballot_sync(kFull, i > 0 && i < s.n && s.parent[i] == cur);
-        for (; kids; kids &= kids - 1) {
-            const int c = base + __ffs(kids) - 1;
-            const int32_t x = s.token[c];
-            const uint32_t ma = __ballot_sync(kFull, lane <= last && ida == x && x >= 0), mb = __ballot_sync(kFull, lane + 32 <= last && idb == x && x >= 0);
-            if (!(ma | mb)) continue;            // not in the nucleus
-            const R xa = __shfl_sync(kFull, qa, ma ? __ffs(ma) - 1 : 0), xb = __shfl_sync(kFull, qb, mb ? __ffs(mb) - 1 : 0);
-            const R q = ma ? xa : xb, goal = (R)s.uniform[c].x * left;
+    for (int base = 0; base < s.n; base += 32) {
+        for (uint32_t kids = s.hits[base >> 5]; kids; kids &= kids - 1) {
+            const int c = base + __ffs(kids) - 1, at = s.place[c];
+            if (at > last) continue;             // not in the nucleus
+            const R xa = __shfl_sync(kFull, qa, at & 31), xb = __shfl_sync(kFull, qb, at & 31);
+            const R q = at < 32 ? xa : xb, goal = (R)s.uniform[c].x * left;
             if (q == (R)0) continue;             // taken out before (or without weight)
-            if (near(goal, q)) return false;
+            if (near(goal, q, sure)) return false;
             // taken out; with nothing left but rounding it is accepted: the uniform is below 1
-            const R na = ma & (1u << lane) ? (R)0 : qa, nb = mb & (1u << lane) ? (R)0 : qb;
+            const R na = lane == at ? (R)0 : qa, nb = lane + 32 == at ? (R)0 : qb;
             const R rest = warp_sum(na + nb);
             if (goal < q || rest == (R)0) {
                 next = c;
-                token = x;
+                token = s.token[c];
                 return true;
             }
             qa = na;
@@ -347,7 +367,7 @@ __device__ __forceinline__ bool decide_sampled(const VerifyArgs &a, VerifySmem &
     // the draw from what is left
     const R goal = (R)s.uniform[cur].y * left;
     const R sa = warp_scan(qa, lane), sb = __shfl_sync(kFull, sa, 31) + (kSingle ? (R)0 : warp_scan(qb, lane));
-    if (__any_sync(kFull, (ha && qa > (R)0 && near(sa, goal)) || (hb && qb > (R)0 && near(sb, goal)))) return false;
+    if (__any_sync(kFull, (ha && qa > (R)0 && near(sa, goal, sure)) || (hb && qb > (R)0 && near(sb, goal, sure)))) return false;
     const uint32_t xa = __ballot_sync(kFull, qa > (R)0 && sa > goal), xb = __ballot_sync(kFull, qb > (R)0 && sb > goal);
     if (kSingle && !xa) return false;
     // none exceeds it (rounding left the goal at the very end): the last that has weight
@@ -358,23 +378,21 @@ __device__ __forceinline__ bool decide_sampled(const VerifyArgs &a, VerifySmem &
     return true;
 }
 
-// What the walk does at node `cur` from its column's list: s.next, s.chosen.  One warp.
-__device__ __forceinline__ void decide(const VerifyArgs &a, VerifySmem &s, int cur, bool last_level, int lane)
+// What the walk does at node `cur` from its column's list (a.k entries, zeros behind the last): s.next, s.chosen.  One warp.
+__device__ __forceinline__ void decide(const VerifyArgs &a, VerifySmem &s, int cur, int lane)
 {
+    const int n = __popc(__ballot_sync(kFull, lane < a.k && s.list[lane])) + __popc(__ballot_sync(kFull, lane + 32 < a.k && s.list[lane + 32]));
     int32_t next = -1, token = -1;
-    if (s.listed == 0) {                         // (a column without a number is outside the contract)
+    if (n == 0) {                                // (a column without a number is outside the contract)
     } else if (a.uniforms) {
-        if (!decide_sampled<float>(a, s, cur, last_level, lane, next, token)) decide_sampled<double>(a, s, cur, last_level, lane, next, token);
+        if (!decide_sampled<float>(a, s, n, cur, lane, next, token)) decide_sampled<double>(a, s, n, cur, lane, next, token);
     } else {
         token = (int32_t)entry_id(s.list[0]);
-        for (int base = 0; base < s.n && !last_level; base += 32) {
-            const int i = base + lane;
-            const uint32_t hit = __ballot_sync(kFull, i > 0 && i < s.n && s.parent[i] == cur && s.token[i] == token);
-            if (hit) {
-                next = base + __ffs(hit) - 1;
+        for (int base = 0; base < s.n; base += 32)
+            if (s.hits[base >> 5]) {
+                next = base + __ffs(s.hits[base >> 5]) - 1;
                 break;
             }
-        }
     }
     if (lane == 0) {
         s.next = next;
@@ -424,12 +442,12 @@ __device__ __forceinline__ void column_part(const VerifyArgs &a, int64_t c, uint
     part_best(a, j0, j0 + each + (rank < more ? 1 : 0), cb, ce, s);
 }
 
-// s.list into inbox `b` of every CTA of the cluster (padded with zeros).
+// s.list into inbox `b` of every CTA of the cluster.
 __device__ __forceinline__ void send_list(VerifySmem &s, int b, uint32_t rank, uint32_t ctas, int k)
 {
     const int t = threadIdx.x, to = t / SPEC_MAX_K, i = t % SPEC_MAX_K;
     if (to < (int)ctas && i < k)
-        gm::st_cluster_u64(gm::cluster_map(&s.inbox[b][rank][i], to), i < s.listed ? s.list[i] : 0ull);
+        gm::st_cluster_u64(gm::cluster_map(&s.inbox[b][rank][i], to), s.list[i]);
 }
 
 template <bool kWide>
@@ -462,7 +480,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
                 gm::cluster_wait();
                 merge_parts(s.inbox[level & 1], (int)ctas, a.k, s);
             }
-            if (w == 0) decide(a, s, cur, level == a.depth, lane);
+            match_children(a, s, cur, level == a.depth, t, kThreads);
+            __syncthreads();
+            if (w == 0) decide(a, s, cur, lane);
             __syncthreads();
             const int next = s.next;
             if (writer) {
@@ -505,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         if (rank != 0) return;
         merge_parts(s.inbox[0], (int)ctas, a.k, s);
     }
-    if (t < a.k) __stcg(a.lists + row * a.k + t, t < s.listed ? s.list[t] : 0ull);
+    if (t < a.k) __stcg(a.lists + row * a.k + t, s.list[t]);
     __syncthreads();
     if (t == 0) {
         __threadfence();
@@ -519,15 +539,11 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     int cur = 0, level = 0;
     for (;; ++level) {
         __syncwarp();
-        int listed = 0;
-        for (int i = lane; i < SPEC_MAX_K; i += 32) {
-            const unsigned long long e = i < a.k ? __ldcg(a.lists + (s.row0 + cur) * a.k + i) : 0ull;
-            s.list[i] = e;
-            listed += __popc(__ballot_sync(kFull, e != 0ull));
-        }
-        if (lane == 0) s.listed = listed;
+        for (int i = lane; i < a.k; i += 32) s.list[i] = __ldcg(a.lists + (s.row0 + cur) * a.k + i);
         __syncwarp();
-        decide(a, s, cur, level == a.depth, lane);
+        match_children(a, s, cur, level == a.depth, lane, 32);
+        __syncwarp();
+        decide(a, s, cur, lane);
         __syncwarp();
         const int next = s.next;
         if (lane == 0) {
