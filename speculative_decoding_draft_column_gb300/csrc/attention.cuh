@@ -88,13 +88,16 @@ struct Shape {
     static constexpr int QB = QT == 1 && D <= (kQ8 ? 64 : 128) ? 2 : 1;   // Q buffers
     static constexpr int kRoom = 224 * 1024 - QB * QT * kQBytes;
     // 8 bits: as many 16-bit tiles as keep the products fed, the rest for tiles of codes on their way
-    static constexpr int kStages = kQ8 ? (D == 64 ? 6 : 3) : kRoom / kStageBytes < 12 ? kRoom / kStageBytes : 12;
+    static constexpr int kStages = kQ8 ? (D == 64 ? 6 : QT == 1 && D == 128 ? 4 : 3) : kRoom / kStageBytes < 12 ? kRoom / kStageBytes : 12;
     static constexpr int kRawCodes = BK * D;                   // codes of a tile, then 128 bytes for a page's scales
     static constexpr int kRawBytes = kRawCodes + BK / 16 * 128;
     static constexpr int kRawMost = (kRoom - kStages * kStageBytes) / kRawBytes;
-    static constexpr int kRaw = !kQ8 ? 0 : kRawMost < 6 ? kRawMost : 6;
+    static constexpr int kRaw = !kQ8 ? 0 : kRawMost < 4 ? kRawMost : 4;
     static constexpr int kSoftmaxWarps = NS * 8;
-    static constexpr int kConverters = kQ8 ? 8 : 0;            // warps
+    // converting warps, in teams of four that take half tiles in turn (64 registers a thread with three teams: two row tiles
+    // have the softmax of twice the rows to compute with them, 2.60 against 2.49 us a tile)
+    static constexpr int kTeams = QT == 1 && D <= 128 ? 3 : 2;
+    static constexpr int kConverters = kQ8 ? kTeams * 4 : 0;
     static constexpr int kThreads = kSoftmaxWarps * 32 + 128 + kConverters * 32;  // softmax; K/V loader, MMA, two Q loaders; converters
     static constexpr int kSwap = 512;                          // floats that softmax warps exchange through
     static constexpr int kPayload = QB * QT * kQBytes + kStages * kStageBytes + kRaw * kRawBytes + kSwap * 4;
@@ -106,7 +109,11 @@ struct Shape {
     static constexpr int kPartFloats = kRows * (D + 2);        // O, then m and sum
     static_assert(D == 64 || D == 128 || (D == 256 && QT == 1), "");
     static_assert(kO + NS * D <= 512, "TMEM");
-    static_assert(!kQ8 || kRaw >= 2, "a K and a V tile on their way");
+    // A team does not meet every use of a barrier, and a parity tells a use from its neighbours, not from the one before
+    // those.  So a slot has two barriers, in turn: when a team waits for tile T its last one, T - 1 or T - 2, has landed, so
+    // the loader has had T - 2 kRaw's slot back.  And when it waits for T's stage, the stage of that last one
+    // has been read, and with it T - 2 kStages.
+    static_assert(!kQ8 || (kRaw >= 2 && 2 * kRaw >= kStages + 2), "");
 };
 
 struct Args {
@@ -526,7 +533,7 @@ constexpr int kItems = 4;
 template <typename S>
 struct Bars {
     uint64_t full[S::kStages], empty[S::kStages];
-    uint64_t raw_full[S::kRaw + 1], raw_empty[S::kRaw + 1];   // of the codes' tiles (8 bits)
+    uint64_t raw_full[2 * S::kRaw + 1], raw_empty[S::kRaw + 1];   // of the codes' tiles (8 bits)
     uint64_t s_full[2], p_full[2], o_done[2];
     uint64_t q_full[2], q_empty[2], item_full[kItems], item_empty[kItems], drain;
     uint64_t part_full[2], part_known[2];   // the part in a slot is written; the others know
@@ -586,42 +593,51 @@ __device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t scale)
 }
 
 // The converting warps (8 bits): each tile of codes, as it lands, into a 16-bit tile in the
-// layout of the products' operands.  A thread takes 16 codes of a row at a time; lanes of every
+// layout of the products' operands.  Teams take half tiles in turn.  A thread takes 16 codes of a row at a time; lanes of every
 // second block of 64 elements write their two pieces in the other order, so that eight lanes
 // are on different banks.
 template <typename S, bool F16>
 __device__ __forceinline__ void convert_tiles(Bars<S> &bar, const Item *items, const uint8_t *raw_smem, uint8_t *kv_smem, int rows,
                                               int warp, int lane)
 {
-    constexpr int kPieces = S::D / 16, kStep = S::kConverters * 32 / kPieces, kPasses = S::BK / kStep;   // lanes a row, rows a pass
-    static_assert(kStep % 8 == 0 && S::BK % kStep == 0, "a thread's rows have one place in the swizzle");
-    const int id = warp * 32 + lane, p = id % kPieces, r0 = id / kPieces;
+    constexpr int kHalf = S::BK / 2, kPieces = S::D / 16, kStep = 128 / kPieces, kPasses = kHalf / kStep;   // lanes a row, rows a pass
+    static_assert(kStep % 8 == 0, "a thread's rows have one place in the swizzle");
+    const int team = warp >> 2, id = (warp & 3) * 32 + lane, p = id % kPieces, r0 = id / kPieces;
     const int block = p >> 2, piece = (p & 3) * 2, flip = block & 1;
     // where the thread's pieces go, and the scale of each of its rows
     const uint32_t x0 = ((piece + flip) ^ (r0 & 7)) << 4, x1 = x0 ^ 16;
     uint8_t *const to = kv_smem + block * (S::BK * 128) + r0 * 128;
-    const int log_rows = 31 - __clz(rows);
+    const int log_rows = 31 - __clz(rows), half_scales = rows > kHalf ? kHalf : (kHalf >> log_rows) * 128;
     int at[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) at[i] = S::kRawCodes + ((r0 + i * kStep) >> log_rows) * 128 + ((r0 + i * kStep) & (rows - 1));
-    uint32_t rs = 0, rs_phase = 0, st = 0, st_phase = 0;     // the next tile's slot and stage, K and V in turn
+    // the team's next half (of K tiles and V tiles in turn), the barrier of that tile's slot and its stage
+    int next = team;
+    uint32_t rb = team >> 1, rb_phase = 0, st = team >> 1, st_phase = 0;
+    static_assert(S::kTeams <= 4 && S::kRaw >= 2 && S::kStages > 2, "");
     for (uint32_t n = 0;; ++n) {
         if (!__all_sync(kFull, wait(&bar.item_full[n % kItems], (n / kItems) & 1))) return;
         const int tiles = items[n % kItems].tiles;
         __syncwarp();
         if (tiles == 0) return;
         if (lane == 0) mbar_arrive(&bar.item_empty[n % kItems]);
-        for (int t = 0; t < 2 * tiles; ++t) {
-            if (!__all_sync(kFull, wait(&bar.empty[st], st_phase ^ 1) && wait(&bar.raw_full[rs], rs_phase))) return;
+        while (next < 4 * tiles) {
+            const int half = next & 1;
+            const uint32_t rs = rb < (uint32_t)S::kRaw ? rb : rb - S::kRaw;
             const uint8_t *raw = raw_smem + rs * S::kRawBytes;
-            uint8_t *tile = to + st * S::kStageBytes;
+            uint8_t *tile = to + st * S::kStageBytes + half * (kHalf * 128);
+            if (!__all_sync(kFull, wait(&bar.raw_full[rb], rb_phase))) return;
             uint4 w[kPasses];
             uint32_t f[kPasses];
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
-                w[i] = *reinterpret_cast<const uint4 *>(raw + id * 16 + i * (kStep * S::D));
-                f[i] = raw[at[i]];
+                w[i] = *reinterpret_cast<const uint4 *>(raw + half * (kHalf * S::D) + id * 16 + i * (kStep * S::D));
+                f[i] = raw[at[i] + half * half_scales];
             }
+            // (the slot's next copies need not wait for the rest, nor the reads for the stage)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
+            if (!__all_sync(kFull, wait(&bar.empty[st], st_phase ^ 1))) return;
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
                 const uint32_t k = scale_pair<F16>(f[i]);
@@ -632,19 +648,21 @@ __device__ __forceinline__ void convert_tiles(Bars<S> &bar, const Item *items, c
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bar.raw_empty[rs]);
-                mbar_arrive(&bar.full[st]);
+            if (lane == 0) mbar_arrive(&bar.full[st]);
+            const int on = (half + S::kTeams) >> 1;              // tiles to the team's next half
+            next += S::kTeams;
+            rb += on;
+            if (rb >= 2u * S::kRaw) {
+                rb -= 2 * S::kRaw;
+                rb_phase ^= 1;
             }
-            if (++rs == (uint32_t)S::kRaw) {
-                rs = 0;
-                rs_phase ^= 1;
-            }
-            if (++st == (uint32_t)S::kStages) {
-                st = 0;
+            st += on;
+            if (st >= (uint32_t)S::kStages) {
+                st -= S::kStages;
                 st_phase ^= 1;
             }
         }
+        next -= 4 * tiles;
     }
 }
 
@@ -668,12 +686,13 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
     if (tid == 0) {
         s_gave_up = 0u;
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&bar.full[i], Q8 ? S::kConverters : 1);
+            mbar_init(&bar.full[i], Q8 ? 8 : 1);                // (8 bits: two halves by four warps)
             mbar_init(&bar.empty[i], 1);
         }
         for (int i = 0; i < S::kRaw; ++i) {
             mbar_init(&bar.raw_full[i], 1);
-            mbar_init(&bar.raw_empty[i], S::kConverters);
+            mbar_init(&bar.raw_full[S::kRaw + i], 1);
+            mbar_init(&bar.raw_empty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
@@ -835,7 +854,7 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
         const int boxes = S::BK / rows, box = Q8 ? lane & 7 : lane;   // (8 bits: 8 at most)
         const bool whole = !Q8 && rows == S::BK;                 // one box brings all blocks
         const uint32_t box_bytes = (uint32_t)rows * (Q8 ? D + 1 : D * 2);
-        constexpr uint32_t kRing = Q8 ? S::kRaw : S::kStages;    // where the copies land
+        constexpr uint32_t kRing = Q8 ? 2 * S::kRaw : S::kStages;   // barriers of copies that land
         uint64_t *landed = Q8 ? bar.raw_full : bar.full;
         auto page_of = [&](const Segment &s, int t) -> int {     // of this lane's box of tile t
             const int64_t k0 = (int64_t)(s.tile + t) * S::BK + box * rows, pi = k0 >> a.log_page;
@@ -843,8 +862,7 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
                        ? __ldg(a.block_table + s.lane * a.max_pages + pi) : -1;
         };
         uint32_t idx = 0;                                        // stage uses so far (8 bits: of slots)
-        [[maybe_unused]] uint32_t slot = 0, phase = 0;           // 8 bits: the next slot, the parity of its use, what this lane copies
-        [[maybe_unused]] const CUtensorMap *map8 = &a.kmap;
+        [[maybe_unused]] const CUtensorMap *map8 = &a.kmap;      // 8 bits: what this lane copies
         if constexpr (Q8) map8 = lane < 8 ? &a.kmap : lane < 16 ? &a.vmap : lane < 24 ? &a.ksmap : &a.vsmap;
         bool ok = true;
         if (lane < 2) joins[lane].n = joins[lane].count = joins[lane].lg = came_last[lane] = 0;
@@ -876,24 +894,19 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
                     const uint32_t bytes = __popc(__ballot_sync(kFull, mine) & 0xFFu) * (uint32_t)(rows * (D + 1));
                     const int next_page = t + 1 < s.tiles ? page_of(s, t + 1) : -1;   // on its way while this tile's copies wait for room
                     const bool v = (lane >> 3) & 1;
-                    const uint32_t second = slot + 1 < (uint32_t)S::kRaw ? slot + 1 : 0, mine_slot = v ? second : slot;
-                    ok = __all_sync(kFull, wait(&bar.raw_empty[mine_slot], (v && second == 0 ? phase ^ 1 : phase) ^ 1));
+                    const uint32_t at = idx + v, mine_slot = at % S::kRaw, use = at / S::kRaw;
+                    uint64_t *full = &bar.raw_full[mine_slot + (use & 1) * S::kRaw];
+                    ok = __all_sync(kFull, wait(&bar.raw_empty[mine_slot], (use & 1) ^ 1));
                     if (!ok) break;
-                    if (lane == 0 || lane == 8) mbar_arrive_expect_tx(&bar.raw_full[mine_slot], bytes);
+                    if (lane == 0 || lane == 8) mbar_arrive_expect_tx(full, bytes);
                     __syncwarp();
                     if (mine) {
                         const uint32_t dst = smem_u32(raw_smem) + mine_slot * S::kRawBytes;
                         tma_codes(lane < 16 ? dst + box * rows * D : dst + S::kRawCodes + box * 128, map8, lane < 16 ? 0 : row,
-                                  lane < 16 ? row : 0, s.head, page, &bar.raw_full[mine_slot]);
+                                  lane < 16 ? row : 0, s.head, page, full);
                     }
                     __syncwarp();
                     idx += 2;
-                    if (second == 0) phase ^= 1;
-                    slot = second + 1;
-                    if (slot == (uint32_t)S::kRaw) {
-                        slot = 0;
-                        phase ^= 1;
-                    }
                     page = next_page;
                 }
             }
