@@ -30,7 +30,6 @@ cudaError_t take_flag(const F &flag, unsigned int *flags)
 cudaError_t take_paged_timeouts(unsigned int *flags);
 cudaError_t take_tree_attention_timeouts(unsigned int *flags);
 cudaError_t take_attention8_timeouts(unsigned int *flags);
-cudaError_t take_tree_timeouts(unsigned int *flags);
 
 // The current device's scratch for a call on the calling thread's stream: a ticket a lane, zero between calls,
 // and `entries` words of lists.  False where there is none to be had (it would have to grow inside

@@ -1096,8 +1096,7 @@ spec_status spec_device_status(void)
     unsigned int flags = 0, zero = 0;
     e = cudaMemcpyFromSymbol(&flags, g_wait_timeouts, sizeof flags);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyFromSymbol");
-    for (auto take : {host::take_paged_timeouts, host::take_tree_attention_timeouts, host::take_attention8_timeouts,
-                      host::take_tree_timeouts}) {
+    for (auto take : {host::take_paged_timeouts, host::take_tree_attention_timeouts, host::take_attention8_timeouts}) {
         unsigned int more = 0;
         e = take(&more);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyFromSymbol");

@@ -137,12 +137,6 @@ spec_status verify(const uint16_t *logits, const int32_t *drafts, const int32_t 
 
 }  // namespace
 
-namespace host {
-
-cudaError_t take_tree_timeouts(unsigned int *flags) { return take_flag(g_wait_timeouts, flags); }
-
-}  // namespace host
-
 extern "C" {
 
 spec_status spec_paged_store8(const void *k, const void *v, int64_t tokens, int64_t k_token_stride,

@@ -18,7 +18,7 @@
 // Should many (ties), a bisection over values and then places finds exactly the k best.
 #pragma once
 
-#include "round_gm.cuh"
+#include "select.cuh"
 #include "tree.cuh"
 
 namespace tree {
