@@ -157,8 +157,8 @@ spec_status spec_paged_store8(const void *k, const void *v, int64_t tokens, int6
     a.tokens = tokens;
     a.ks_t = k_token_stride; a.ks_h = k_head_stride; a.vs_t = v_token_stride; a.vs_h = v_head_stride;
     a.slots = slots; a.c = *cache;
-    a.group = 2;
-    while (a.group * 8 < cache->head_dim) a.group *= 2;
+    a.group = 1;
+    while (a.group * 16 < cache->head_dim) a.group *= 2;
     const int32_t most = tree::kStoreThreads / a.group;
     a.heads = cache->heads < most ? cache->heads : most;
     a.per = most / a.heads;
