@@ -78,35 +78,37 @@ constexpr int kMaxSms = 512;     // counters at the start of the workspace: [2][
 // new tokens of a lane are the nodes of a tree, with a mask each.
 template <int D_, int QT_, bool Q8_ = false, bool TREE_ = false>
 struct Shape {
-    static constexpr int D = D_, QT = QT_;
-    static constexpr bool kQ8 = Q8_, kTree = TREE_;
+    static constexpr int D = D_, QT = QT_ == 0 ? 1 : QT_;
+    static constexpr bool kQ8 = Q8_, kTree = TREE_, kFew = QT_ == 0;   // kFew: at most 16 rows an item, keys across the tensor cores' lanes
     static constexpr int BK = D == 256 ? 64 : 128;             // keys of a tile
     static constexpr int NS = D == 256 ? 1 : 2;                // streams (softmax warpgroups)
     static constexpr int NB = D / 64;                          // 128-byte-wide blocks of an operand
-    static constexpr int kQBytes = 128 * D * 2;                // one row tile
+    static constexpr int kQBytes = (kFew ? 16 : 128) * D * 2;  // one row tile
     static constexpr int kStageBytes = BK * D * 2;             // a K or a V tile
     static constexpr int QB = QT == 1 && D <= (kQ8 ? 64 : 128) ? 2 : 1;   // Q buffers
-    static constexpr int kRoom = 224 * 1024 - QB * QT * kQBytes;
+    static constexpr int kPBytes = kFew ? NS * BK * 128 : 0;   // weights of a tile, a stream
+    static constexpr int kRoom = 224 * 1024 - QB * QT * kQBytes - kPBytes;
     // 8 bits: as many 16-bit tiles as keep the products fed, the rest for tiles of codes on their way
-    static constexpr int kStages = kQ8 ? (D == 64 ? 6 : QT == 1 && D == 128 ? 4 : 3) : kRoom / kStageBytes < 12 ? kRoom / kStageBytes : 12;
+    static constexpr int kStages = kQ8 ? (D == 64 ? 6 : QT == 1 && D == 128 && !kFew ? 4 : 3) : kRoom / kStageBytes < 12 ? kRoom / kStageBytes : 12;
     static constexpr int kRawCodes = BK * D;                   // codes of a tile, then 128 bytes for a page's scales
     static constexpr int kRawBytes = kRawCodes + BK / 16 * 128;
     static constexpr int kRawMost = (kRoom - kStages * kStageBytes) / kRawBytes;
     static constexpr int kRaw = !kQ8 ? 0 : kRawMost < 4 ? kRawMost : 4;
-    static constexpr int kSoftmaxWarps = NS * 8;
+    static constexpr int kSoftmaxWarps = kFew ? 8 : NS * 8;
     // converting warps, in teams of four that take half tiles in turn (64 registers a thread with three teams: two row tiles
     // have the softmax of twice the rows to compute with them, 2.60 against 2.49 us a tile)
-    static constexpr int kTeams = QT == 1 && D <= 128 ? 3 : 2;
+    static constexpr int kTeams = QT == 1 && D <= 128 && !kFew ? 3 : 2;
     static constexpr int kConverters = kQ8 ? kTeams * 4 : 0;
     static constexpr int kThreads = kSoftmaxWarps * 32 + 128 + kConverters * 32;  // softmax; K/V loader, MMA, two Q loaders; converters
-    static constexpr int kSwap = 512;                          // floats that softmax warps exchange through
-    static constexpr int kPayload = QB * QT * kQBytes + kStages * kStageBytes + kRaw * kRawBytes + kSwap * 4;
-    static constexpr int kRows = QT * 128;
+    static constexpr int kSwap = kFew ? 2048 : 512;            // floats that softmax warps exchange through (kFew: struct Few)
+    static constexpr int kPayload = QB * QT * kQBytes + kPBytes + kStages * kStageBytes + kRaw * kRawBytes + kSwap * 4;
+    static constexpr int kRows = kFew ? 16 : QT * 128;
     static constexpr int kExtra = QT == 2 ? 4 : 3;             // tiles that an item's other work costs
     static constexpr int kLeast = QT == 1 ? 2 : 1;             // units of a run that an item is cut into, at least
     // TMEM columns: S buffers, then O
-    static constexpr int kO = 2 * BK;
-    static constexpr int kPartFloats = kRows * (D + 2);        // O, then m and sum
+    static constexpr int kS = kFew ? kRows : BK, kO = 2 * kS;
+    static constexpr int kPartFloats = (kFew ? 128 : kRows) * (D + 2);   // O, then m and sum
+    static_assert(!kFew || (kQ8 && D == 128), "");
     static_assert(D == 64 || D == 128 || (D == 256 && QT == 1), "");
     static_assert(kO + NS * D <= 512, "TMEM");
     // A team does not meet every use of a barrier, and a parity tells a use from its neighbours, not from the one before
@@ -343,10 +345,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 __device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t leading) { return ((addr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16); }
 
 // Instruction descriptor: fp32 accumulator, A and B both bf16 or both fp16, M =
-// 128, N columns, B K-major or MN-major.
-__host__ __device__ constexpr uint32_t instr(bool f16, int n, bool b_mn)
+// 128, N columns, A and B K-major or MN-major.
+__host__ __device__ constexpr uint32_t instr(bool f16, int n, bool b_mn, bool a_mn = false)
 {
-    return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+    return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(128 >> 4) << 24);
 }
 
@@ -368,10 +370,14 @@ __device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap *map, 
                  : "memory");
 }
 
-// 16 bytes global -> shared, and the wait for all of the thread's
+// 16 bytes global -> shared (or zeros), and the wait for all of the thread's
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -379,6 +385,13 @@ __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// the same down to subnormal results
+__device__ __forceinline__ float exp2_deep(float x)
+{
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 template <bool F16>
@@ -529,6 +542,7 @@ struct Item {
     int32_t pad[2];
 };
 constexpr int kItems = 4;
+constexpr int kPairs = 4;   // kFew: K/V tiles whose factors are kept
 
 template <typename S>
 struct Bars {
@@ -537,6 +551,7 @@ struct Bars {
     uint64_t s_full[2], p_full[2], o_done[2];
     uint64_t q_full[2], q_empty[2], item_full[kItems], item_empty[kItems], drain;
     uint64_t part_full[2], part_known[2];   // the part in a slot is written; the others know
+    uint64_t scaled[S::kFew ? kPairs : 1];  // kFew: the factors of a pair of tiles are there
 };
 
 __device__ __forceinline__ void named_barrier(int id, int threads)
@@ -666,11 +681,14 @@ __device__ __forceinline__ void convert_tiles(Bars<S> &bar, const Item *items, c
     }
 }
 
-template <int D, int QT, bool F16, bool Q8, bool TREE>
-__global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
+#include "attention_few.cuh"
+
+template <int D, int QT_, bool F16, bool Q8, bool TREE>
+__global__ void __launch_bounds__(Shape<D, QT_, Q8, TREE>::kThreads, 1)
     attention_kernel(const __grid_constant__ std::conditional_t<Q8, Args8, Args> a)
 {
-    using S = Shape<D, QT, Q8, TREE>;
+    using S = Shape<D, QT_, Q8, TREE>;
+    constexpr int QT = S::QT;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars<S> bar;
     __shared__ Item items[kItems];
@@ -696,13 +714,15 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 8);
+            mbar_init(&bar.p_full[i], S::kFew ? 4 : 8);
             mbar_init(&bar.o_done[i], 1);
             mbar_init(&bar.q_full[i], 2);
             mbar_init(&bar.q_empty[i], 1);
             mbar_init(&bar.part_full[i], S::kSoftmaxWarps);
             mbar_init(&bar.part_known[i], 1);
         }
+        if constexpr (S::kFew)
+            for (int i = 0; i < kPairs; ++i) mbar_init(&bar.scaled[i], S::kConverters);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&bar.item_full[i], 1);
             mbar_init(&bar.item_empty[i], S::kSoftmaxWarps + 3 + S::kConverters);
@@ -814,9 +834,11 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
     const uint32_t tmem = tmem_slot;
 
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *q_smem = smem, *kv_smem = smem + S::QB * QT * S::kQBytes;
+    uint8_t *q_smem = smem, *p_smem = smem + S::QB * QT * S::kQBytes, *kv_smem = p_smem + S::kPBytes;
     uint8_t *raw_smem = kv_smem + S::kStages * S::kStageBytes;
     float *swap = reinterpret_cast<float *>(raw_smem + S::kRaw * S::kRawBytes);
+    [[maybe_unused]] Few &few = *reinterpret_cast<Few *>(swap);
+    static_assert(!S::kFew || sizeof(Few) <= S::kSwap * 4, "");
 
     if (warp == kLoader) {
         // ---- the items of this CTA's run, and their K and V tiles: a lane of
@@ -968,6 +990,7 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
     } else if (warp == kMma) {
         // ---- the products, issued by one thread (the warp walks along with it)
         constexpr uint32_t kQk = instr(F16, S::BK, false), kPv = instr(F16, D, true);
+        constexpr uint32_t few_qk = instr(true, 16, false), few_pv = instr(true, 16, true, true);   // kFew: 16 columns
         const bool leader = elect_one();
         uint32_t units[2] = {0, 0};                          // units per S buffer
         uint32_t k_stage = 0, k_phase = 0, v_stage = 1, v_phase = 0;   // of the next K and V tile (every second stage use)
@@ -996,11 +1019,18 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
                 fence_after();
                 if (leader) {
                     const uint32_t qa = q_desc + (qb * QT + (QT == 2 ? b : 0)) * (S::kQBytes >> 4), ka = k_desc + k_stage * (S::kStageBytes >> 4);
-                    const uint32_t d = tmem + b * S::BK;
-                    mma_ss<false>(d, qa, ka, kQk);
+                    const uint32_t d = tmem + b * S::kS;
+                    if constexpr (S::kFew) {                 // S^T = K Q^T
+                        mma_ss<false>(d, ka, qa, few_qk);
 #pragma unroll
-                    for (int k = 1; k < D / 16; ++k)
-                        mma_ss<true>(d, qa + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, ka + (k >> 2) * (S::BK * 128 >> 4) + (k & 3) * 2, kQk);
+                        for (int k = 1; k < D / 16; ++k)
+                            mma_ss<true>(d, ka + (k >> 2) * (S::BK * 128 >> 4) + (k & 3) * 2, qa + (k >> 2) * (S::kRows * 128 >> 4) + (k & 3) * 2, few_qk);
+                    } else {
+                        mma_ss<false>(d, qa, ka, kQk);
+#pragma unroll
+                        for (int k = 1; k < D / 16; ++k)
+                            mma_ss<true>(d, qa + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, ka + (k >> 2) * (S::BK * 128 >> 4) + (k & 3) * 2, kQk);
+                    }
                     commit(&bar.s_full[b]);
                     if (QT == 1 || b == 1) commit(&bar.empty[k_stage]);
                     if (i == U - 1) commit(&bar.q_empty[qb]);
@@ -1021,11 +1051,20 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
                 ++units[b];
                 fence_after();
                 if (leader) {
-                    const uint32_t va = v_desc + v_stage * (S::kStageBytes >> 4), d = tmem + S::kO + ob * D, pa = tmem + b * S::BK;
-                    mma_ts(d, pa, va, kPv, S::NS == 2 ? i >= 2 : i >= 1);
+                    const uint32_t va = v_desc + v_stage * (S::kStageBytes >> 4);
+                    if constexpr (S::kFew) {                 // O^T += V^T P^T
+                        const uint32_t d = tmem + S::kO + b * S::kRows, pa = operand(smem_u32(p_smem) + b * (S::BK * 128), 16);
+                        if (i >= 2) mma_ss<true>(d, va, pa, few_pv);
+                        else mma_ss<false>(d, va, pa, few_pv);
 #pragma unroll
-                    for (int k = 1; k < S::BK / 16; ++k)   // the halves' weights lie half a tile apart
-                        mma_ts_acc(d, pa + k / (S::BK / 32) * (S::BK / 2) + k % (S::BK / 32) * 8, va + k * (2048 >> 4), kPv);
+                        for (int k = 1; k < S::BK / 16; ++k) mma_ss<true>(d, va + k * (2048 >> 4), pa + k * (2048 >> 4), few_pv);
+                    } else {
+                        const uint32_t d = tmem + S::kO + ob * D, pa = tmem + b * S::BK;
+                        mma_ts(d, pa, va, kPv, S::NS == 2 ? i >= 2 : i >= 1);
+#pragma unroll
+                        for (int k = 1; k < S::BK / 16; ++k)   // the halves' weights lie half a tile apart
+                            mma_ts_acc(d, pa + k / (S::BK / 32) * (S::BK / 2) + k % (S::BK / 32) * 8, va + k * (2048 >> 4), kPv);
+                    }
                     commit(&bar.o_done[ob]);
                     if (QT == 1 || b == 1) commit(&bar.empty[v_stage]);
                 }
@@ -1042,7 +1081,8 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
         }
         __syncwarp();
     } else if (Q8 && warp >= kConvert) {
-        if constexpr (Q8) convert_tiles<S, F16>(bar, items, raw_smem, kv_smem, min(1 << a.log_page, S::BK), warp - kConvert, lane);
+        if constexpr (S::kFew) convert_bare<S, F16>(bar, items, raw_smem, kv_smem, few, min(1 << a.log_page, S::BK), warp - kConvert, lane);
+        else if constexpr (Q8) convert_tiles<S, F16>(bar, items, raw_smem, kv_smem, min(1 << a.log_page, S::BK), warp - kConvert, lane);
     } else if (warp >= kQLoader) {
         // ---- Q: 16-byte pieces of the item's rows, consecutive lanes on
         // consecutive pieces, all of them on their way together; rows past the item's
@@ -1084,7 +1124,7 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
             if (!__all_sync(kFull, wait(&bar.q_empty[qb], ((n / S::QB) & 1) ^ 1))) break;
             const int64_t row0 = (int64_t)it.rt * S::kRows, have = (int64_t)it.n * a.group - row0;
             const int valid = have < S::kRows ? (int)have : S::kRows;
-            const uint32_t dst = smem_u32(q_smem) + qb * QT * S::kQBytes + (p >> 3) * (128 * 128);
+            const uint32_t dst = smem_u32(q_smem) + qb * QT * S::kQBytes + (p >> 3) * ((S::kFew ? S::kRows : 128) * 128);
             const uint32_t gr = (uint32_t)row0 + r0, tok = div_group(a, gr);
             int h = (int)(gr - tok * a.group);
             const uint16_t *src = a.q + (int64_t)(it.first + (int)tok) * a.qs_t + (int64_t)(it.head * a.group + h) * a.qs_h + p * 8;
@@ -1098,7 +1138,11 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
                     src += carry;
                 }
             }
+            if constexpr (S::kFew)                                     // whole groups of 16 columns: zeros behind the last row
+                for (int r = valid + (r0 - valid % kStep + kStep) % kStep; r < ((valid + 15) & ~15); r += kStep)
+                    copy16(dst + r * 128 + (((p & 7) ^ (r & 7)) << 4), a.q, false);
             copies_landed();
+            if constexpr (S::kFew) scale_rows<F16, kPieces, kStep, S::kRows>(q_smem + qb * QT * S::kQBytes, few.row_factor[n % kItems], a.c, valid, r0, p);
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.q_full[qb]);
@@ -1113,7 +1157,8 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
         const int pair = 1 + st * 4 + quad;                       // barrier of the two warps with these rows
         uint32_t tile_n = 0, s_n[2] = {0, 0}, pv_n = 0;           // tiles so far, units per S buffer, PVs of this stream
         bool stop = false;                                        // a wait gave up: no parts, no joins
-        for (uint32_t n = 0;; ++n) {
+        if constexpr (S::kFew) stop = few_rows<S, F16>(a, bar, items, few, p_smem, kv_smem, tmem, warp, lane);
+        for (uint32_t n = 0; !S::kFew; ++n) {
             const bool ok = wait(&bar.item_full[n % kItems], (n / kItems) & 1);
             // all softmax warps go on or none does: the barriers below count on it
             stop = named_barrier_any(kAllSoftmax, S::kSoftmaxWarps * 32, !ok);
@@ -1398,8 +1443,8 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
             for (int i = 0; i < 16; ++i) o[i] = 0.f;
             auto scales = [&](float mp, float lp, float &fo, float &fp) {
                 const float Mn = fmaxf(M, mp), ref = Mn == -INFINITY ? 0.f : Mn;
-                fo = exp2_fast(M - ref);
-                fp = exp2_fast(mp - ref);
+                fo = S::kFew ? exp2_deep(M - ref) : exp2_fast(M - ref);
+                fp = S::kFew ? exp2_deep(mp - ref) : exp2_fast(mp - ref);
                 M = Mn;
                 L = L * fo + lp * fp;
             };
@@ -1430,13 +1475,14 @@ __global__ void __launch_bounds__(Shape<D, QT, Q8, TREE>::kThreads, 1)
             if (n == 0 || p0 != 0) continue;
             const uint32_t gr = (uint32_t)j.rt * S::kRows + r, tok = div_group(a, gr);
             const int64_t orow = ((int64_t)j.first + tok) * a.heads_q + (int64_t)j.head * a.group + (gr - tok * a.group);
-            const float iv = L == 0.f ? 0.f : 1.f / L;
+            constexpr float kUp = S::kFew ? 0x1p-60f : 1.f, kLogUp = S::kFew ? (float)kDown : 0.f;
+            const float iv = L == 0.f ? 0.f : kUp / L;
             uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + g * 16);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 dst[i] = make_uint4(pack2<F16>(o[8 * i] * iv, o[8 * i + 1] * iv), pack2<F16>(o[8 * i + 2] * iv, o[8 * i + 3] * iv),
                                     pack2<F16>(o[8 * i + 4] * iv, o[8 * i + 5] * iv), pack2<F16>(o[8 * i + 6] * iv, o[8 * i + 7] * iv));
-            if (g == 0 && a.lse) a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+            if (g == 0 && a.lse) a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L) + kLogUp) * kLn2;
         }
     }
     __syncthreads();

@@ -1,0 +1,353 @@
+// Few rows over an 8-bit cache of heads of 128: at most 16 rows an item.  Included by attention.cuh,
+// inside its namespace.
+//
+// Codes widened and scaled in 16 bits, as the other 8-bit variants have them, take some 3
+// instructions of the ALU pipe a code pair, which made a token's step slower than over the 16-bit
+// cache (64 tokens 369 us against 320).  Here the products are transposed, S^T = K Q^T and O^T += V^T P^T: a
+// softmax thread has one key, so that the key's scale is one factor of all its scores, and its
+// value's scale one of all its weights.  Codes then go to fp16 as they are, one instruction a
+// pair, and a thread's 16 columns (rows of q) stay in registers for both passes over them.
+//
+// All products are fp16's.  A bf16 row of q is taken times a power of two that brings its largest element to
+// 2^14 (its eight bits fit; what lies below 2^-38 of the largest is lost, far below what the
+// sums lose).  With t the score in log2 units and v that of the value's scale, the running maximum is of t + v, a weight
+// 2^(t + v - m) is what multiplies the code, and the sum is of weight * 2^-v, that is of
+// 2^(t - m), unrounded.  v runs from -120 (a vector of zeros, for one) to 7, so sums are kept times 2^-kDown, and
+// where references meet 2^x is taken down to subnormals: keys of equal scores may lie 2^127 apart.
+// Weights are fp16 as elsewhere: against a reference 2^7 below the maximum, lag 2^4.
+
+constexpr int kDown = 60;
+
+// What the softmax threads, the converting warps and the Q loaders exchange.
+struct Few {
+    float factors[kPairs][3][128];      // of a pair of tiles' keys: of the score; log2 of the value's, and 1 over it (times 2^-kDown)
+    float row_factor[kItems][16];       // log2 units of a score of the row's, but for its key's factor
+    float ref[2][16], moved[2][16];     // a stream's references, and what its sums are to be multiplied by
+    float top[2][4][16];                // maxima of 32 keys
+    float sum[2][4][16];                // sums over 32 keys
+    float w0[16], w1[16], inv[16];      // weights of the streams' O^T, and 1 over the sum
+    int32_t klo[16], khi[16], token[16];   // keys of a row; its token's row of masks
+    int64_t out_row[16];
+};
+
+// Four codes to four fp16 values, without a scale.
+__device__ __forceinline__ uint2 bare4(uint32_t w)
+{
+    uint2 r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(r.x), "=r"(r.y) : "r"(w));
+    return r;
+}
+
+// The factor of a key's scores, and of a value's scale its log2 and what takes it out of a weight.
+template <bool F16>
+__device__ __forceinline__ float key_factor(uint32_t byte)
+{
+    constexpr uint32_t kLeast = F16 ? 113u : 7u;
+    return byte > 134u ? __uint_as_float(0x7FC00000u) : __uint_as_float((byte < kLeast ? kLeast : byte) << 23);
+}
+template <bool F16>
+__device__ __forceinline__ void value_factors(uint32_t byte, float &log2v, float &inverse)
+{
+    constexpr uint32_t kLeast = F16 ? 113u : 7u;
+    const uint32_t b = byte < kLeast ? kLeast : byte > 134u ? 127u : byte;   // (no number: its codes say so)
+    log2v = (float)((int)b - 127);
+    inverse = __uint_as_float((254u - kDown - b) << 23);
+}
+
+// The converting warps: all of them share a tile, a thread 16 codes of a row at a time (as
+// convert_tiles, whose comments hold here too).
+template <typename S, bool F16>
+__device__ __forceinline__ void convert_bare(Bars<S> &bar, const Item *items, const uint8_t *raw_smem, uint8_t *kv_smem, Few &few,
+                                             int rows, int warp, int lane)
+{
+    constexpr int kPieces = S::D / 16, kStep = S::kConverters * 32 / kPieces, kPasses = S::BK / kStep;
+    static_assert(kStep % 8 == 0 && S::BK % kStep == 0 && S::BK <= S::kConverters * 32, "");
+    const int id = warp * 32 + lane, p = id % kPieces, r0 = id / kPieces;
+    const int block = p >> 2, piece = (p & 3) * 2, flip = block & 1;
+    const uint32_t x0 = ((piece + flip) ^ (r0 & 7)) << 4, x1 = x0 ^ 16;
+    uint8_t *const to = kv_smem + block * (S::BK * 128) + r0 * 128;
+    const int log_rows = 31 - __clz(rows), scale_at = S::kRawCodes + (id >> log_rows) * 128 + (id & (rows - 1));   // of key id
+    uint32_t rb = 0, rb_phase = 0, st = 0, st_phase = 0, pair = 0;   // barrier of the tile's slot, its stage, its factors
+    for (uint32_t n = 0;; ++n) {
+        if (!__all_sync(kFull, wait(&bar.item_full[n % kItems], (n / kItems) & 1))) return;
+        const int tiles = items[n % kItems].tiles;
+        __syncwarp();
+        if (tiles == 0) return;
+        if (lane == 0) mbar_arrive(&bar.item_empty[n % kItems]);
+        for (int t = 0; t < 2 * tiles; ++t) {
+            const uint32_t rs = rb < (uint32_t)S::kRaw ? rb : rb - S::kRaw;
+            if (!__all_sync(kFull, wait(&bar.raw_full[rb], rb_phase))) return;
+            const uint8_t *raw = raw_smem + rs * S::kRawBytes;
+            uint4 w[kPasses];
+            uint32_t byte = 0;
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + id * 16 + i * (kStep * S::D));
+            if (id < S::BK) byte = raw[scale_at];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
+            // the factors are there before the tile is: the softmax need not wait for a stage
+            if (id < S::BK) {
+                if (t & 1) value_factors<F16>(byte, few.factors[pair][1][id], few.factors[pair][2][id]);
+                else few.factors[pair][0][id] = key_factor<F16>(byte);
+            }
+            if (t & 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.scaled[pair]);
+                pair = (pair + 1) % kPairs;
+            }
+            if (!__all_sync(kFull, wait(&bar.empty[st], st_phase ^ 1))) return;
+            uint8_t *tile = to + st * S::kStageBytes;
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const uint2 b0 = bare4(w[i].x), b1 = bare4(w[i].y), b2 = bare4(w[i].z), b3 = bare4(w[i].w);
+                const uint4 u = make_uint4(b0.x, b0.y, b1.x, b1.y), v = make_uint4(b2.x, b2.y, b3.x, b3.y);
+                *reinterpret_cast<uint4 *>(tile + i * (kStep * 128) + x0) = flip ? v : u;
+                *reinterpret_cast<uint4 *>(tile + i * (kStep * 128) + x1) = flip ? u : v;
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.full[st]);
+            if (++rb == 2u * S::kRaw) {
+                rb = 0;
+                rb_phase ^= 1;
+            }
+            if (++st == (uint32_t)S::kStages) {
+                st = 0;
+                st_phase ^= 1;
+            }
+        }
+    }
+}
+
+// An item's rows of q, which the lanes copied: bf16 to fp16 in place, each with its factor.  A
+// row's pieces are with kPieces neighbouring lanes, each with what it copied itself.
+template <bool F16, int kPieces, int kStep, int kRows>
+__device__ __forceinline__ void scale_rows(uint8_t *q, float *factor, float c, int valid, int r0, int p)
+{
+    const int columns = (valid + 15) & ~15;
+    for (int r = r0; r - r0 < columns; r += kStep) {     // (a warp's lanes go on together)
+        int up = 0;
+        if (!F16) {
+            uint4 *at = reinterpret_cast<uint4 *>(q + (p >> 3) * (kRows * 128) + r * 128 + (((p & 7) ^ (r & 7)) << 4));
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (r < valid) x = *at;
+            uint32_t most = 0u;
+#pragma unroll
+            for (uint32_t w : {x.x, x.y, x.z, x.w}) most = max(most, max(w & 0x7FFFu, w >> 16 & 0x7FFFu));
+#pragma unroll
+            for (int d = 1; d < kPieces; d <<= 1) most = max(most, __shfl_xor_sync(kFull, most, d));
+            const int e = (int)(most >> 7);              // the largest's exponent + 127
+            up = e == 255 ? 0 : min(141 - e, 126);       // (no numbers: as they are)
+            const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+            auto two16 = [&](uint32_t w) { return pack2<true>(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f); };
+            if (r < valid) *at = make_uint4(two16(x.x), two16(x.y), two16(x.z), two16(x.w));
+        }
+        if (p == 0 && r < columns) factor[r] = r < valid ? c * __uint_as_float((uint32_t)(127 - up) << 23) : 0.f;
+    }
+}
+
+// Softmax, correction and epilogue of the softmax warps, four a stream: a thread a key of its tiles.  Returns
+// whether a wait gave up.
+template <typename S, bool F16>
+__device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item *items, Few &few, uint8_t *p_smem, uint8_t *kv_smem,
+                                         uint32_t tmem, int warp, int lane)
+{
+    constexpr int kAll = S::kSoftmaxWarps * 32;
+    constexpr float kPast = kLag<true> + kRaise<true>;
+    const int st = warp >> 2, quad = warp & 3, key = quad * 32 + lane, tid = warp * 32 + lane, stream_barrier = 1 + st;
+    const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+    uint8_t *const weights = p_smem + st * (S::BK * 128) + key * 128;
+    uint32_t tile_n = 0, s_n = 0, pv_n = 0;                   // tiles so far, units and products of this stream
+    for (uint32_t n = 0;; ++n) {
+        const bool ok = wait(&bar.item_full[n % kItems], (n / kItems) & 1);
+        // all softmax warps go on or none does: the barriers below count on it
+        if (named_barrier_any(kAllSoftmax, kAll, !ok)) return true;
+        const Item &it = items[n % kItems];
+        const int tiles = it.tiles;
+        if (tiles == 0) return false;
+        const int lo = it.lo, hi = it.hi, tile0 = it.tile, ctx = it.seq - it.n;
+        const int64_t row0 = (int64_t)it.rt * S::kRows, left = (int64_t)it.n * a.group - row0;
+        const int rows = left < S::kRows ? (int)left : S::kRows;
+        if (tid < S::kRows) {
+            const bool valid = tid < rows;
+            const uint32_t gr = (uint32_t)row0 + (valid ? tid : 0), tok = div_group(a, gr);
+            const uint32_t *mask = S::kTree ? a.masks + (int64_t)(it.first + (int)tok) * a.mask_words : nullptr;
+            const int64_t klo = a.window > 0 ? (int64_t)ctx + (S::kTree ? node_depth(mask, a.mask_words, (int)tok) : (int)tok) - a.window + 1 : 0;
+            few.klo[tid] = klo > 0 ? (int)klo : 0;
+            few.khi[tid] = valid ? ctx + (int)tok + 1 : -1;
+            few.token[tid] = it.first + (int)tok;
+            few.out_row[tid] = ((int64_t)it.first + tok) * a.heads_q + (int64_t)it.head * a.group + (gr - tok * a.group);
+        }
+        if (tid < 32) few.ref[tid >> 4][tid & 15] = -INFINITY;
+        named_barrier(kAllSoftmax, kAll);
+        // no tile within these has a key that some row does not see
+        const int tok0 = (int)div_group(a, (uint32_t)row0), tok1 = (int)div_group(a, (uint32_t)row0 + rows - 1);
+        const int64_t last_lo = a.window > 0 ? (int64_t)ctx + tok1 - a.window + 1 : 0;
+        const int first_hi = S::kTree ? ctx : ctx + tok0 + 1;
+
+        float l[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) l[e] = 0.f;
+        const int U = (tiles - st + 1) >> 1;
+        for (int i = 0; i < U; ++i) {
+            const int t = 2 * i + st, key0 = (tile0 + t) * S::BK, at = key0 + key;
+            const uint32_t pair = tile_n + t;
+            wait(&bar.scaled[pair % kPairs], (pair / kPairs) & 1);
+            const float *f = few.factors[pair % kPairs][0] + key;
+            const float ks = f[0], v = f[128], over = f[256];
+            wait(&bar.s_full[st], s_n++ & 1);
+            // the weights of the last tile are read, and its product may be multiplied
+            if (i > 0) wait(&bar.o_done[st], (pv_n - 1) & 1);
+            fence_after();
+            const bool edge = key0 < last_lo || key0 + S::BK > first_hi;
+            {
+                uint32_t x[16];
+                float u[16];
+                tmem_ld16(x, tmem + lane_base + st * S::kRows);
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 c = *reinterpret_cast<const float4 *>(&few.row_factor[n % kItems][e]);
+                    u[e] = fmaf(__uint_as_float(x[e]) * ks, c.x, v);
+                    u[e + 1] = fmaf(__uint_as_float(x[e + 1]) * ks, c.y, v);
+                    u[e + 2] = fmaf(__uint_as_float(x[e + 2]) * ks, c.z, v);
+                    u[e + 3] = fmaf(__uint_as_float(x[e + 3]) * ks, c.w, v);
+                }
+                if (edge) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        bool sees = at >= few.klo[e] && at < few.khi[e];
+                        if (S::kTree && sees && at >= ctx) {
+                            const int node = at - ctx;
+                            sees = (node >> 5) < a.mask_words &&
+                                   (__ldg(a.masks + (int64_t)few.token[e] * a.mask_words + (node >> 5)) >> (node & 31) & 1u);
+                        }
+                        if (!sees) u[e] = -INFINITY;
+                    }
+                }
+                bool past = false;
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 m = *reinterpret_cast<const float4 *>(&few.ref[st][e]);
+                    past = past || u[e] > m.x + kPast || u[e + 1] > m.y + kPast || u[e + 2] > m.z + kPast || u[e + 3] > m.w + kPast;
+                }
+                if (named_barrier_any(stream_barrier, 128, past)) {
+                    // new references, for the columns that are past the lag (or have their first key)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float top;
+                        asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top) : "f"(u[e]));
+                        if (lane == 0) few.top[st][quad][e] = top;
+                    }
+                    named_barrier(stream_barrier, 128);
+                    if (quad == 0 && lane < 16) {
+                        const float top = fmaxf(fmaxf(few.top[st][0][lane], few.top[st][1][lane]), fmaxf(few.top[st][2][lane], few.top[st][3][lane]));
+                        const float m = few.ref[st][lane], to = top - kRaise<true>;
+                        const bool move = top > m + kPast;     // (m = -inf: any key's)
+                        few.moved[st][lane] = move ? exp2_deep(m - to) : 1.f;
+                        if (move) few.ref[st][lane] = to;
+                    }
+                    named_barrier(stream_barrier, 128);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) l[e] *= few.moved[st][e];
+                    if (i > 0) {
+                        const uint32_t oa = tmem + lane_base + S::kO + st * S::kRows;
+                        uint32_t o[16];
+                        tmem_ld16(o, oa);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * few.moved[st][e]);
+                        tmem_st16(oa, o);
+                    }
+                }
+                uint32_t pk[8];
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const float2 m = *reinterpret_cast<const float2 *>(&few.ref[st][e]);
+                    const float p0 = exp2_fast(u[e] - (m.x == -INFINITY ? 0.f : m.x)), p1 = exp2_fast(u[e + 1] - (m.y == -INFINITY ? 0.f : m.y));
+                    l[e] = fmaf(p0, over, l[e]);
+                    l[e + 1] = fmaf(p1, over, l[e + 1]);
+                    pk[e / 2] = pack2<true>(p0, p1);
+                }
+                *reinterpret_cast<uint4 *>(weights + ((key & 7) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                *reinterpret_cast<uint4 *>(weights + ((1 ^ (key & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+            }
+            // V rows that no row of the item may see hold anything, NaN included: 0 * NaN must not reach O
+            if (key0 < lo || key0 + S::BK > hi) {
+                const uint32_t idx = 2 * pair + 1, vs = idx % S::kStages;
+                wait(&bar.full[vs], (idx / S::kStages) & 1);
+                if (at < lo || at >= hi) {
+                    uint8_t *row = kv_smem + vs * S::kStageBytes + key * 128;
+#pragma unroll
+                    for (int k = 0; k < 2 * 8; ++k) *reinterpret_cast<uint4 *>(row + (k >> 3) * (S::BK * 128) + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            fence_proxy_async();
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.p_full[st]);
+            ++pv_n;
+        }
+        tile_n += tiles;
+        if (U > 0) wait(&bar.o_done[st], (pv_n - 1) & 1);
+
+        // the columns' sums over the keys and the streams
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float x = warp_sum_f(l[e]);
+            if (lane == 0) few.sum[st][quad][e] = x;
+        }
+        fence_before();
+        named_barrier(kAllSoftmax, kAll);
+        fence_after();
+        const int slot = it.slot;
+        const bool split = slot >= 0;
+        float *part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * S::kPartFloats;
+        if (tid < S::kRows) {
+            const float m0 = few.ref[0][tid], m1 = few.ref[1][tid], m = fmaxf(m0, m1);
+            const float f0 = m0 == -INFINITY ? 0.f : exp2_deep(m0 - m), f1 = m1 == -INFINITY ? 0.f : exp2_deep(m1 - m);
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                s0 += few.sum[0][q][tid];
+                s1 += few.sum[1][q][tid];
+            }
+            const float sum = s0 * f0 + s1 * f1;
+            few.w0[tid] = f0;
+            few.w1[tid] = tiles > 1 ? f1 : 0.f;
+            few.inv[tid] = sum == 0.f ? 0.f : split ? 1.f : 0x1p-60f / sum;   // (NaN scores: NaN)
+            if (tid < rows) {
+                if (split) {
+                    part[128 * S::D + tid] = m;
+                    part[128 * S::D + 128 + tid] = sum;
+                } else if (a.lse) {
+                    a.lse[few.out_row[tid]] = sum == 0.f ? -INFINITY : (m + log2f(sum) + (float)kDown) * kLn2;
+                }
+            }
+        }
+        named_barrier(kAllSoftmax, kAll);
+        // O^T: this thread has an element of every row; each stream's warps write half the rows
+        if (st * 8 < rows) {
+            uint32_t o0[16], o1[16];
+            tmem_ld16(o0, tmem + lane_base + S::kO);
+            if (tiles > 1) tmem_ld16(o1, tmem + lane_base + S::kO + S::kRows);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int row = e;
+                if ((e >> 3) != st) continue;
+                const float f0 = few.w0[row], f1 = few.w1[row], inv = few.inv[row];
+                const float v = (f0 > 0.f ? __uint_as_float(o0[e]) * f0 : 0.f) + (f1 > 0.f ? __uint_as_float(o1[e]) * f1 : 0.f);
+                if (row >= rows) continue;
+                if (split) part[((key >> 2) * 128 + row) * 4 + (key & 3)] = inv == 0.f ? 0.f : v;
+                else a.out[few.out_row[row] * S::D + key] = (uint16_t)pack2<F16>(inv == 0.f ? 0.f : v * inv, 0.f);
+            }
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            if (split) mbar_arrive(&bar.part_full[slot]);
+            mbar_arrive(&bar.item_empty[n % kItems]);
+        }
+        // (O, Few and the barriers are used again only past the barrier at the next item's start)
+    }
+}

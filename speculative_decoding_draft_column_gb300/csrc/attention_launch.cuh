@@ -99,7 +99,7 @@ spec_status launch_one(const A &a, int64_t chunk, int dev, int grid)
 // What picks the variant besides the kind of cache and of mask.
 struct Pick {
     int32_t head_dim;      // 64, 128 or 256
-    bool two, f16;         // two row tiles share every K/V tile; fp16
+    bool two, few, f16;    // two row tiles share every K/V tile; at most 16 rows an item; fp16
     int64_t chunk;         // new tokens of a lane to expect
     int dev, grid;
 };
@@ -110,6 +110,8 @@ spec_status launch(const A &a, const Pick &p)
     auto go = [&](auto kernel) { return kernel(a, p.chunk, p.dev, p.grid); };
     if (p.head_dim == 256) return go(p.f16 ? launch_one<256, 1, true, Q8, TREE, A> : launch_one<256, 1, false, Q8, TREE, A>);
     if (p.head_dim == 128) {
+        if constexpr (Q8)
+            if (p.few) return go(p.f16 ? launch_one<128, 0, true, Q8, TREE, A> : launch_one<128, 0, false, Q8, TREE, A>);
         if (p.two) return go(p.f16 ? launch_one<128, 2, true, Q8, TREE, A> : launch_one<128, 2, false, Q8, TREE, A>);
         return go(p.f16 ? launch_one<128, 1, true, Q8, TREE, A> : launch_one<128, 1, false, Q8, TREE, A>);
     }

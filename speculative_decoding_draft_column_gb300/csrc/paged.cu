@@ -263,7 +263,8 @@ spec_status attention_call(const AttentionCall &call)
     a.mask_words = call.mask_words;
     const int64_t hint = max_new < tokens ? max_new : tokens, chunk = hint > 0 ? hint : (tokens + b.lanes - 1) / b.lanes;
     const bool two = chunk * a.group > 128;   // more rows than one tile: two tiles share every K/V tile
-    const attn::Pick pick = {c.head_dim, two, c.dtype == SPEC_F16, chunk, d->index, attention_grid(*d)};
+    const bool few = chunk * a.group <= 16;   // (8 bits, heads of 128)
+    const attn::Pick pick = {c.head_dim, two, few, c.dtype == SPEC_F16, chunk, d->index, attention_grid(*d)};
     if (eight) return attn::launch8(a, pick, call.tree);
     const attn::Args &a16 = a;
     return call.tree ? attn::launch_tree(a16, pick) : attn::launch<false, false>(a16, pick);
