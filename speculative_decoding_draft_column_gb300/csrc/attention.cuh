@@ -86,10 +86,10 @@ struct Shape {
     static constexpr int kQBytes = (kFew ? 16 : 128) * D * 2;  // one row tile
     static constexpr int kStageBytes = BK * D * 2;             // a K or a V tile
     static constexpr int QB = QT == 1 && D <= (kQ8 ? 64 : 128) ? 2 : 1;   // Q buffers
-    static constexpr int kPBytes = kFew ? NS * BK * 128 : 0;   // weights of a tile, a stream
+    static constexpr int kPBytes = kFew ? BK * 128 : 0;        // weights of the streams' tiles
     static constexpr int kRoom = 224 * 1024 - QB * QT * kQBytes - kPBytes;
     // 8 bits: as many 16-bit tiles as keep the products fed, the rest for tiles of codes on their way
-    static constexpr int kStages = kQ8 ? (D == 64 ? 6 : QT == 1 && D == 128 && !kFew ? 4 : 3) : kRoom / kStageBytes < 12 ? kRoom / kStageBytes : 12;
+    static constexpr int kStages = kQ8 ? (D == 64 ? 6 : QT == 1 && D == 128 ? 4 : 3) : kRoom / kStageBytes < 12 ? kRoom / kStageBytes : 12;
     static constexpr int kRawCodes = BK * D;                   // codes of a tile, then 128 bytes for a page's scales
     static constexpr int kRawBytes = kRawCodes + BK / 16 * 128;
     static constexpr int kRawMost = (kRoom - kStages * kStageBytes) / kRawBytes;
@@ -1053,7 +1053,7 @@ __global__ void __launch_bounds__(Shape<D, QT_, Q8, TREE>::kThreads, 1)
                 if (leader) {
                     const uint32_t va = v_desc + v_stage * (S::kStageBytes >> 4);
                     if constexpr (S::kFew) {                 // O^T += V^T P^T
-                        const uint32_t d = tmem + S::kO + b * S::kRows, pa = operand(smem_u32(p_smem) + b * (S::BK * 128), 16);
+                        const uint32_t d = tmem + S::kO + b * S::kRows, pa = operand(smem_u32(p_smem) + b * 32, 16);   // (the streams' columns side by side)
                         if (i >= 2) mma_ss<true>(d, va, pa, few_pv);
                         else mma_ss<false>(d, va, pa, few_pv);
 #pragma unroll

@@ -157,7 +157,7 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
     constexpr float kPast = kLag<true> + kRaise<true>;
     const int st = warp >> 2, quad = warp & 3, key = quad * 32 + lane, tid = warp * 32 + lane, stream_barrier = 1 + st;
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-    uint8_t *const weights = p_smem + st * (S::BK * 128) + key * 128;
+    uint8_t *const weights = p_smem + key * 128;              // 16 columns of either stream
     uint32_t tile_n = 0, s_n = 0, pv_n = 0;                   // tiles so far, units and products of this stream
     for (uint32_t n = 0;; ++n) {
         const bool ok = wait(&bar.item_full[n % kItems], (n / kItems) & 1);
@@ -268,8 +268,8 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
                     l[e + 1] = fmaf(p1, over, l[e + 1]);
                     pk[e / 2] = pack2<true>(p0, p1);
                 }
-                *reinterpret_cast<uint4 *>(weights + ((key & 7) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                *reinterpret_cast<uint4 *>(weights + ((1 ^ (key & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                *reinterpret_cast<uint4 *>(weights + ((2 * st ^ (key & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                *reinterpret_cast<uint4 *>(weights + ((2 * st + 1 ^ (key & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
             }
             // V rows that no row of the item may see hold anything, NaN included: 0 * NaN must not reach O
             if (key0 < lo || key0 + S::BK > hi) {
