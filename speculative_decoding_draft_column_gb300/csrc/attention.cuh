@@ -98,9 +98,10 @@ struct Shape {
     // converting warps, in teams of four that take half tiles in turn (64 registers a thread with three teams: two row tiles
     // have the softmax of twice the rows to compute with them, 2.60 against 2.49 us a tile)
     static constexpr int kTeams = QT == 1 && D <= 128 && !kFew ? 3 : 2;
+    static constexpr int kTileWarps = kFew ? 4 : 8;            // that convert a tile (kFew: a team K tiles, one V tiles)
     static constexpr int kConverters = kQ8 ? kTeams * 4 : 0;
     static constexpr int kThreads = kSoftmaxWarps * 32 + 128 + kConverters * 32;  // softmax; K/V loader, MMA, two Q loaders; converters
-    static constexpr int kSwap = kFew ? 2048 : 512;            // floats that softmax warps exchange through (kFew: struct Few)
+    static constexpr int kSwap = kFew ? 2432 : 512;            // floats that softmax warps exchange through (kFew: struct Few)
     static constexpr int kPayload = QB * QT * kQBytes + kPBytes + kStages * kStageBytes + kRaw * kRawBytes + kSwap * 4;
     static constexpr int kRows = kFew ? 16 : QT * 128;
     static constexpr int kExtra = QT == 2 ? 4 : 3;             // tiles that an item's other work costs
@@ -542,7 +543,7 @@ struct Item {
     int32_t pad[2];
 };
 constexpr int kItems = 4;
-constexpr int kPairs = 4;   // kFew: K/V tiles whose factors are kept
+constexpr int kPairs = 5;   // kFew: K/V tiles whose factors are kept
 
 template <typename S>
 struct Bars {
@@ -704,13 +705,13 @@ __global__ void __launch_bounds__(Shape<D, QT_, Q8, TREE>::kThreads, 1)
     if (tid == 0) {
         s_gave_up = 0u;
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&bar.full[i], Q8 ? 8 : 1);                // (8 bits: two halves by four warps)
+            mbar_init(&bar.full[i], Q8 ? S::kTileWarps : 1);
             mbar_init(&bar.empty[i], 1);
         }
         for (int i = 0; i < S::kRaw; ++i) {
             mbar_init(&bar.raw_full[i], 1);
             mbar_init(&bar.raw_full[S::kRaw + i], 1);
-            mbar_init(&bar.raw_empty[i], 8);
+            mbar_init(&bar.raw_empty[i], S::kTileWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(Shape<D, QT_, Q8, TREE>::kThreads, 1)
             mbar_init(&bar.part_known[i], 1);
         }
         if constexpr (S::kFew)
-            for (int i = 0; i < kPairs; ++i) mbar_init(&bar.scaled[i], S::kConverters);
+            for (int i = 0; i < kPairs; ++i) mbar_init(&bar.scaled[i], 2 * S::kTileWarps);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&bar.item_full[i], 1);
             mbar_init(&bar.item_empty[i], S::kSoftmaxWarps + 3 + S::kConverters);

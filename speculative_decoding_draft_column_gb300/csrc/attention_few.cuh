@@ -55,47 +55,46 @@ __device__ __forceinline__ void value_factors(uint32_t byte, float &log2v, float
     inverse = __uint_as_float((254u - kDown - b) << 23);
 }
 
-// The converting warps: all of them share a tile, a thread 16 codes of a row at a time (as
-// convert_tiles, whose comments hold here too).
+// The converting warps: a team of four the K tiles, another the V tiles, a thread 16 codes of a row at a time (as
+// convert_tiles, whose comments hold here too).  Stages and barriers of slots are even in number, so that a
+// team meets every use of its own.
 template <typename S, bool F16>
 __device__ __forceinline__ void convert_bare(Bars<S> &bar, const Item *items, const uint8_t *raw_smem, uint8_t *kv_smem, Few &few,
                                              int rows, int warp, int lane)
 {
-    constexpr int kPieces = S::D / 16, kStep = S::kConverters * 32 / kPieces, kPasses = S::BK / kStep;
-    static_assert(kStep % 8 == 0 && S::BK % kStep == 0 && S::BK <= S::kConverters * 32, "");
-    const int id = warp * 32 + lane, p = id % kPieces, r0 = id / kPieces;
+    constexpr int kPieces = S::D / 16, kStep = 128 / kPieces, kPasses = S::BK / kStep;
+    static_assert(kStep % 8 == 0 && S::BK == 128 && S::kConverters == 8, "");
+    // The K tile kPairs on is read once the one before it is converted, that is, once the one kStages / 2 before that is
+    // read, by a product that is issued after that of the weights two tiles earlier.
+    static_assert(S::kStages % 2 == 0 && kPairs >= S::kStages / 2 + 3, "factors that are still read");
+    const int team = warp >> 2, id = (warp & 3) * 32 + lane, p = id % kPieces, r0 = id / kPieces;
     const int block = p >> 2, piece = (p & 3) * 2, flip = block & 1;
     const uint32_t x0 = ((piece + flip) ^ (r0 & 7)) << 4, x1 = x0 ^ 16;
     uint8_t *const to = kv_smem + block * (S::BK * 128) + r0 * 128;
     const int log_rows = 31 - __clz(rows), scale_at = S::kRawCodes + (id >> log_rows) * 128 + (id & (rows - 1));   // of key id
-    uint32_t rb = 0, rb_phase = 0, st = 0, st_phase = 0, pair = 0;   // barrier of the tile's slot, its stage, its factors
+    uint32_t rb = team, rb_phase = 0, st = team, st_phase = 0, pair = 0;   // barrier of the tile's slot, its stage, its factors
     for (uint32_t n = 0;; ++n) {
         if (!__all_sync(kFull, wait(&bar.item_full[n % kItems], (n / kItems) & 1))) return;
         const int tiles = items[n % kItems].tiles;
         __syncwarp();
         if (tiles == 0) return;
         if (lane == 0) mbar_arrive(&bar.item_empty[n % kItems]);
-        for (int t = 0; t < 2 * tiles; ++t) {
+        for (int t = 0; t < tiles; ++t) {
             const uint32_t rs = rb < (uint32_t)S::kRaw ? rb : rb - S::kRaw;
             if (!__all_sync(kFull, wait(&bar.raw_full[rb], rb_phase))) return;
             const uint8_t *raw = raw_smem + rs * S::kRawBytes;
             uint4 w[kPasses];
-            uint32_t byte = 0;
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + id * 16 + i * (kStep * S::D));
-            if (id < S::BK) byte = raw[scale_at];
+            const uint32_t byte = raw[scale_at];
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
             // the factors are there before the tile is: the softmax need not wait for a stage
-            if (id < S::BK) {
-                if (t & 1) value_factors<F16>(byte, few.factors[pair][1][id], few.factors[pair][2][id]);
-                else few.factors[pair][0][id] = key_factor<F16>(byte);
-            }
-            if (t & 1) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.scaled[pair]);
-                pair = (pair + 1) % kPairs;
-            }
+            if (team) value_factors<F16>(byte, few.factors[pair][1][id], few.factors[pair][2][id]);
+            else few.factors[pair][0][id] = key_factor<F16>(byte);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.scaled[pair]);
+            pair = pair + 1 < kPairs ? pair + 1 : 0;
             if (!__all_sync(kFull, wait(&bar.empty[st], st_phase ^ 1))) return;
             uint8_t *tile = to + st * S::kStageBytes;
 #pragma unroll
@@ -108,12 +107,14 @@ __device__ __forceinline__ void convert_bare(Bars<S> &bar, const Item *items, co
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.full[st]);
-            if (++rb == 2u * S::kRaw) {
-                rb = 0;
+            rb += 2;
+            if (rb >= 2u * S::kRaw) {
+                rb -= 2 * S::kRaw;
                 rb_phase ^= 1;
             }
-            if (++st == (uint32_t)S::kStages) {
-                st = 0;
+            st += 2;
+            if (st >= (uint32_t)S::kStages) {
+                st -= S::kStages;
                 st_phase ^= 1;
             }
         }
