@@ -423,15 +423,15 @@ typedef struct {
  * 448 * 2^e, from -120 (fp16: -14) to 7; element x becomes the code nearest to
  * x / 2^e (ties to even).  So a value is off by at most 2^-4 of itself or 2^-10 * 2^e;
  * magnitudes above 57,344 become 57,344, and a vector that holds an infinity or a
- * NaN reads as NaN throughout (scale 255, codes 127). */
+ * NaN reads as NaN throughout (scale 255, codes 127).  A cache of at most 524,280 heads. */
 spec_status spec_paged_store8(const void *k, const void *v, int64_t tokens, int64_t k_token_stride,
                               int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
                               const int64_t *slots, const spec_paged_cache8 *cache);
 
 /* spec_paged_attention over an 8-bit cache: the same arguments, workspace and
- * limits, pages of 16 tokens or more, q and out of type cache->dtype.  Codes times
- * their scale are exact in dtype, so the result is that of spec_paged_attention over
- * those values.  What the cache holds past a lane's last position or before its
+ * limits, pages of 16 tokens or more, q and out of type cache->dtype.  The result is that of
+ * spec_paged_attention over the values that the codes and scales stand for (which
+ * dtype holds exactly); scales above 134 stand for a vector that is no number.  What the cache holds past a lane's last position or before its
  * window, scales included, does not matter. */
 spec_status spec_paged_attention8(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
                                   int64_t q_head_stride, const spec_paged_cache8 *cache, const spec_paged_batch *batch,
@@ -497,7 +497,7 @@ spec_status spec_tree_attention8(const void *q, int64_t tokens, int32_t heads_q,
  *   out_path       int32 [lanes][depth+1]: 0 (the anchor), the accepted nodes, then -1.
  * For a chain of gamma = depth drafts this is spec_verify_v.  Only the columns of a
  * lane's path have to be read, and where there are many nodes only they are.  lanes at
- * most 65,535.  Outputs must not overlap inputs or each other.  One launch; scratch as for spec_verify
+ * most 65,535; cu must not decrease.  Outputs must not overlap inputs or each other.  One launch; scratch as for spec_verify
  * (spec_reserve(tokens, top_k, lanes, SPEC_MAX_GAMMA) covers it). */
 spec_status spec_tree_verify(const uint16_t *target_logits, const int32_t *drafts, const int32_t *parents,
                              const int32_t *cu, int64_t tokens, int64_t lanes, int32_t depth, int64_t V,

@@ -55,6 +55,18 @@
 // 1-2, product 0.4, output 1), and 3 us more where parts are joined.  Neither the exponentials (a polynomial for a
 // quarter of them: 748 -> 804 us) nor the second pass over S (held back in registers: 745 -> 769 us)
 // nor the weights' last columns (their product in two lots: 733 -> 742 us) is what a chunk waits for.
+//
+// Variants.  Trees: a row sees the cached keys and the new tokens of its mask; on the tiles past the cached
+// keys a thread selects by the mask's bits.  8-bit caches: tiles of codes arrive by TMA, a box for K, V and their
+// scales each, and converting warps widen them into the 16-bit tiles that the products read
+// (bf16: 9 instructions for four codes, sign and fraction moved by halves of bytes, one
+// multiplication by 2^120 times the scale; fp16 has an instruction for the conversion).  What bounds them: slots and
+// stages are few beside 16-bit tiles of 32 KB, and a tile passes from copy to converters to products in some 3,000
+// cycles.  1.61 us a pair of K and V tiles of one row tile (0.87 over 16 bits from L2, 1.45 from DRAM), 2.49 of two
+// (1.92): 16 tokens at 262,128 keys 181 us (161 over 16 bits), 8 trees of 64 nodes 108 (91).  So the 8-bit
+// cache takes half the memory, and is faster where rows are few (attention_few.cuh: 283 us against 320).
+// Converters tried: four warps, 2.54 us a pair; eight in lockstep 1.70; copies by the
+// converting warps themselves, without TMA, 2.03; scales by cp.async 1.62 (pages of 16 tokens 1.84 instead of 2.10).
 #pragma once
 
 #include <cuda.h>
@@ -1480,14 +1492,13 @@ __global__ void __launch_bounds__(Shape<D, QT_, Q8, TREE>::kThreads, 1)
             if (n == 0 || p0 != 0) continue;
             const uint32_t gr = (uint32_t)j.rt * S::kRows + r, tok = div_group(a, gr);
             const int64_t orow = ((int64_t)j.first + tok) * a.heads_q + (int64_t)j.head * a.group + (gr - tok * a.group);
-            constexpr float kUp = S::kFew ? 0x1p-60f : 1.f, kLogUp = S::kFew ? (float)kDown : 0.f;
-            const float iv = L == 0.f ? 0.f : kUp / L;
+            const float iv = L == 0.f ? 0.f : (S::kFew ? 0x1p-60f : 1.f) / L;
             uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + g * 16);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 dst[i] = make_uint4(pack2<F16>(o[8 * i] * iv, o[8 * i + 1] * iv), pack2<F16>(o[8 * i + 2] * iv, o[8 * i + 3] * iv),
                                     pack2<F16>(o[8 * i + 4] * iv, o[8 * i + 5] * iv), pack2<F16>(o[8 * i + 6] * iv, o[8 * i + 7] * iv));
-            if (g == 0 && a.lse) a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L) + kLogUp) * kLn2;
+            if (g == 0 && a.lse) a.lse[orow] = L == 0.f ? -INFINITY : (S::kFew ? log2_up(M, L) : M + log2f(L)) * kLn2;
         }
     }
     __syncthreads();

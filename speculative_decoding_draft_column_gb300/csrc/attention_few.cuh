@@ -1,12 +1,17 @@
 // Few rows over an 8-bit cache of heads of 128: at most 16 rows an item.  Included by attention.cuh,
 // inside its namespace.
 //
-// Codes widened and scaled in 16 bits, as the other 8-bit variants have them, take some 3
-// instructions of the ALU pipe a code pair, which made a token's step slower than over the 16-bit
-// cache (64 tokens 369 us against 320).  Here the products are transposed, S^T = K Q^T and O^T += V^T P^T: a
-// softmax thread has one key, so that the key's scale is one factor of all its scores, and its
-// value's scale one of all its weights.  Codes then go to fp16 as they are, one instruction a
-// pair, and a thread's 16 columns (rows of q) stay in registers for both passes over them.
+// Codes widened and scaled in 16 bits, as the other 8-bit variants have them, take 4.5
+// instructions a pair of codes, two thirds of them of the ALU pipe, and made a token's step slower than over the
+// 16-bit cache (64 tokens of 4 rows a head at 500-16,000 keys 369 us against 320).  Here the products are
+// transposed, S^T = K Q^T and O^T += V^T P^T: a softmax thread has one key, so that the key's scale is one
+// factor of all its scores, and its value's scale one of all its weights.  Codes then go to fp16 as they
+// are, one instruction a pair, and a thread's 16 columns (rows of q) stay in registers for both passes over
+// them.  281 us, 3.8 TB/s.  What bounds it: chains, none of them full.  A pair of tiles takes 1.13 us from L2 and
+// 1.25 from DRAM; the loader's copies are issued in 0.75 (eight of 100 ns each, for pages of 64), the issuing warp
+// works for 0.75, a stream's softmax for 1.5 every second pair.  With 32 rows (two columns' groups) or 64 a
+// thread's sums went to local memory: 440 and 496 us.  More converting warps take its registers: 16 373 us, three
+// teams of four 341.  Codes brought to L2 two tiles ahead cost the loader what they save.
 //
 // All products are fp16's.  A bf16 row of q is taken times a power of two that brings its largest element to
 // 2^14 (its eight bits fit; what lies below 2^-38 of the largest is lost, far below what the
@@ -17,6 +22,15 @@
 // Weights are fp16 as elsewhere: against a reference 2^7 below the maximum, lag 2^4.
 
 constexpr int kDown = 60;
+
+// m + log2(sum * 2^kDown), exponent and fraction apart: the logarithm of a sum near 2^-kDown would be rounded
+// as a number near kDown is.
+__device__ __forceinline__ float log2_up(float m, float sum)
+{
+    const uint32_t b = __float_as_uint(sum);
+    if ((b & 0x7F800000u) == 0x7F800000u) return sum;         // (no number)
+    return (m + (float)((int)(b >> 23) - 127 + kDown)) + log2f(__uint_as_float((b & 0x007FFFFFu) | 0x3F800000u));
+}
 
 // What the softmax threads, the converting warps and the Q loaders exchange.
 struct Few {
@@ -324,7 +338,7 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
                     part[128 * S::D + tid] = m;
                     part[128 * S::D + 128 + tid] = sum;
                 } else if (a.lse) {
-                    a.lse[few.out_row[tid]] = sum == 0.f ? -INFINITY : (m + log2f(sum) + (float)kDown) * kLn2;
+                    a.lse[few.out_row[tid]] = sum == 0.f ? -INFINITY : log2_up(m, sum) * kLn2;
                 }
             }
         }
