@@ -251,8 +251,15 @@ spec_status attention_call(const AttentionCall &call)
     a.group_magic = (uint32_t)((((1ull << a.group_shift) - a.group) << 32) / a.group + 1);
     a.block_table = b.block_table; a.cu_new = b.cu_new; a.seq_lens = b.seq_lens;
     a.lanes = (int32_t)b.lanes; a.max_pages = b.max_pages;
+    const int64_t hint = max_new < tokens ? max_new : tokens, chunk = hint > 0 ? hint : (tokens + b.lanes - 1) / b.lanes;
+    const bool two = chunk * a.group > 128;   // more rows than one tile: two tiles share every K/V tile
+    // Few rows (8 bits, heads of 128): items of 16 rows, if the step's can be counted.  A lane of more reads its cache again for
+    // every 16, so the lanes' most is to be known, or a token each.
+    const int64_t most = hint > 0 ? hint : tokens <= b.lanes ? 1 : tokens;
+    const int64_t few_items = tokens * heads_q / 16 + (tokens < b.lanes ? tokens : b.lanes) * c.heads;
+    const bool few = eight && c.head_dim == 128 && most * a.group <= 16 && few_items < 1ll << (63 - attn::kItemBit);
     // (of tiles of 64 keys, the smaller; 2^31 - 2^16 unless there are 2^15 items)
-    const int64_t tiles = (1ll << attn::kItemBit) / items - 2;
+    const int64_t tiles = (1ll << attn::kItemBit) / (few ? few_items : items) - 2;
     a.most_keys = (int32_t)(tiles < (0x7FFF0000 >> 6) ? tiles << 6 : 0x7FFF0000);
     a.c = call.scale * attn::kLog2e;
     a.window = window > INT32_MAX ? 0 : window;   // past every position: none (and positions less it stay within 64 bits)
@@ -261,9 +268,6 @@ spec_status attention_call(const AttentionCall &call)
     a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + SPEC_PAGED_WORKSPACE_ZEROED);
     a.masks = call.tree ? call.masks : nullptr;
     a.mask_words = call.mask_words;
-    const int64_t hint = max_new < tokens ? max_new : tokens, chunk = hint > 0 ? hint : (tokens + b.lanes - 1) / b.lanes;
-    const bool two = chunk * a.group > 128;   // more rows than one tile: two tiles share every K/V tile
-    const bool few = chunk * a.group <= 16;   // (8 bits, heads of 128)
     const attn::Pick pick = {c.head_dim, two, few, c.dtype == SPEC_F16, chunk, d->index, attention_grid(*d)};
     if (eight) return attn::launch8(a, pick, call.tree);
     const attn::Args &a16 = a;

@@ -91,6 +91,29 @@ def test_attention8_refusals(sd):
     assert call(tokens=0, ws=None, out=None, q=None) == sd.SPEC_OK
 
 
+def test_few_rows_items_are_counted():
+    """Items of 16 rows: where the host lets a step take them, they and their tiles fit the words they are counted in,
+    lane by lane; the lanes need not have what the hint says."""
+    import random
+    rng = random.Random(7)
+    for _ in range(2_000):
+        lanes, hk, g = rng.randint(1, 60), rng.randint(1, 16), rng.randint(1, 16)
+        new = [rng.choice([0, 1, 1, rng.randint(0, 900)]) for _ in range(lanes)]
+        tokens = sum(new)
+        bound = tokens * hk * g // 16 + min(tokens, lanes) * hk
+        assert sum(-(-n * g // 16) for n in new) * hk <= bound
+        if bound:
+            most = ((1 << 40) // bound - 2) << 6              # keys of a lane at most
+            assert bound * (-(-most // 64) + 1) < 1 << 40
+
+
+def test_large_steps_with_a_small_hint_are_taken(sd):
+    """2^26 items of 16 rows would not fit; items of 128 rows do."""
+    c = _cache8(sd, heads=8, head_dim=128, k_strides=(1 << 20, 1024, 128), v_strides=(1 << 20, 1024, 128))
+    st = sd.lib.spec_paged_attention8(P, 1 << 26, 8, 1024, 128, c, _batch(sd), 0.1, 0, 1, 1 << 44, None, None, 0)
+    _refused(sd, st, "null pointer")
+
+
 @pytest.mark.parametrize("eight", [False, True])
 def test_tree_attention_refusals(sd, eight):
     f, cache = (sd.lib.spec_tree_attention8, _cache8(sd)) if eight else (sd.lib.spec_tree_attention, _cache(sd))
