@@ -119,7 +119,7 @@ struct Shape {
     static constexpr int kExtra = QT == 2 ? 4 : 3;             // tiles that an item's other work costs
     static constexpr int kLeast = QT == 1 ? 2 : 1;             // units of a run that an item is cut into, at least
     // TMEM columns: S buffers, then O
-    static constexpr int kSBuffers = kFew ? 4 : 2, kS = kFew ? kRows : BK, kO = kSBuffers * kS;
+    static constexpr int kS = kFew ? kRows : BK, kO = 2 * kS;
     static constexpr int kPartFloats = (kFew ? 128 : kRows) * (D + 2);   // O, then m and sum
     static_assert(!kFew || (kQ8 && D == 128), "");
     static_assert(D == 64 || D == 128 || (D == 256 && QT == 1), "");
@@ -561,7 +561,7 @@ template <typename S>
 struct Bars {
     uint64_t full[S::kStages], empty[S::kStages];
     uint64_t raw_full[2 * S::kRaw + 1], raw_empty[S::kRaw + 1];   // of the codes' tiles (8 bits)
-    uint64_t s_full[S::kSBuffers], p_full[2], o_done[2];
+    uint64_t s_full[2], p_full[2], o_done[2];
     uint64_t q_full[2], q_empty[2], item_full[kItems], item_empty[kItems], drain;
     uint64_t part_full[2], part_known[2];   // the part in a slot is written; the others know
     uint64_t scaled[S::kFew ? kPairs : 1];  // kFew: the factors of a pair of tiles are there
@@ -727,7 +727,6 @@ __global__ void __launch_bounds__(Shape<D, QT_, Q8, TREE>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
-            if constexpr (S::kSBuffers > 2) mbar_init(&bar.s_full[2 + i], 1);
             mbar_init(&bar.p_full[i], S::kFew ? 4 : 8);
             mbar_init(&bar.o_done[i], 1);
             mbar_init(&bar.q_full[i], 2);
@@ -1028,12 +1027,12 @@ __global__ void __launch_bounds__(Shape<D, QT_, Q8, TREE>::kThreads, 1)
             const int U = QT == 2 ? 2 * tiles : tiles;
             const uint32_t qb = n % S::QB;
             auto qk = [&](int i) -> bool {
-                const int b = i & 1, sb = i & (S::kSBuffers - 1);
+                const int b = i & 1;
                 if ((QT == 1 || b == 0) && !wait(&bar.full[k_stage], k_phase)) return false;
                 fence_after();
                 if (leader) {
                     const uint32_t qa = q_desc + (qb * QT + (QT == 2 ? b : 0)) * (S::kQBytes >> 4), ka = k_desc + k_stage * (S::kStageBytes >> 4);
-                    const uint32_t d = tmem + sb * S::kS;
+                    const uint32_t d = tmem + b * S::kS;
                     if constexpr (S::kFew) {                 // S^T = K Q^T
                         mma_ss<false>(d, ka, qa, few_qk);
 #pragma unroll
@@ -1045,7 +1044,7 @@ __global__ void __launch_bounds__(Shape<D, QT_, Q8, TREE>::kThreads, 1)
                         for (int k = 1; k < D / 16; ++k)
                             mma_ss<true>(d, qa + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, ka + (k >> 2) * (S::BK * 128 >> 4) + (k & 3) * 2, kQk);
                     }
-                    commit(&bar.s_full[sb]);
+                    commit(&bar.s_full[b]);
                     if (QT == 1 || b == 1) commit(&bar.empty[k_stage]);
                     if (i == U - 1) commit(&bar.q_empty[qb]);
                 }
@@ -1056,11 +1055,8 @@ __global__ void __launch_bounds__(Shape<D, QT_, Q8, TREE>::kThreads, 1)
             ok = wait(&bar.q_full[qb], (n / S::QB) & 1);
             fence_after();
             ok = ok && qk(0);
-            // scores ahead of the weights' products: one tile, or (kFew) two, since a stream's softmax is what its next scores wait for
-            constexpr int kAhead = S::kSBuffers / 2;
-            if (kAhead > 1 && U > 1) ok = ok && qk(1);
             for (int i = 0; i < U && ok; ++i) {
-                if (i + kAhead < U) ok = qk(i + kAhead);
+                if (i + 1 < U) ok = qk(i + 1);
                 const int b = i & 1, ob = S::NS == 2 ? b : 0;
                 if (QT == 1 || b == 0) ok = ok && wait(&bar.full[v_stage], v_phase);
                 ok = ok && wait(&bar.p_full[b], units[b] & 1);

@@ -173,7 +173,7 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
     const int st = warp >> 2, quad = warp & 3, key = quad * 32 + lane, tid = warp * 32 + lane, stream_barrier = 1 + st;
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     uint8_t *const weights = p_smem + key * 128;              // 16 columns of either stream
-    uint32_t tile_n = 0, s_uses = 0, pv_n = 0;                // tiles so far, parities of S buffers' uses, products of this stream
+    uint32_t tile_n = 0, s_n = 0, pv_n = 0;                   // tiles so far, units and products of this stream
     for (uint32_t n = 0;; ++n) {
         const bool ok = wait(&bar.item_full[n % kItems], (n / kItems) & 1);
         // all softmax warps go on or none does: the barriers below count on it
@@ -211,9 +211,7 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
             wait(&bar.scaled[pair % kPairs], (pair / kPairs) & 1);
             const float *f = few.factors[pair % kPairs][0] + key;
             const float ks = f[0], v = f[128], over = f[256];
-            const int sb = t & (S::kSBuffers - 1);
-            wait(&bar.s_full[sb], s_uses >> sb & 1);
-            s_uses ^= 1u << sb;
+            wait(&bar.s_full[st], s_n++ & 1);
             // the weights of the last tile are read, and its product may be multiplied
             if (i > 0) wait(&bar.o_done[st], (pv_n - 1) & 1);
             fence_after();
@@ -221,7 +219,7 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
             {
                 uint32_t x[16];
                 float u[16];
-                tmem_ld16(x, tmem + lane_base + sb * S::kS);
+                tmem_ld16(x, tmem + lane_base + st * S::kRows);
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     const float4 c = *reinterpret_cast<const float4 *>(&few.row_factor[n % kItems][e]);
