@@ -345,6 +345,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t d;
@@ -398,13 +404,6 @@ __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// the same down to subnormal results
-__device__ __forceinline__ float exp2_deep(float x)
-{
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 template <bool F16>
@@ -1455,11 +1454,18 @@ __global__ void __launch_bounds__(Shape<D, QT_, Q8, TREE>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] = 0.f;
             auto scales = [&](float mp, float lp, float &fo, float &fp) {
-                const float Mn = fmaxf(M, mp), ref = Mn == -INFINITY ? 0.f : Mn;
-                fo = S::kFew ? exp2_deep(M - ref) : exp2_fast(M - ref);
-                fp = S::kFew ? exp2_deep(mp - ref) : exp2_fast(mp - ref);
+                const float Mo = M, Mn = fmaxf(M, mp), ref = Mn == -INFINITY ? 0.f : Mn;
                 M = Mn;
-                L = L * fo + lp * fp;
+                if constexpr (S::kFew) {
+                    const float2 a = exp2_pair(Mo - ref), b = exp2_pair(mp - ref);
+                    fo = a.x * a.y;
+                    fp = b.x * b.y;
+                    L = L * a.x * a.y + lp * b.x * b.y;
+                } else {
+                    fo = exp2_fast(Mo - ref);
+                    fp = exp2_fast(mp - ref);
+                    L = L * fo + lp * fp;
+                }
             };
 #pragma unroll 2
             for (int p = p0; p < n; p += step) {
@@ -1488,7 +1494,7 @@ __global__ void __launch_bounds__(Shape<D, QT_, Q8, TREE>::kThreads, 1)
             if (n == 0 || p0 != 0) continue;
             const uint32_t gr = (uint32_t)j.rt * S::kRows + r, tok = div_group(a, gr);
             const int64_t orow = ((int64_t)j.first + tok) * a.heads_q + (int64_t)j.head * a.group + (gr - tok * a.group);
-            const float iv = L == 0.f ? 0.f : (S::kFew ? 0x1p-60f : 1.f) / L;
+            const float iv = L == 0.f ? 0.f : (S::kFew ? kUp : 1.f) / L;
             uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + g * 16);
 #pragma unroll
             for (int i = 0; i < 2; ++i)

@@ -7,7 +7,7 @@
 // transposed, S^T = K Q^T and O^T += V^T P^T: a softmax thread has one key, so that the key's scale is one
 // factor of all its scores, and its value's scale one of all its weights.  Codes then go to fp16 as they
 // are, one instruction a pair, and a thread's 16 columns (rows of q) stay in registers for both passes over
-// them.  281 us, 3.8 TB/s.  What bounds it: chains, none of them full.  A pair of tiles takes 1.13 us from L2 and
+// them.  273 us, 3.9 TB/s.  What bounds it: chains, none of them full.  A pair of tiles takes 1.13 us from L2 and
 // 1.25 from DRAM; the loader's copies are issued in 0.75 (eight of 100 ns each, for pages of 64), the issuing warp
 // works for 0.75, a stream's softmax for 1.5 every second pair.  With 32 rows (two columns' groups) or 64 a
 // thread's sums went to local memory: 440 and 496 us.  More converting warps take its registers: 16 373 us, three
@@ -17,11 +17,21 @@
 // 2^14 (its eight bits fit; what lies below 2^-38 of the largest is lost, far below what the
 // sums lose).  With t the score in log2 units and v that of the value's scale, the running maximum is of t + v, a weight
 // 2^(t + v - m) is what multiplies the code, and the sum is of weight * 2^-v, that is of
-// 2^(t - m), unrounded.  v runs from -120 (a vector of zeros, for one) to 7, so sums are kept times 2^-kDown, and
-// where references meet 2^x is taken down to subnormals: keys of equal scores may lie 2^127 apart.
+// 2^(t - m), unrounded.  v runs from -120 (a vector of zeros, for one) to 7, so keys of equal scores lie up to 2^127
+// apart: a weight below 2^-126 would be 0 and its key gone from the sum, so the sum is of weights 2^kLift above (what is
+// lost then has t - m below -63, the largest weight's is 0 or more); it is kept times 2^-kDown; and where references move or
+// meet it is multiplied by 2^x in two factors, as x may be below -126.
 // Weights are fp16 as elsewhere: against a reference 2^7 below the maximum, lag 2^4.
 
-constexpr int kDown = 60;
+constexpr int kDown = 48, kLift = 64;
+constexpr float kUp = 0x1p-48f, kUnlift = 0x1p-64f;   // what takes out kDown, kLift
+
+// 2^x as a product of two factors, neither subnormal for x from -190 on (the first is all of it from -64 on).
+__device__ __forceinline__ float2 exp2_pair(float x)
+{
+    const float a = fmaxf(x, -64.f);
+    return make_float2(exp2_fast(a), exp2_fast(x - a));
+}
 
 // m + log2(sum * 2^kDown), exponent and fraction apart: the logarithm of a sum near 2^-kDown would be rounded
 // as a number near kDown is.
@@ -34,9 +44,10 @@ __device__ __forceinline__ float log2_up(float m, float sum)
 
 // What the softmax threads, the converting warps and the Q loaders exchange.
 struct Few {
-    float factors[kPairs][3][128];      // of a pair of tiles' keys: of the score; log2 of the value's, and 1 over it (times 2^-kDown)
+    float factors[kPairs][2][128];      // of a pair of tiles' keys: of the score; what the sums have of the value's
     float row_factor[kItems][16];       // log2 units of a score of the row's, but for its key's factor
-    float ref[2][16], moved[2][16];     // a stream's references, and what its sums are to be multiplied by
+    float ref[2][16];                   // a stream's references
+    float2 moved[2][16];                // what its sums are to be multiplied by: the root, and the whole (O^T)
     float top[2][4][16];                // maxima of 32 keys
     float sum[2][4][16];                // sums over 32 keys
     float w0[16], w1[16], inv[16];      // weights of the streams' O^T, and 1 over the sum
@@ -53,20 +64,20 @@ __device__ __forceinline__ uint2 bare4(uint32_t w)
     return r;
 }
 
-// The factor of a key's scores, and of a value's scale its log2 and what takes it out of a weight.
+// The factor of a key's scores.
 template <bool F16>
 __device__ __forceinline__ float key_factor(uint32_t byte)
 {
     constexpr uint32_t kLeast = F16 ? 113u : 7u;
     return byte > 134u ? __uint_as_float(0x7FC00000u) : __uint_as_float((byte < kLeast ? kLeast : byte) << 23);
 }
+// Of a value's scale what takes it out of a lifted weight, times 2^-kDown, and its log2: the upper halves of two floats.
 template <bool F16>
-__device__ __forceinline__ void value_factors(uint32_t byte, float &log2v, float &inverse)
+__device__ __forceinline__ float value_factors(uint32_t byte)
 {
     constexpr uint32_t kLeast = F16 ? 113u : 7u;
     const uint32_t b = byte < kLeast ? kLeast : byte > 134u ? 127u : byte;   // (no number: its codes say so)
-    log2v = (float)((int)b - 127);
-    inverse = __uint_as_float((254u - kDown - b) << 23);
+    return __uint_as_float((254u - kDown - kLift - b) << 23 | __float_as_uint((float)((int)b - 127)) >> 16);
 }
 
 // The converting warps: a team of four the K tiles, another the V tiles, a thread 16 codes of a row at a time (as
@@ -104,8 +115,7 @@ __device__ __forceinline__ void convert_bare(Bars<S> &bar, const Item *items, co
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
             // the factors are there before the tile is: the softmax need not wait for a stage
-            if (team) value_factors<F16>(byte, few.factors[pair][1][id], few.factors[pair][2][id]);
-            else few.factors[pair][0][id] = key_factor<F16>(byte);
+            few.factors[pair][team][id] = team ? value_factors<F16>(byte) : key_factor<F16>(byte);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.scaled[pair]);
             pair = pair + 1 < kPairs ? pair + 1 : 0;
@@ -173,7 +183,7 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
     const int st = warp >> 2, quad = warp & 3, key = quad * 32 + lane, tid = warp * 32 + lane, stream_barrier = 1 + st;
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     uint8_t *const weights = p_smem + key * 128;              // 16 columns of either stream
-    uint32_t tile_n = 0, s_n = 0, pv_n = 0;                   // tiles so far, units and products of this stream
+    uint32_t tile_n = 0, unit = 0;                            // tiles so far, those of this stream
     for (uint32_t n = 0;; ++n) {
         const bool ok = wait(&bar.item_full[n % kItems], (n / kItems) & 1);
         // all softmax warps go on or none does: the barriers below count on it
@@ -181,7 +191,7 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
         const Item &it = items[n % kItems];
         const int tiles = it.tiles;
         if (tiles == 0) return false;
-        const int lo = it.lo, hi = it.hi, tile0 = it.tile, ctx = it.seq - it.n;
+        const int tile0 = it.tile, ctx = it.seq - it.n;
         const int64_t row0 = (int64_t)it.rt * S::kRows, left = (int64_t)it.n * a.group - row0;
         const int rows = left < S::kRows ? (int)left : S::kRows;
         if (tid < S::kRows) {
@@ -198,22 +208,25 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
         named_barrier(kAllSoftmax, kAll);
         // no tile within these has a key that some row does not see
         const int tok0 = (int)div_group(a, (uint32_t)row0), tok1 = (int)div_group(a, (uint32_t)row0 + rows - 1);
-        const int64_t last_lo = a.window > 0 ? (int64_t)ctx + tok1 - a.window + 1 : 0;
+        const int64_t last = a.window > 0 ? (int64_t)ctx + tok1 - a.window + 1 : 0;
+        const int last_lo = last > 0 ? (int)last : 0;
         const int first_hi = S::kTree ? ctx : ctx + tok0 + 1;
 
-        float l[16];
+        uint64_t l[8];                                         // two columns' sums each
 #pragma unroll
-        for (int e = 0; e < 16; ++e) l[e] = 0.f;
+        for (int e = 0; e < 8; ++e) l[e] = 0ull;
         const int U = (tiles - st + 1) >> 1;
         for (int i = 0; i < U; ++i) {
             const int t = 2 * i + st, key0 = (tile0 + t) * S::BK, at = key0 + key;
             const uint32_t pair = tile_n + t;
             wait(&bar.scaled[pair % kPairs], (pair / kPairs) & 1);
             const float *f = few.factors[pair % kPairs][0] + key;
-            const float ks = f[0], v = f[128], over = f[256];
-            wait(&bar.s_full[st], s_n++ & 1);
+            const float ks = f[0];
+            const uint32_t vf = __float_as_uint(f[128]);
+            const float v = __uint_as_float(vf << 16), over = __uint_as_float(vf & 0xFFFF0000u);
+            wait(&bar.s_full[st], unit & 1);
             // the weights of the last tile are read, and its product may be multiplied
-            if (i > 0) wait(&bar.o_done[st], (pv_n - 1) & 1);
+            if (i > 0) wait(&bar.o_done[st], (unit - 1) & 1);
             fence_after();
             const bool edge = key0 < last_lo || key0 + S::BK > first_hi;
             {
@@ -259,18 +272,25 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
                         const float top = fmaxf(fmaxf(few.top[st][0][lane], few.top[st][1][lane]), fmaxf(few.top[st][2][lane], few.top[st][3][lane]));
                         const float m = few.ref[st][lane], to = top - kRaise<true>;
                         const bool move = top > m + kPast;     // (m = -inf: any key's)
-                        few.moved[st][lane] = move ? exp2_deep(m - to) : 1.f;
+                        const float f = move ? exp2_fast(0.5f * (m - to)) : 1.f;
+                        few.moved[st][lane] = make_float2(f, f * f);
                         if (move) few.ref[st][lane] = to;
                     }
                     named_barrier(stream_barrier, 128);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) l[e] *= few.moved[st][e];
+                    for (int e = 0; e < 16; e += 2) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&few.moved[st][e]);
+                        const uint64_t f2 = two(f.x, f.z);
+                        l[e / 2] = mul2(mul2(l[e / 2], f2), f2);
+                    }
                     if (i > 0) {
                         const uint32_t oa = tmem + lane_base + S::kO + st * S::kRows;
                         uint32_t o[16];
                         tmem_ld16(o, oa);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * few.moved[st][e]);
+                        for (int e = 0; e < 16; ++e) {
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * few.moved[st][e].y);
+                        }
                         tmem_st16(oa, o);
                     }
                 }
@@ -278,19 +298,21 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
                     const float2 m = *reinterpret_cast<const float2 *>(&few.ref[st][e]);
-                    const float p0 = exp2_fast(u[e] - (m.x == -INFINITY ? 0.f : m.x)), p1 = exp2_fast(u[e + 1] - (m.y == -INFINITY ? 0.f : m.y));
-                    l[e] = fmaf(p0, over, l[e]);
-                    l[e + 1] = fmaf(p1, over, l[e + 1]);
+                    float p0 = exp2_fast(u[e] - (m.x == -INFINITY ? 0.f : m.x) + (float)kLift),
+                          p1 = exp2_fast(u[e + 1] - (m.y == -INFINITY ? 0.f : m.y) + (float)kLift);
+                    const uint64_t p = two(p0, p1);
+                    l[e / 2] = fma2(p, two(over, over), l[e / 2]);
+                    halves(mul2(p, two(kUnlift, kUnlift)), p0, p1);
                     pk[e / 2] = pack2<true>(p0, p1);
                 }
                 *reinterpret_cast<uint4 *>(weights + ((2 * st ^ (key & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                 *reinterpret_cast<uint4 *>(weights + ((2 * st + 1 ^ (key & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
             }
             // V rows that no row of the item may see hold anything, NaN included: 0 * NaN must not reach O
-            if (key0 < lo || key0 + S::BK > hi) {
+            if (edge && (key0 < it.lo || key0 + S::BK > it.hi)) {
                 const uint32_t idx = 2 * pair + 1, vs = idx % S::kStages;
                 wait(&bar.full[vs], (idx / S::kStages) & 1);
-                if (at < lo || at >= hi) {
+                if (at < it.lo || at >= it.hi) {
                     uint8_t *row = kv_smem + vs * S::kStageBytes + key * 128;
 #pragma unroll
                     for (int k = 0; k < 2 * 8; ++k) *reinterpret_cast<uint4 *>(row + (k >> 3) * (S::BK * 128) + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -301,16 +323,19 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.p_full[st]);
-            ++pv_n;
+            ++unit;
         }
         tile_n += tiles;
-        if (U > 0) wait(&bar.o_done[st], (pv_n - 1) & 1);
+        if (U > 0) wait(&bar.o_done[st], (unit - 1) & 1);
 
         // the columns' sums over the keys and the streams
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const float x = warp_sum_f(l[e]);
-            if (lane == 0) few.sum[st][quad][e] = x;
+        for (int e = 0; e < 16; e += 2) {
+            float a0, a1;
+            halves(l[e / 2], a0, a1);
+            a0 = warp_sum_f(a0);
+            a1 = warp_sum_f(a1);
+            if (lane == 0) *reinterpret_cast<float2 *>(&few.sum[st][quad][e]) = make_float2(a0, a1);
         }
         fence_before();
         named_barrier(kAllSoftmax, kAll);
@@ -320,17 +345,18 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
         float *part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * S::kPartFloats;
         if (tid < S::kRows) {
             const float m0 = few.ref[0][tid], m1 = few.ref[1][tid], m = fmaxf(m0, m1);
-            const float f0 = m0 == -INFINITY ? 0.f : exp2_deep(m0 - m), f1 = m1 == -INFINITY ? 0.f : exp2_deep(m1 - m);
+            const float2 f0 = m0 == -INFINITY ? make_float2(0.f, 0.f) : exp2_pair(m0 - m),
+                         f1 = m1 == -INFINITY ? make_float2(0.f, 0.f) : exp2_pair(m1 - m);
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 s0 += few.sum[0][q][tid];
                 s1 += few.sum[1][q][tid];
             }
-            const float sum = s0 * f0 + s1 * f1;
-            few.w0[tid] = f0;
-            few.w1[tid] = tiles > 1 ? f1 : 0.f;
-            few.inv[tid] = sum == 0.f ? 0.f : split ? 1.f : 0x1p-60f / sum;   // (NaN scores: NaN)
+            const float sum = s0 * f0.x * f0.y + s1 * f1.x * f1.y;
+            few.w0[tid] = f0.x * f0.y;
+            few.w1[tid] = tiles > 1 ? f1.x * f1.y : 0.f;
+            few.inv[tid] = sum == 0.f ? 0.f : split ? 1.f : kUp / sum;   // (NaN scores: NaN)
             if (tid < rows) {
                 if (split) {
                     part[128 * S::D + tid] = m;
