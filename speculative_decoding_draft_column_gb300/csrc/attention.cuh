@@ -1494,7 +1494,10 @@ __global__ void __launch_bounds__(Shape<D, QT_, Q8, TREE>::kThreads, 1)
             if (n == 0 || p0 != 0) continue;
             const uint32_t gr = (uint32_t)j.rt * S::kRows + r, tok = div_group(a, gr);
             const int64_t orow = ((int64_t)j.first + tok) * a.heads_q + (int64_t)j.head * a.group + (gr - tok * a.group);
-            const float iv = L == 0.f ? 0.f : (S::kFew ? kUp : 1.f) / L;
+            const float iv = L == 0.f ? 0.f : 1.f / L;
+            if constexpr (S::kFew)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] *= kUp;
             uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + g * 16);
 #pragma unroll
             for (int i = 0; i < 2; ++i)

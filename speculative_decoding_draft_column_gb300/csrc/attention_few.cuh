@@ -20,7 +20,8 @@
 // 2^(t - m), unrounded.  v runs from -120 (a vector of zeros, for one) to 7, so keys of equal scores lie up to 2^127
 // apart: a weight below 2^-126 would be 0 and its key gone from the sum, so the sum is of weights 2^kLift above (what is
 // lost then has t - m below -63, the largest weight's is 0 or more); it is kept times 2^-kDown; and where references move or
-// meet it is multiplied by 2^x in two factors, as x may be below -126.
+// meet it is multiplied by 2^x in two factors, as x may be below -126.  (2^-kDown over a sum may be, too: O^T is
+// multiplied by each.)
 // Weights are fp16 as elsewhere: against a reference 2^7 below the maximum, lag 2^4.
 
 constexpr int kDown = 48, kLift = 64;
@@ -356,7 +357,7 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
             const float sum = s0 * f0.x * f0.y + s1 * f1.x * f1.y;
             few.w0[tid] = f0.x * f0.y;
             few.w1[tid] = tiles > 1 ? f1.x * f1.y : 0.f;
-            few.inv[tid] = sum == 0.f ? 0.f : split ? 1.f : kUp / sum;   // (NaN scores: NaN)
+            few.inv[tid] = sum == 0.f ? 0.f : split ? 1.f : 1.f / sum;   // (NaN scores: NaN)
             if (tid < rows) {
                 if (split) {
                     part[128 * S::D + tid] = m;
@@ -380,7 +381,7 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
                 const float v = (f0 > 0.f ? __uint_as_float(o0[e]) * f0 : 0.f) + (f1 > 0.f ? __uint_as_float(o1[e]) * f1 : 0.f);
                 if (row >= rows) continue;
                 if (split) part[((key >> 2) * 128 + row) * 4 + (key & 3)] = inv == 0.f ? 0.f : v;
-                else a.out[few.out_row[row] * S::D + key] = (uint16_t)pack2<F16>(inv == 0.f ? 0.f : v * inv, 0.f);
+                else a.out[few.out_row[row] * S::D + key] = (uint16_t)pack2<F16>(inv == 0.f ? 0.f : v * kUp * inv, 0.f);
             }
         }
         fence_before();

@@ -97,3 +97,20 @@ def test_values_of_both_kinds(sd, w, below, order):
             got = out[0, row].double()
             assert ((got - want).abs() <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -13) * want).all(), (n, row, got[0].item(), want)
             assert abs(float(lse[0, row]) - math.log(z)) <= 2.0 ** -14 + 2.0 ** -20 * math.log(z)
+
+
+@pytest.mark.parametrize("n", [1, 192, 100_032, 250_048])
+def test_values_all_of_the_least_scale(sd, n):
+    """The output is as small as the values, and as exact as any."""
+    import torch
+    n_pages = -(-n // 64) * 64
+    large = torch.zeros(n_pages, dtype=torch.bool, device="cuda")
+    cache, _ = _cache_of(sd, "bf16", n_pages, 64, large, 0, 3, 0x7E)
+    b = _batch(sd, [list(range(n_pages // 64))], [0, 1], [n], 64)
+    q = torch.zeros((1, 2, 128), dtype=torch.bfloat16, device="cuda")
+    q[0, 1, 0] = 1.0
+    out, lse = _attend(sd, q, cache, b, None, math.log(2.0), 0, 1, True)
+    # all weights alike: a 16-bit rounding of the output, one of a weight, and sums as above
+    assert ((out.double() - 448 * 2.0 ** -120).abs() <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -13) * 448 * 2.0 ** -120).all(), out[0, :, 0]
+    for row, t in enumerate((0.0, -3 * float(np.float32(math.log(2.0))))):
+        assert abs(float(lse[0, row]) - t - math.log(n)) <= 2.0 ** -14 + 2.0 ** -20 * math.log(max(n, 2))
