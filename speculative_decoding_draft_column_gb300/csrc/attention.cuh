@@ -118,6 +118,7 @@ struct Shape {
     static constexpr int kRows = kFew ? 16 : QT * 128;
     static constexpr int kExtra = QT == 2 ? 4 : 3;             // tiles that an item's other work costs
     static constexpr int kLeast = QT == 1 ? 2 : 1;             // units of a run that an item is cut into, at least
+    static constexpr int kAhead = 1;                           // units whose scores are issued before the weights' product of one is waited for
     // TMEM columns: S buffers, then O
     static constexpr int kS = kFew ? kRows : BK, kO = 2 * kS;
     static constexpr int kPartFloats = (kFew ? 128 : kRows) * (D + 2);   // O, then m and sum
@@ -1053,9 +1054,9 @@ __global__ void __launch_bounds__(Shape<D, QT_, Q8, TREE>::kThreads, 1)
             };
             ok = wait(&bar.q_full[qb], (n / S::QB) & 1);
             fence_after();
-            ok = ok && qk(0);
+            for (int i = 0; i < S::kAhead && i < U; ++i) ok = ok && qk(i);
             for (int i = 0; i < U && ok; ++i) {
-                if (i + 1 < U) ok = qk(i + 1);
+                if (i + S::kAhead < U) ok = qk(i + S::kAhead);
                 const int b = i & 1, ob = S::NS == 2 ? b : 0;
                 if (QT == 1 || b == 0) ok = ok && wait(&bar.full[v_stage], v_phase);
                 ok = ok && wait(&bar.p_full[b], units[b] & 1);

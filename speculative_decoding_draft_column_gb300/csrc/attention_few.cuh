@@ -90,9 +90,11 @@ __device__ __forceinline__ void convert_bare(Bars<S> &bar, const Item *items, co
 {
     constexpr int kPieces = S::D / 16, kStep = 128 / kPieces, kPasses = S::BK / kStep;
     static_assert(kStep % 8 == 0 && S::BK == 128 && S::kConverters == 8, "");
-    // The K tile kPairs on is read once the one before it is converted, that is, once the one kStages / 2 before that is
-    // read, by a product that is issued after that of the weights two tiles earlier.
-    static_assert(S::kStages % 2 == 0 && kPairs >= S::kStages / 2 + 3, "factors that are still read");
+    // A key's factors are written over those of the key kPairs tiles before, which the softmax of that tile must have read
+    // (its weights were waited for).  A team writes those of tile n once it has converted tile n - 1, that is, once the
+    // product of tile n - 1 - kStages / 2 has read that tile's stage: the weights' product for V; for K the scores',
+    // which are issued once the weights of the tile kAhead + 1 before theirs were waited for.
+    static_assert(S::kStages % 2 == 0 && kPairs >= S::kStages / 2 + 2 + S::kAhead, "factors that are still read");
     const int team = warp >> 2, id = (warp & 3) * 32 + lane, p = id % kPieces, r0 = id / kPieces;
     const int block = p >> 2, piece = (p & 3) * 2, flip = block & 1;
     const uint32_t x0 = ((piece + flip) ^ (r0 & 7)) << 4, x1 = x0 ^ 16;
