@@ -18,13 +18,14 @@
 // sums lose).  With t the score in log2 units and v that of the value's scale, the running maximum is of t + v, a weight
 // 2^(t + v - m) is what multiplies the code, and the sum is of weight * 2^-v, that is of
 // 2^(t - m), unrounded.  v runs from -120 (a vector of zeros, for one) to 7, so keys of equal scores lie up to 2^127
-// apart: a weight below 2^-126 would be 0 and its key gone from the sum, so the sum is of weights 2^kLift above (what is
-// lost then has t - m below -63, the largest weight's is 0 or more); it is kept times 2^-kDown; and where references move or
+// apart: a weight below 2^-126 would be 0 and its key gone from the sum.  So keys with v below kTiny have weights 2^kLift
+// above in the sum (what is lost then has t - m below -63, and of other keys below -86; the largest weight's is 0 or
+// more; lifted, an exponent is rounded as a number near 64 is).  The sum is kept times 2^-kDown, and where references move or
 // meet it is multiplied by 2^x in two factors, as x may be below -126.  (2^-kDown over a sum may be, too: O^T is
 // multiplied by each.)
 // Weights are fp16 as elsewhere: against a reference 2^7 below the maximum, lag 2^4.
 
-constexpr int kDown = 48, kLift = 64;
+constexpr int kDown = 48, kLift = 64, kTiny = -40;
 constexpr float kUp = 0x1p-48f, kUnlift = 0x1p-64f;   // what takes out kDown, kLift
 
 // 2^x as a product of two factors, neither subnormal for x from -190 on (the first is all of it from -64 on).
@@ -72,13 +73,13 @@ __device__ __forceinline__ float key_factor(uint32_t byte)
     constexpr uint32_t kLeast = F16 ? 113u : 7u;
     return byte > 134u ? __uint_as_float(0x7FC00000u) : __uint_as_float((byte < kLeast ? kLeast : byte) << 23);
 }
-// Of a value's scale what takes it out of a lifted weight, times 2^-kDown, and its log2: the upper halves of two floats.
+// Of a value's scale what takes it (and the lift) out of a weight, times 2^-kDown, and its log2: the upper halves of two floats.
 template <bool F16>
 __device__ __forceinline__ float value_factors(uint32_t byte)
 {
     constexpr uint32_t kLeast = F16 ? 113u : 7u;
     const uint32_t b = byte < kLeast ? kLeast : byte > 134u ? 127u : byte;   // (no number: its codes say so)
-    return __uint_as_float((254u - kDown - kLift - b) << 23 | __float_as_uint((float)((int)b - 127)) >> 16);
+    return __uint_as_float((254u - kDown - b - (b < 127u + kTiny ? kLift : 0)) << 23 | __float_as_uint((float)((int)b - 127)) >> 16);
 }
 
 // The converting warps: a team of four the K tiles, another the V tiles, a thread 16 codes of a row at a time (as
@@ -227,6 +228,8 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
             const float ks = f[0];
             const uint32_t vf = __float_as_uint(f[128]);
             const float v = __uint_as_float(vf << 16), over = __uint_as_float(vf & 0xFFFF0000u);
+            const bool tiny = !F16 && v < kTiny;                      // (fp16's are -14 or more)
+            const float lift = tiny ? (float)kLift : 0.f, unlift = tiny ? kUnlift : 1.f;
             wait(&bar.s_full[st], unit & 1);
             // the weights of the last tile are read, and its product may be multiplied
             if (i > 0) wait(&bar.o_done[st], (unit - 1) & 1);
@@ -301,11 +304,11 @@ __device__ __forceinline__ bool few_rows(const Args &a, Bars<S> &bar, const Item
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
                     const float2 m = *reinterpret_cast<const float2 *>(&few.ref[st][e]);
-                    float p0 = exp2_fast(u[e] - (m.x == -INFINITY ? 0.f : m.x) + (float)kLift),
-                          p1 = exp2_fast(u[e + 1] - (m.y == -INFINITY ? 0.f : m.y) + (float)kLift);
+                    float p0 = exp2_fast(u[e] - (m.x == -INFINITY ? 0.f : m.x) + lift),
+                          p1 = exp2_fast(u[e + 1] - (m.y == -INFINITY ? 0.f : m.y) + lift);
                     const uint64_t p = two(p0, p1);
                     l[e / 2] = fma2(p, two(over, over), l[e / 2]);
-                    halves(mul2(p, two(kUnlift, kUnlift)), p0, p1);
+                    halves(mul2(p, two(unlift, unlift)), p0, p1);
                     pk[e / 2] = pack2<true>(p0, p1);
                 }
                 *reinterpret_cast<uint4 *>(weights + ((2 * st ^ (key & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
