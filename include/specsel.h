@@ -431,8 +431,9 @@ spec_status spec_paged_store8(const void *k, const void *v, int64_t tokens, int6
 /* spec_paged_attention over an 8-bit cache: the same arguments, workspace and
  * limits, pages of 16 tokens or more, q and out of type cache->dtype.  The result is that of
  * spec_paged_attention over the values that the codes and scales stand for (which
- * dtype holds exactly); scales above 134 stand for a vector that is no number.  What the cache holds past a lane's last position or before its
- * window, scales included, does not matter. */
+ * dtype holds exactly).  Scales above 134 stand for a vector that is no number, whatever its codes: a row that sees such a key or
+ * value gets NaN (for a value its lse may be NaN, too, and other rows may get NaN).  What the cache holds past a lane's last position or
+ * before its window, scales included, does not matter. */
 spec_status spec_paged_attention8(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
                                   int64_t q_head_stride, const spec_paged_cache8 *cache, const spec_paged_batch *batch,
                                   float scale, int64_t window, int64_t max_new, void *out, float *lse,

@@ -74,12 +74,15 @@ __device__ __forceinline__ float key_factor(uint32_t byte)
     return byte > 134u ? __uint_as_float(0x7FC00000u) : __uint_as_float((byte < kLeast ? kLeast : byte) << 23);
 }
 // Of a value's scale what takes it (and the lift) out of a weight, times 2^-kDown, and its log2: the upper halves of two floats.
+// The log2 of a scale of no number is none: the scores of the rows that see the key are then no numbers (the others' are
+// masked), and with them their outputs.
 template <bool F16>
 __device__ __forceinline__ float value_factors(uint32_t byte)
 {
     constexpr uint32_t kLeast = F16 ? 113u : 7u;
-    const uint32_t b = byte < kLeast ? kLeast : byte > 134u ? 127u : byte;   // (no number: its codes say so)
-    return __uint_as_float((254u - kDown - b - (b < 127u + kTiny ? kLift : 0)) << 23 | __float_as_uint((float)((int)b - 127)) >> 16);
+    const uint32_t b = byte < kLeast ? kLeast : byte > 134u ? 127u : byte;
+    const float log2v = byte > 134u ? __uint_as_float(0x7FC00000u) : (float)((int)b - 127);
+    return __uint_as_float((254u - kDown - b - ((int)b < 127 + kTiny ? kLift : 0)) << 23 | __float_as_uint(log2v) >> 16);
 }
 
 // The converting warps: a team of four the K tiles, another the V tiles, a thread 16 codes of a row at a time (as
