@@ -17,7 +17,7 @@
 // 2^14 (its eight bits fit; what lies below 2^-38 of the largest is lost, far below what the
 // sums lose).  With t the score in log2 units and v that of the value's scale, the running maximum is of t + v, a weight
 // 2^(t + v - m) is what multiplies the code, and the sum is of weight * 2^-v, that is of
-// 2^(t - m), unrounded.  v runs from -120 (a vector of zeros, for one) to 7, so keys of equal scores lie up to 2^127
+// 2^(t - m), unrounded.  v runs from -127 (the store gives -120 to a vector of zeros) to 7, so keys of equal scores lie up to 2^134
 // apart: a weight below 2^-126 would be 0 and its key gone from the sum.  So keys with v below kTiny have weights 2^kLift
 // above in the sum (what is lost then has t - m below -63, and of other keys below -86; the largest weight's is 0 or
 // more; lifted, an exponent is rounded as a number near 64 is).  The sum is kept times 2^-kDown, and where references move or
@@ -70,8 +70,8 @@ __device__ __forceinline__ uint2 bare4(uint32_t w)
 template <bool F16>
 __device__ __forceinline__ float key_factor(uint32_t byte)
 {
-    constexpr uint32_t kLeast = F16 ? 113u : 7u;
-    return byte > 134u ? __uint_as_float(0x7FC00000u) : __uint_as_float((byte < kLeast ? kLeast : byte) << 23);
+    const uint32_t bits = F16 ? (byte < 113u ? 113u : byte) << 23 : byte > 0u ? byte << 23 : 0x00400000u;   // (2^-127 is subnormal)
+    return byte > 134u ? __uint_as_float(0x7FC00000u) : __uint_as_float(bits);
 }
 // Of a value's scale what takes it (and the lift) out of a weight, times 2^-kDown, and its log2: the upper halves of two floats.
 // The log2 of a scale of no number is none: the scores of the rows that see the key are then no numbers (the others' are
@@ -79,8 +79,7 @@ __device__ __forceinline__ float key_factor(uint32_t byte)
 template <bool F16>
 __device__ __forceinline__ float value_factors(uint32_t byte)
 {
-    constexpr uint32_t kLeast = F16 ? 113u : 7u;
-    const uint32_t b = byte < kLeast ? kLeast : byte > 134u ? 127u : byte;
+    const uint32_t b = F16 && byte < 113u ? 113u : byte > 134u ? 127u : byte;
     const float log2v = byte > 134u ? __uint_as_float(0x7FC00000u) : (float)((int)b - 127);
     return __uint_as_float((254u - kDown - b - ((int)b < 127 + kTiny ? kLift : 0)) << 23 | __float_as_uint(log2v) >> 16);
 }

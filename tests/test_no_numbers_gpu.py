@@ -62,3 +62,58 @@ def test_scales_of_no_number(sd, dim, dtype, rows, scale):
         cache.v_scales[at(ctx + n)] = cache.k_scales[at(ctx + n)] = scale
     out, again = _attend(sd, q, cache, b, None, 0.125, 0, max_new, True)
     assert torch.equal(out, good) and torch.equal(again, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_every_scale(sd, dim, dtype):
+    """One key a lane.  The output is its value, lse its score: codes times 2^(scale - 127), in fp16 2^-14 at least."""
+    import torch
+    scales, ps = list(range(135)), 16
+    lanes = len(scales)
+    codes = [c for c in range(256) if c & 127 != 127]
+    codes = [codes[i * 3 % len(codes)] for i in range(dim)]
+    size = 2.0 ** np.maximum(np.array(scales, np.float64) - 127, -14.0 if dtype == "f16" else -127.0)
+    v, k = np.zeros((lanes, ps, 1, dim), np.uint8), np.zeros((lanes, ps, 1, dim), np.uint8)
+    v[:, 0, 0], k[:, 0, 0, 0] = codes, 0x38
+    ks, vs = np.full((lanes, 1, ps), 127, np.uint8), np.full((lanes, 1, ps), 127, np.uint8)
+    t = lambda x: torch.tensor(x, device="cuda")  # noqa: E731
+    q = torch.zeros((lanes, 2, dim), dtype=_dt(dtype), device="cuda")
+    q[:, 0, 0], q[:, 1, 0] = 1.0, -0.5
+    b = _batch(sd, [[i] for i in range(lanes)], list(range(lanes + 1)), [1] * lanes, ps)
+    tiny = torch.finfo(_dt(dtype)).tiny
+    # the values' scales: exact, but for what the tensor cores and the output's type have below the smallest normal number
+    vs[:, 0, 0] = scales
+    out, lse = _attend(sd, q, sd.PagedCache8(t(k), t(ks), t(v), t(vs), dtype=_dt(dtype)), b, None, 1.0, 0, 1, True)
+    want = torch.tensor(ref.code_values()[codes] * size[:, None])
+    for h in range(2):
+        off = (out[:, h].cpu().double() - want).abs()
+        assert off[want.abs() >= tiny].max() == 0 and off.max() < tiny
+    # exponents of up to 2^7 in size and of 7 less, rounded: 2^-18 each
+    assert (lse - torch.tensor([1.0, -0.5], device="cuda")).abs().max() <= 2.0 ** -17
+    # the keys'
+    ks[:, 0, 0], vs[:, 0, 0] = scales, 127
+    out, lse = _attend(sd, q, sd.PagedCache8(t(k), t(ks), t(v), t(vs), dtype=_dt(dtype)), b, None, 1.0, 0, 1, True)
+    for h, x in enumerate((1.0, -0.5)):
+        assert (lse[:, h].cpu().double() - torch.tensor(size * x)).abs().max() <= 2.0 ** -20 * 128
+        at = [i for i, s in enumerate(size) if s >= 2.0 ** -14]
+        assert ((lse[at, h].cpu().double() - torch.tensor(size[at] * x)).abs() <= 2.0 ** -20 * torch.tensor(size[at]).clamp(min=8.0)).all()
+
+
+def test_smallest_scales_of_both(sd):
+    """Keys and values of bf16 caches with scales below those that the store writes: a key times 2^100 in q tells 2^-127 from
+    2^-120."""
+    import torch
+    ps = 16
+    for dim in (64, 128, 256):
+        for byte in range(8):
+            k = torch.zeros((1, ps, 1, dim), dtype=torch.uint8, device="cuda")
+            k[0, :2, 0, 0] = 0x38
+            ks = torch.full((1, 1, ps), 127, dtype=torch.uint8, device="cuda")
+            ks[0, 0, 0], ks[0, 0, 1] = byte, 0
+            cache = sd.PagedCache8(k, ks, torch.zeros_like(k), ks.clone(), dtype=torch.bfloat16)
+            q = torch.zeros((1, 1, dim), dtype=torch.bfloat16, device="cuda")
+            q[0, 0, 0] = 2.0 ** 125
+            _, lse = _attend(sd, q, cache, _batch(sd, [[0]], [0, 1], [2], ps), None, 1.0, 0, 1, True)
+            want = np.logaddexp(2.0 ** (byte - 2), 2.0 ** -2)
+            assert abs(float(lse) - want) <= 2.0 ** -16 * max(1.0, want), (dim, byte, float(lse), want)
