@@ -404,7 +404,10 @@ int64_t spec_paged_attention_workspace(void);
  * A vector (the head_dim elements of a token's key, or value, of one head) is
  * head_dim e4m3 codes (sign, 4 bits of exponent, 3 of fraction; largest 448) and
  * one byte of scale: element i is code[i] * 2^(scale - 127) (fp16: 2^-14 for
- * scales below 113; above 134: no number).  spec_paged_store8
+ * scales below 113; above 134: no number).  The codes 127 and 255, e4m3's NaN, go
+ * under a scale above 134, as the store has them: under another one a bf16 cache
+ * may read them as 480 * 2^(scale - 127) (telling them apart costs attention up
+ * to 8 %).  spec_paged_store8
  * quantises as it stores, spec_paged_attention8 (and spec_tree_attention8) reads.
  * Strides as in spec_paged_cache but multiples of 16; scales are contiguous
  * [pages][heads][page_size]; all four addresses 16-byte aligned. */

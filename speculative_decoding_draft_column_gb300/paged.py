@@ -157,7 +157,8 @@ class PagedCache8:
     """Keys and values of one layer in 8 bits: codes in two CUDA tensors [pages, page_size, heads,
     head_dim] (torch.float8_e4m3fn, or uint8 with the same bits), any strides over the first three
     dimensions, and their scales in two contiguous uint8 tensors [pages, heads, page_size].  ``dtype``
-    (torch.bfloat16 or torch.float16) is what is stored from and attended with."""
+    (torch.bfloat16 or torch.float16) is what is stored from and attended with.  Codes that are NaN
+    need a scale above 134 (``spec_paged_store8`` writes 255)."""
 
     def __init__(self, k, k_scales, v, v_scales, *, dtype=None):
         import torch
