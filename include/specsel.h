@@ -427,7 +427,8 @@ typedef struct {
  * 448 * 2^e, from -120 (fp16: -14) to 7; element x becomes the code nearest to
  * x / 2^e (ties to even).  So a value is off by at most 2^-4 of itself or 2^-10 * 2^e;
  * magnitudes above 57,344 become 57,344, and a vector that holds an infinity or a
- * NaN reads as NaN throughout (scale 255, codes 127).  A cache of at most 524,280 heads. */
+ * NaN reads as NaN throughout (scale 255, codes 127).  A cache of at most 1,048,560 heads
+ * (of more where head_dim is 128 or less). */
 spec_status spec_paged_store8(const void *k, const void *v, int64_t tokens, int64_t k_token_stride,
                               int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
                               const int64_t *slots, const spec_paged_cache8 *cache);

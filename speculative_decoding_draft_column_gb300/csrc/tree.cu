@@ -148,9 +148,6 @@ spec_status spec_paged_store8(const void *k, const void *v, int64_t tokens, int6
     if (st != SPEC_OK) return st;
     st = check_new(k, v, tokens, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots);
     if (st != SPEC_OK || tokens == 0) return st;
-    int64_t sms = 0;
-    st = sm_count(&sms);
-    if (st != SPEC_OK) return st;
     tree::StoreArgs a;
     memset(&a, 0, sizeof a);
     a.k = static_cast<const uint16_t *>(k); a.v = static_cast<const uint16_t *>(v);
@@ -167,6 +164,9 @@ spec_status spec_paged_store8(const void *k, const void *v, int64_t tokens, int6
     // heads past a CTA's: more CTAs a token, as far as a grid's second dimension goes
     const int64_t parts = ((int64_t)cache->heads + a.heads - 1) / a.heads;
     if (parts > 65535) return fail(SPEC_ERR_ARG, "cache: heads = %d, the store takes %d of this size", cache->heads, 65535 * a.heads);
+    int64_t sms = 0;
+    st = sm_count(&sms);
+    if (st != SPEC_OK) return st;
     int64_t grid = (tokens + a.per - 1) / a.per;
     const int64_t room = (tree::kStoreCtas * sms + parts - 1) / parts;
     if (grid > room) grid = room;
