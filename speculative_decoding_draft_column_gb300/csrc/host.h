@@ -5,6 +5,8 @@
 
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "specsel.h"
 
 namespace host {
@@ -33,7 +35,9 @@ cudaError_t take_attention8_timeouts(unsigned int *flags);
 
 // The current device's scratch for a call on the calling thread's stream: a ticket a lane, zero between calls,
 // and `entries` words of lists.  False where there is none to be had (it would have to grow inside
-// a stream capture, or memory is out).
-bool lane_scratch(int64_t lanes, int64_t entries, unsigned int **tickets, unsigned long long **lists);
+// a stream capture, or memory is out).  It stays as long as `hold` is locked, so the call is launched before that
+// is let go of: spec_release, on another thread, waits for the lock and then for what was launched.
+bool lane_scratch(int64_t lanes, int64_t entries, unsigned int **tickets, unsigned long long **lists,
+                  std::unique_lock<std::mutex> *hold);
 
 }  // namespace host

@@ -1236,10 +1236,10 @@ spec_status fail(spec_status st, const char *fmt, ...)
     return st;
 }
 
-
-bool lane_scratch(int64_t lanes, int64_t entries, unsigned int **tickets, unsigned long long **lists)
+bool lane_scratch(int64_t lanes, int64_t entries, unsigned int **tickets, unsigned long long **lists,
+                  std::unique_lock<std::mutex> *hold)
 {
-    std::lock_guard<std::mutex> lock(g_mu);
+    std::unique_lock<std::mutex> lock(g_mu);
     DeviceState *d = nullptr;
     spec_status st = device_state(&d);
     if (st == SPEC_OK) st = ensure_scratch(*d, {0, lanes, entries}, t_stream);
@@ -1248,6 +1248,7 @@ bool lane_scratch(int64_t lanes, int64_t entries, unsigned int **tickets, unsign
     const ScratchPtrs sp = scratch_ptrs(*d);
     *tickets = sp.lane_ticket;
     *lists = sp.partials;
+    *hold = std::move(lock);
     return true;
 }
 

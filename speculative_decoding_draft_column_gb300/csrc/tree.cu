@@ -130,7 +130,8 @@ spec_status verify(const uint16_t *logits, const int32_t *drafts, const int32_t 
     unsigned ctas = 1;
     while (ctas < tree::kMostCtas && lanes * ctas * 2 <= 8 * sms && vectors >= 2 * ctas * tree::kThreads) ctas *= 2;
     // All nodes' columns at once, where they fit the GPU together; else the paths' only.
-    if (tokens * ctas <= 2 * sms && host::lane_scratch(lanes, tokens * a.k, &a.tickets, &a.lists) && tokens > 0)
+    std::unique_lock<std::mutex> hold;
+    if (tokens * ctas <= 2 * sms && tokens > 0 && host::lane_scratch(lanes, tokens * a.k, &a.tickets, &a.lists, &hold))
         return launch(tree::verify_kernel<true>, dim3((unsigned)(tokens * ctas)), tree::kThreads, sizeof(tree::VerifySmem), ctas, a, (uint32_t)ctas);
     return launch(tree::verify_kernel<false>, dim3((unsigned)(lanes * ctas)), tree::kThreads, sizeof(tree::VerifySmem), ctas, a, (uint32_t)ctas);
 }
