@@ -464,7 +464,7 @@ spec_status spec_paged_attention8(const void *q, int64_t tokens, int32_t heads_q
  *   masks[t][w], bit b: node 32 w + b is node i or above it (uint32 [tokens][mask_words]);
  *   positions[t] = context + the number of nodes above it, context = seq_len - new (for
  *   rotary positions; spec_paged_plan's count the nodes in a row).
- * Rows past the step's total get 0.  1 <= mask_words <= 8; nodes from 32 * mask_words on
+ * Rows past the step's total get 0 (without lanes nothing is written).  1 <= mask_words <= 8; nodes from 32 * mask_words on
  * have no bit.  parents int32 [tokens]; masks and positions must not overlap the inputs, or
  * each other.  Reads the batch's cu_new and seq_lens.  One launch. */
 spec_status spec_tree_plan(const int32_t *parents, int64_t tokens, const spec_paged_batch *batch, uint32_t *masks,
@@ -473,8 +473,8 @@ spec_status spec_tree_plan(const int32_t *parents, int64_t tokens, const spec_pa
 /* spec_paged_attention for trees: node i of a lane attends the lane's cached
  * tokens (positions below seq_len - new) and those new tokens j <= i whose bit of
  * masks[t] is set -- any bits: those of spec_tree_plan, or a caller's own.  With a window
- * the cached tokens are cut to positions above p - window, p = context + (set bits up to i) - 1;
- * a tree's window is 0 or at least SPEC_TREE_MAX_NODES.  A row that sees no key
+ * the cached tokens are cut to positions above p - window, p = context + (set bits up to i) - 1, or context
+ * where there are none; a tree's window is 0 or at least SPEC_TREE_MAX_NODES.  A row that sees no key
  * gets out = 0 and lse = -inf.  All else, workspace included, as there; values of all the
  * step's new tokens must be finite, seen or not. */
 spec_status spec_tree_attention(const void *q, int64_t tokens, int32_t heads_q, int64_t q_token_stride,
