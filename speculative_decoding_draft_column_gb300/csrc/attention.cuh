@@ -64,7 +64,8 @@
 // stages are few beside 16-bit tiles of 32 KB, and a tile passes from copy to converters to products in some 3,000
 // cycles.  1.61 us a pair of K and V tiles of one row tile (0.87 over 16 bits from L2, 1.45 from DRAM), 2.49 of two
 // (1.92): 16 tokens at 262,128 keys 181 us (161 over 16 bits), 8 trees of 64 nodes 108 (91).  So the 8-bit
-// cache takes half the memory, and is faster where rows are few (attention_few.cuh: 283 us against 320).
+// cache takes half the memory, and is faster where rows are few, heads of 128 and contexts long (attention_few.cuh: 275 us against 320).
+// 64 single tokens at 8,000 keys, heads of 64 and 256, which have no such form: 271 (256 over 16 bits) and 720 (612).
 // Converters tried: four warps, 2.54 us a pair; eight in lockstep 1.70; copies by the
 // converting warps themselves, without TMA, 2.03; scales by cp.async 1.62 (pages of 16 tokens 1.84 instead of 2.10).
 #pragma once
@@ -108,7 +109,9 @@ struct Shape {
     static constexpr int kRaw = !kQ8 ? 0 : kRawMost < 4 ? kRawMost : 4;
     static constexpr int kSoftmaxWarps = kFew ? 8 : NS * 8;
     // converting warps, in teams of four that take half tiles in turn (64 registers a thread with three teams: two row tiles
-    // have the softmax of twice the rows to compute with them, 2.60 against 2.49 us a tile)
+    // have the softmax of twice the rows to compute with them, 2.60 against 2.49 us a tile; heads of 64 over long contexts
+    // gain, 16 tokens at 262,128 keys 134.6 against 142.4 us, 64 tokens at 8,000 271 against 280, short ones lose, 16 lanes
+    // of 16 at 3,000 keys 43.5 against 40.9)
     static constexpr int kTeams = QT == 1 && D <= 128 && !kFew ? 3 : 2;
     static constexpr int kTileWarps = kFew ? 4 : 8;            // that convert a tile (kFew: a team K tiles, one V tiles)
     static constexpr int kConverters = kQ8 ? kTeams * 4 : 0;

@@ -6,11 +6,13 @@
 // 16-bit cache (64 tokens of 4 rows a head at 500-16,000 keys 369 us against 320).  Here the products are
 // transposed, S^T = K Q^T and O^T += V^T P^T: a softmax thread has one key, so that the key's scale is one
 // factor of all its scores, and its value's scale one of all its weights.  Codes then go to fp16 as they
-// are, one instruction a pair, and a thread's 16 columns (rows of q) stay in registers for both passes over
-// them.  273 us, 3.9 TB/s.  What bounds it: chains, none of them full.  A pair of tiles takes 1.13 us from L2 and
-// 1.25 from DRAM; the loader's copies are issued in 0.75 (eight of 100 ns each, for pages of 64), the issuing warp
-// works for 0.75, a stream's softmax for 1.5 every second pair.  With 32 rows (two columns' groups) or 64 a
-// thread's sums went to local memory: 440 and 496 us.  More converting warps take its registers: 16 373 us, three
+// are, one instruction a pair, and a thread's 16 columns (rows of q) are read from TMEM once for both passes over
+// them.  275 us, 3.9 TB/s.  What bounds it: chains, none of them full.  A pair of tiles takes 1.27 us; the loader's
+// copies are issued in 0.6 (eight, for pages of 64), the issuing warp works for 0.75, a converting team for 0.65, a stream's
+// softmax for 1.5 every second pair.  640 threads leave 96 registers each, and 36 to 48 bytes of a thread's are kept in
+// local memory (of its counters and places; with more of them there the same loop took 279 to 293 us).  With 32 rows (two
+// columns' groups) or 64 a thread's sums went there: 440 and 496 us.  Scores two tiles ahead of the weights' products
+// instead of one: 2 % slower.  More converting warps take its registers: 16 373 us, three
 // teams of four 341.  Codes brought to L2 two tiles ahead cost the loader what they save.
 //
 // All products are fp16's.  A bf16 row of q is taken times a power of two that brings its largest element to
